@@ -17,11 +17,14 @@ OK, EINVAL, EUNSUPPORTED, ENOSPACE, EHIP, ENOTRESIDENT = range(6)
 F32, BF16 = 0, 1
 FMT_ABSENT, FMT_VQ2, FMT_MXFP4 = 0, 1, 2
 MAT_GATE, MAT_UP, MAT_DOWN = 0, 1, 2
+ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = range(4)
 
 EXPORTS = ("moe_vq_expert_bytes", "moe_vq_slot_layout", "moe_vq_workspace_bytes", "moe_vq_route_topk",
            "moe_vq_fc1_silu", "moe_vq_fc2_combine", "moe_vq_forward", "moe_vq_forward_static", "moe_vq_shared_expert", "moe_vq_prefill_gemm", "moe_vq_decode_expert",
            "moe_vq_check", "moe_vq_step_info", "moe_vq_tier_init", "moe_vq_tier_plan", "moe_vq_tier_resolve", "moe_vq_cpu_experts",
-           "moe_vq_time_next_kernel", "moe_vq_read_probe", "moe_vq_last_hip_error", "moe_vq_strerror")
+           "moe_vq_time_next_kernel", "moe_vq_read_probe",
+           "moe_vq_sort_bytes", "moe_vq_sort_pairs", "moe_vq_gather_rows", "moe_vq_combine_rows", "moe_vq_combine_rows_backward",
+           "moe_vq_linear_bytes", "moe_vq_linear_forward", "moe_vq_linear_backward", "moe_vq_last_hip_error", "moe_vq_strerror")
 
 
 class MoeVqError(RuntimeError):
@@ -50,6 +53,13 @@ class Tier(ctypes.Structure):
                 ("step", ctypes.c_uint64), ("readback", ctypes.c_void_p)]
 
 
+class LinearDesc(ctypes.Structure):
+    """struct moe_vq_linear"""
+    _fields_ = [("n_in", ctypes.c_int32), ("n_out", ctypes.c_int32), ("n_groups", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("dtype", ctypes.c_int32), ("swiglu_limit", ctypes.c_float),
+                ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
+
+
 def _load():
     # The library must run on the same HIP runtime as PyTorch, whose streams and
     # device memory it is handed.  The torch wheel bundles libamdhip64.so.7 under the
@@ -64,6 +74,7 @@ def _load():
     lib = ctypes.CDLL(LIB_PATH, mode=ctypes.RTLD_GLOBAL)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     LP = ctypes.POINTER(Layer)
+    DP = ctypes.POINTER(LinearDesc)
     sig = {
         "moe_vq_expert_bytes": (sz, [i32, i32, i32]),
         "moe_vq_slot_layout": (i32, [i32, i32, i32, ctypes.POINTER(ctypes.c_uint64)]),
@@ -87,6 +98,14 @@ def _load():
                                      vp, i32]),
         "moe_vq_time_next_kernel": (i32, [vp, vp]),
         "moe_vq_read_probe": (i32, [vp, sz, vp, vp]),
+        "moe_vq_sort_bytes": (sz, [i32, i32, i32]),
+        "moe_vq_sort_pairs": (i32, [vp, i32, i32, i32, vp, vp, vp, vp, sz, vp]),
+        "moe_vq_gather_rows": (i32, [vp, i32, i32, i32, i32, vp, vp, vp]),
+        "moe_vq_combine_rows": (i32, [vp, i32, i32, i32, i32, vp, vp, vp, vp, i32, vp]),
+        "moe_vq_combine_rows_backward": (i32, [vp, i32, i32, i32, i32, vp, vp, vp, i32, vp, vp, vp]),
+        "moe_vq_linear_bytes": (sz, [DP, i32, i32]),
+        "moe_vq_linear_forward": (i32, [DP, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
+        "moe_vq_linear_backward": (i32, [DP, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
         "moe_vq_last_hip_error": (ctypes.c_char_p, []),
         "moe_vq_strerror": (ctypes.c_char_p, [i32]),
     }
@@ -264,6 +283,53 @@ def cpu_experts(layer: Layer, host_pool: int, host_pool_bytes: int, host_slots, 
     """The CPU miss path (host pointers only); host_slots is a ctypes Slot array."""
     _ok(_lib.moe_vq_cpu_experts(ctypes.byref(layer), host_pool, host_pool_bytes, host_slots, codebook, x, x_dtype,
                                 n_tokens, topk_ids, topk_w, compute, y, n_threads), "cpu_experts")
+
+
+def sort_bytes(n_tokens: int, top_k: int, n_experts: int) -> int:
+    return int(_lib.moe_vq_sort_bytes(n_tokens, top_k, n_experts))
+
+
+def sort_pairs(topk_ids: int, n_tokens: int, top_k: int, n_experts: int, expert_start: int, pair_row: int,
+               row_pair: int, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    _ok(_lib.moe_vq_sort_pairs(topk_ids, n_tokens, top_k, n_experts, expert_start, pair_row, row_pair, ws, ws_bytes,
+                               stream), "sort_pairs")
+
+
+def gather_rows(x: int, dtype: int, n_tokens: int, top_k: int, n_cols: int, pair_row: int, xs: int,
+                stream: int = 0) -> None:
+    _ok(_lib.moe_vq_gather_rows(x, dtype, n_tokens, top_k, n_cols, pair_row, xs, stream), "gather_rows")
+
+
+def combine_rows(rows: int, dtype: int, n_tokens: int, top_k: int, n_cols: int, pair_row: int, w: int,
+                 residual: int, y: int, y_dtype: int, stream: int = 0) -> None:
+    """w and residual may be 0 (NULL)."""
+    _ok(_lib.moe_vq_combine_rows(rows, dtype, n_tokens, top_k, n_cols, pair_row, w, residual, y, y_dtype, stream),
+        "combine_rows")
+
+
+def combine_rows_backward(dy: int, dy_dtype: int, n_tokens: int, top_k: int, n_cols: int, pair_row: int, w: int,
+                          rows: int, dtype: int, drows: int, dw: int, stream: int = 0) -> None:
+    """w, rows, drows and dw may be 0 (NULL)."""
+    _ok(_lib.moe_vq_combine_rows_backward(dy, dy_dtype, n_tokens, top_k, n_cols, pair_row, w, rows, dtype, drows, dw,
+                                          stream), "combine_rows_backward")
+
+
+def linear_bytes(lin: LinearDesc, n_rows: int, backward: bool = False) -> int:
+    return int(_lib.moe_vq_linear_bytes(ctypes.byref(lin), n_rows, int(backward)))
+
+
+def linear_forward(lin: LinearDesc, x: int, n_rows: int, group_start: int, residual: int, y: int, y_dtype: int,
+                   z: int, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    """group_start, residual and z may be 0 (NULL)."""
+    _ok(_lib.moe_vq_linear_forward(ctypes.byref(lin), x, n_rows, group_start, residual, y, y_dtype, z, ws, ws_bytes,
+                                   stream), "linear_forward")
+
+
+def linear_backward(lin: LinearDesc, x: int, n_rows: int, group_start: int, z: int, dy: int, dy_dtype: int, dx: int,
+                    dw: int, dbias: int, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    """group_start, z, dx, dw and dbias may be 0 (NULL)."""
+    _ok(_lib.moe_vq_linear_backward(ctypes.byref(lin), x, n_rows, group_start, z, dy, dy_dtype, dx, dw, dbias, ws,
+                                    ws_bytes, stream), "linear_backward")
 
 
 def raw():

@@ -5,6 +5,7 @@
 
 #include <mutex>
 
+#include "dense.h"
 #include "moe_vq_internal.h"
 #include "moe_vq_launch.h"
 
@@ -13,13 +14,6 @@ using namespace mvq;
 namespace {
 
 thread_local hipError_t g_last_hip_error = hipSuccess;
-
-// Record a failed HIP call and map it to MOE_VQ_EHIP.
-int hip_status(hipError_t e) {
-  if (e == hipSuccess) return MOE_VQ_OK;
-  g_last_hip_error = e;
-  return MOE_VQ_EHIP;
-}
 
 bool dims_ok(int H, int I, int E, int k) {
   if (H < 128 || H > MAX_DIM || H % 128) return false;
@@ -256,6 +250,12 @@ hipError_t static_scratch(void** out) {
 }  // namespace
 
 namespace mvq {
+int hip_status(hipError_t e) {
+  if (e == hipSuccess) return MOE_VQ_OK;
+  g_last_hip_error = e;
+  return MOE_VQ_EHIP;
+}
+
 KernelTiming& kernel_timing() {
   thread_local KernelTiming t;
   return t;

@@ -366,6 +366,111 @@ int moe_vq_cpu_experts(const moe_vq_layer *layer, const uint8_t *host_pool, uint
                        int n_tokens, const int32_t *topk_ids, const float *topk_w, const uint8_t *compute,
                        float *y, int n_threads);
 
+/* ---- The step with unquantised experts, and its gradients.  The coded experts above are
+ * made from, and judged against, experts in bf16 or fp32; the shared expert and the dense
+ * layers of such models are kept that way, and a router or the experts are tuned through
+ * them.  These calls run that layer from the same routing (topk_ids, topk_w):
+ *   sort_pairs      the routed pairs p = t*k + i sorted by expert
+ *   gather_rows     the tokens' rows in that order
+ *   linear_forward  the experts' products, with bias, activation and residual
+ *   combine_rows    the experts' rows added up per token with the routing weights
+ * They are no part of the sources' pages.  Conventions as above; every sum is fp32 (or
+ * fp32 products on the matrix cores) in a fixed order, without atomics.  None of them
+ * leaves anything in the workspace for a later call, so one workspace may serve several
+ * calls that are stream-ordered; two calls (or two replayed graphs) that may overlap need
+ * two.  Every call may be captured into a graph. */
+
+/* [host] Workspace bytes of moe_vq_sort_pairs, 0 if an argument is invalid. */
+size_t moe_vq_sort_bytes(int n_tokens, int top_k, int n_experts);
+
+/* Sort the pairs p = t*k + i of n_tokens tokens by expert, stably: expert_start [E + 1] gets
+ * the first row of each expert (expert_start[E]: the rows in all), pair_row [n_tokens*k] the
+ * row of each pair and row_pair [n_tokens*k] the pair of each row.  A pair whose id is
+ * outside 0..E-1 is dropped: pair_row -1; the rows behind the last expert's get row_pair -1.
+ * The same expert may occur more than once in a token.  1 <= top_k <= 32, 1 <= n_experts <=
+ * 1024 (top_k may exceed n_experts), 0 <= n_tokens <= 65536.  With n_tokens == 0 expert_start
+ * is set to zeros.  Errors: MOE_VQ_EINVAL, MOE_VQ_ENOSPACE, MOE_VQ_EHIP. */
+int moe_vq_sort_pairs(const int32_t *topk_ids, int n_tokens, int top_k, int n_experts,
+                      int32_t *expert_start, int32_t *pair_row, int32_t *row_pair,
+                      void *ws, size_t ws_bytes, void *stream);
+
+/* xs[pair_row[t*k + i]] = x[t]: the token's row copied to each of its pairs' rows.  x
+ * [n_tokens][n_cols], xs [n_tokens*k][n_cols], both in dtype and 16-byte aligned, n_cols
+ * 1..65536.  A pair_row outside 0..n_tokens*k-1 is a dropped pair; rows of xs that no pair
+ * names are left as they were.  The gradient is moe_vq_combine_rows without weights:
+ * dx[t] = sum_i dxs[pair_row[t*k + i]]. */
+int moe_vq_gather_rows(const void *x, int dtype, int n_tokens, int top_k, int n_cols,
+                       const int32_t *pair_row, void *xs, void *stream);
+
+/* y[t] = residual[t] + sum_i w[t*k + i] * rows[pair_row[t*k + i]], summed over i in order in
+ * fp32 and rounded once.  rows [n_tokens*k][n_cols] in dtype; w fp32 [n_tokens*k] or NULL (all
+ * 1); residual and y [n_tokens][n_cols] in y_dtype (residual may be NULL, and may be y
+ * itself).  rows, residual, y 16-byte aligned.  A dropped pair adds nothing, and its weight and
+ * whatever lies in unnamed rows are not looked at; a token without pairs gets its residual,
+ * or zeros. */
+int moe_vq_combine_rows(const void *rows, int dtype, int n_tokens, int top_k, int n_cols,
+                        const int32_t *pair_row, const float *w, const void *residual, void *y, int y_dtype,
+                        void *stream);
+
+/* Gradients of moe_vq_combine_rows: drows[pair_row[p]] = w[p] * dy[t] (dtype; rows that no
+ * pair names are left as they were) and dw[p] = <dy[t], rows[pair_row[p]]> (fp32, 0 for a
+ * dropped pair).  drows or dw may be NULL (rows is needed for dw only; w NULL: all 1).  The
+ * residual's gradient is dy.  dy [n_tokens][n_cols] in dy_dtype.  drows must not overlap rows. */
+int moe_vq_combine_rows_backward(const void *dy, int dy_dtype, int n_tokens, int top_k, int n_cols,
+                                 const int32_t *pair_row, const float *w, const void *rows, int dtype,
+                                 void *drows, float *dw, void *stream);
+
+enum moe_vq_act {
+  MOE_VQ_ACT_NONE = 0,
+  MOE_VQ_ACT_SILU = 1,   /* z / (1 + exp(-z))                                             */
+  MOE_VQ_ACT_GELU = 2,   /* z * Phi(z), Phi by the error function                          */
+  MOE_VQ_ACT_SWIGLU = 3  /* silu(min(g, L)) * clamp(u, -L, L), L = swiglu_limit (0: none) */
+};
+
+/* [host] A dense product; its pointers are device buffers.  w holds n_groups matrices
+ * [R][n_in] in dtype, R = n_out, or 2 n_out for MOE_VQ_ACT_SWIGLU: n_out gate rows g, then
+ * n_out up rows u.  bias: fp32 [n_groups][R] or NULL. */
+typedef struct moe_vq_linear {
+  int32_t n_in;        /* 1..16384                                              */
+  int32_t n_out;       /* 1..16384                                              */
+  int32_t n_groups;    /* 1..1024                                               */
+  int32_t act;         /* enum moe_vq_act                                       */
+  int32_t dtype;       /* enum moe_vq_dtype of x, w, z, dx and dw               */
+  float swiglu_limit;  /* L; finite, >= 0; read for MOE_VQ_ACT_SWIGLU only      */
+  const void *w;
+  const float *bias;
+} moe_vq_linear;
+
+/* [host] Workspace bytes of moe_vq_linear_forward (backward = 0) or moe_vq_linear_backward
+ * (backward = 1) for up to n_rows rows, 0 if an argument is invalid.  Pointers are not
+ * inspected.  A call with fewer rows may use it too. */
+size_t moe_vq_linear_bytes(const moe_vq_linear *lin, int n_rows, int backward);
+
+/* y = act(x W^T + b) + residual.  x [n_rows][n_in]; y and residual [n_rows][n_out] in y_dtype
+ * (residual may be NULL, and may be y itself).  group_start [n_groups + 1] (device, ascending):
+ * rows group_start[g] .. group_start[g+1]-1 use matrix g (moe_vq_sort_pairs's expert_start);
+ * rows in no group are neither read nor written.  It may be NULL with n_groups = 1: every row.
+ * z [n_rows][R] in dtype, or NULL: the values before the activation, kept for the backward
+ * call.  Products of bf16 values are exact and summed in fp32; y and z are each rounded once.
+ * x, w, residual, y, z 16-byte aligned; 0 <= n_rows <= 2097152 (65536 tokens, top-32); no
+ * buffer may overlap y or z except residual as said.  Errors: MOE_VQ_EINVAL, MOE_VQ_ENOSPACE,
+ * MOE_VQ_EHIP. */
+int moe_vq_linear_forward(const moe_vq_linear *lin, const void *x, int n_rows, const int32_t *group_start,
+                          const void *residual, void *y, int y_dtype, void *z, void *ws, size_t ws_bytes,
+                          void *stream);
+
+/* Gradients of moe_vq_linear_forward from dy [n_rows][n_out] in dy_dtype and the kept z (not
+ * read for MOE_VQ_ACT_NONE; may be NULL then): with dz = dy * act'(z),
+ *   dx [n_rows][n_in] = dz W      dw [n_groups][R][n_in] = dz_g^T x_g      dbias [n_groups][R] = sum of dz_g's rows
+ * dx and dw in dtype, dbias fp32; each may be NULL.  A value that the SwiGLU clamp cut has
+ * no gradient.  dz is rounded to dtype once for the products (dbias adds it unrounded); every
+ * output is summed in fp32 and rounded once.  Groups without rows get zeros in dw and dbias (with
+ * n_rows = 0 all of them); rows in no group are neither read nor written.  The residual's
+ * gradient is dy.  Alignment and errors as moe_vq_linear_forward. */
+int moe_vq_linear_backward(const moe_vq_linear *lin, const void *x, int n_rows, const int32_t *group_start,
+                           const void *z, const void *dy, int dy_dtype, void *dx, void *dw, float *dbias,
+                           void *ws, size_t ws_bytes, void *stream);
+
 /* [host] Text of the last HIP runtime error seen by a call of this library on the
  * calling thread (the reason behind MOE_VQ_EHIP), or "" if none. */
 const char *moe_vq_last_hip_error(void);

@@ -1,0 +1,106 @@
+"""The row operators and the dense product without a GPU: sizes, and bad arguments refused
+before any HIP call (pointer values are never dereferenced on these paths)."""
+import ctypes
+
+import pytest
+
+mvq = pytest.importorskip("bit_vector_quantised_amd")
+from bit_vector_quantised_amd import _lib  # noqa: E402
+
+A = 0x100000  # an aligned address
+RAW = _lib.raw()
+
+
+def lin(n_in=256, n_out=128, groups=1, act=_lib.ACT_NONE, dtype=_lib.BF16, lim=0.0, w=A, bias=None):
+    return _lib.LinearDesc(n_in, n_out, groups, act, dtype, lim, w, bias)
+
+
+def test_sort_bytes():
+    assert _lib.sort_bytes(1, 8, 256) > 0 and _lib.sort_bytes(0, 1, 1) > 0
+    for bad in ((-1, 8, 256), (65537, 8, 256), (1, 0, 256), (1, 33, 256), (1, 8, 0), (1, 8, 1025)):
+        assert _lib.sort_bytes(*bad) == 0, bad
+    # a workspace made for more tokens serves any smaller call
+    for k, E in ((1, 1), (8, 256), (32, 1024)):
+        need = [_lib.sort_bytes(t, k, E) for t in (1, 100, 2048, 4096, 4097, 16384, 16385, 40000, 65536)]
+        assert need == sorted(need)
+
+
+def test_sort_refusals():
+    ok = dict(ids=A, T=4, k=2, E=8, start=A, pair=A, row=A, ws=A, n=1 << 20)
+
+    def call(**kw):
+        a = {**ok, **kw}
+        return RAW.moe_vq_sort_pairs(a["ids"], a["T"], a["k"], a["E"], a["start"], a["pair"], a["row"], a["ws"], a["n"], None)
+
+    for kw in (dict(ids=None), dict(start=None), dict(pair=None), dict(row=None), dict(ws=None), dict(ws=A + 16),
+               dict(T=-1), dict(T=65537), dict(k=0), dict(k=33), dict(E=0), dict(E=1025), dict(ids=A + 2),
+               dict(start=A + 1), dict(pair=A + 2), dict(row=A + 2)):
+        assert call(**kw) == _lib.EINVAL, kw
+    assert call(n=31) == _lib.ENOSPACE
+
+
+def test_rows_refusals():
+    def gather(x=A, dt=_lib.BF16, T=4, k=2, C=64, pair=A, xs=A):
+        return RAW.moe_vq_gather_rows(x, dt, T, k, C, pair, xs, None)
+
+    def combine(rows=A, dt=_lib.BF16, T=4, k=2, C=64, pair=A, w=None, res=None, y=A, ydt=_lib.F32):
+        return RAW.moe_vq_combine_rows(rows, dt, T, k, C, pair, w, res, y, ydt, None)
+
+    def back(dy=A, ddt=_lib.F32, T=4, k=2, C=64, pair=A, w=None, rows=A, dt=_lib.BF16, drows=A, dw=A):
+        return RAW.moe_vq_combine_rows_backward(dy, ddt, T, k, C, pair, w, rows, dt, drows, dw, None)
+
+    dims = (dict(T=-1), dict(T=65537), dict(k=0), dict(k=33), dict(C=0), dict(C=65537), dict(dt=2), dict(dt=-1),
+            dict(pair=None), dict(pair=A + 2))
+    for kw in dims + (dict(x=None), dict(x=A + 8), dict(xs=None), dict(xs=A + 4)):
+        assert gather(**kw) == _lib.EINVAL, kw
+    for kw in dims + (dict(rows=None), dict(rows=A + 8), dict(y=None), dict(y=A + 8), dict(res=A + 8), dict(ydt=7),
+                      dict(w=A + 1)):
+        assert combine(**kw) == _lib.EINVAL, kw
+    for kw in dims + (dict(dy=None), dict(dy=A + 8), dict(rows=None), dict(rows=A + 4), dict(drows=A + 8), dict(ddt=7),
+                      dict(w=A + 2), dict(dw=A + 2)):
+        assert back(**kw) == _lib.EINVAL, kw
+    assert gather(T=0) == combine(T=0) == back(T=0) == _lib.OK
+    assert back(drows=None, dw=None) == _lib.OK
+
+
+BAD_LINEAR = (dict(n_in=0), dict(n_in=16385), dict(n_out=0), dict(n_out=16385), dict(groups=0), dict(groups=1025),
+              dict(act=-1), dict(act=4), dict(dtype=2), dict(act=_lib.ACT_SWIGLU, lim=-1.0),
+              dict(act=_lib.ACT_SWIGLU, lim=float("nan")), dict(act=_lib.ACT_SWIGLU, lim=float("inf")))
+
+
+def test_linear_bytes():
+    assert _lib.linear_bytes(lin(), 1) > 0 and _lib.linear_bytes(lin(), 0, True) > 0
+    for kw in BAD_LINEAR:
+        assert _lib.linear_bytes(lin(**kw), 16) == 0, kw
+    assert _lib.linear_bytes(lin(), -1) == 0 and _lib.linear_bytes(lin(), 65536 * 32 + 1) == 0
+    assert RAW.moe_vq_linear_bytes(None, 4, 0) == 0 and RAW.moe_vq_linear_bytes(ctypes.byref(lin()), 4, 2) == 0
+    # a workspace made for more rows serves any smaller call, whose contraction may be split further
+    for kw in (dict(), dict(n_in=8192, n_out=64), dict(n_in=333, n_out=4097, act=_lib.ACT_SWIGLU),
+               dict(groups=16, dtype=_lib.F32), dict(n_in=64, n_out=64)):
+        for backward in (False, True):
+            need = [_lib.linear_bytes(lin(**kw), m, backward) for m in (0, 1, 16, 17, 64, 65, 128, 500, 4096, 100000)]
+            assert need == sorted(need), (kw, backward, need)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_linear_refusals(backward):
+    big = 1 << 40
+
+    def call(desc=None, x=A, M=4, start=None, res=None, y=A, dt=_lib.F32, z=A, dx=A, dw=A, db=A, ws=A, n=big):
+        d = ctypes.byref(desc if desc is not None else lin(act=_lib.ACT_SILU))
+        if backward:
+            return RAW.moe_vq_linear_backward(d, x, M, start, z, y, dt, dx, dw, db, ws, n, None)
+        return RAW.moe_vq_linear_forward(d, x, M, start, res, y, dt, z, ws, n, None)
+
+    for kw in BAD_LINEAR + (dict(w=None), dict(w=A + 8), dict(bias=A + 2), dict(groups=4)):
+        assert call(lin(**kw)) == _lib.EINVAL, kw
+    bad = [dict(x=None), dict(x=A + 4), dict(M=-1), dict(M=65536 * 32 + 1), dict(y=None), dict(y=A + 8), dict(dt=5),
+           dict(z=A + 8), dict(ws=None), dict(ws=A + 128), dict(start=A + 2)]
+    bad += [dict(z=None), dict(dx=A + 8), dict(dw=A + 8), dict(db=A + 2)] if backward else [dict(res=A + 8)]
+    for kw in bad:
+        assert call(**kw) == _lib.EINVAL, kw
+    assert call(n=0) == _lib.ENOSPACE
+    if backward:
+        assert call(dx=None, dw=None, db=None) == _lib.OK
+    else:
+        assert call(M=0) == _lib.OK
