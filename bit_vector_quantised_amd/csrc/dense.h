@@ -49,7 +49,10 @@ struct LinearPlan {
   int dtype, size;           // element type of x, w, z, dx, dw and its bytes
   int Kp, Rp;                // pitches (elements) of packed x / w and of dz: multiples of 16 bytes
   bool pack_k;               // x and w need repacking (K is no multiple of 16 bytes)
-  int split_fwd, split_dx, split_dw, split_bias;
+  struct Cut {
+    int tile, splits;  // side of the square output tiles; parts of the contraction
+  } fwd, dx, dw;
+  int split_bias;            // parts of a group's rows in the sums of dbias
   size_t xp, wp, dz, bias_part, part, total;
 };
 LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward);

@@ -12,8 +12,8 @@
 // LDS for BM * BN * 128 / size products.  What differs is how an operand lies in memory:
 //   "along"   the contraction runs along its rows (x and W forward, dz for dx)
 //   "across"  the contraction runs across its rows (W for dx, dz and x for dw)
-// A contraction step takes 128 bytes of an along operand's row (64 bf16 or 32 fp32 values) and
-// as many rows of an across operand.  Both go from memory to LDS without passing through
+// A contraction step takes 128 bytes of an along operand's row (a cache line: 64 bf16 or 32 fp32
+// values, two matrix instructions deep) and as many rows of an across operand.  Both go from memory to LDS without passing through
 // registers (16 bytes per lane).  The buffer descriptor ends at the last valid row, so what
 // lies behind reads as zero: rows of the next group never enter a sum.
 //
@@ -87,14 +87,14 @@ __device__ __forceinline__ float gelu_grad(float z) {
 
 struct Bf16 {
   using T = uint16_t;
-  static constexpr int SIZE = 2, UNIT = 32;  // UNIT: bytes of 16 values
+  static constexpr int SIZE = 2, DTYPE = MOE_VQ_BF16, UNIT = 32, MMAS = 1;  // UNIT: bytes of 16 values; MMAS: instructions of mma
   static __device__ __forceinline__ void mma(const u32x4_t& a, const u32x4_t& b, f32x4_t& c) {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   }
 };
 struct F32 {
   using T = float;
-  static constexpr int SIZE = 4, UNIT = 64;
+  static constexpr int SIZE = 4, DTYPE = MOE_VQ_F32, UNIT = 64, MMAS = 4;
   static __device__ __forceinline__ void mma(const u32x4_t& a, const u32x4_t& b, f32x4_t& c) {
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
@@ -110,50 +110,71 @@ __device__ __forceinline__ void store_as(void* p, size_t i, int dtype, float v) 
   if (dtype == MOE_VQ_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16_rne(v);
   else static_cast<float*>(p)[i] = v;
 }
-// Up to four consecutive values from index i (n of them valid); as one access where wide.
-__device__ __forceinline__ void load4(const void* p, size_t i, int dtype, int n, bool wide, float* v) {
-  if (wide) {
-    if (dtype == MOE_VQ_BF16) {
+// N consecutive values (1, 4 or 8) from index i, the first `n` of them valid.  wide: all are, and i is a
+// multiple of N, so that they go as one or two accesses.
+template <int N>
+__device__ __forceinline__ void load_n(const void* p, size_t i, int dtype, int n, bool wide, float* v) {
+  if (N == 1) wide = false;
+  if (wide && dtype == MOE_VQ_BF16) {
+    uint32_t w[N == 1 ? 1 : N / 2];
+    if constexpr (N == 8) {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else if constexpr (N == 4) {
       const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      v[0] = bf16_bits_to_f32(u.x & 0xFFFFu); v[1] = bf16_bits_to_f32(u.x >> 16);
-      v[2] = bf16_bits_to_f32(u.y & 0xFFFFu); v[3] = bf16_bits_to_f32(u.y >> 16);
-    } else {
-      const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
-      v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+      w[0] = u.x; w[1] = u.y;
+    }
+#pragma unroll
+    for (int q = 0; q < N / 2; ++q) {
+      v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu);
+      v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u);
+    }
+  } else if (wide) {
+#pragma unroll
+    for (int q = 0; q + 3 < N; q += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + q);
+      v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
+    for (int j = 0; j < N; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
   }
 }
-__device__ __forceinline__ void store4(void* p, size_t i, int dtype, int n, bool wide, const float* v) {
-  if (wide) {
-    if (dtype == MOE_VQ_BF16) {
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-          make_uint2((uint32_t)f32_to_bf16_rne(v[0]) | ((uint32_t)f32_to_bf16_rne(v[1]) << 16),
-                     (uint32_t)f32_to_bf16_rne(v[2]) | ((uint32_t)f32_to_bf16_rne(v[3]) << 16));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-    }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});  // (rounds to nearest even, NaN stays NaN)
+}
+template <int N>
+__device__ __forceinline__ void store_n(void* p, size_t i, int dtype, int n, bool wide, const float* v) {
+  if (N == 1) wide = false;
+  if (wide && dtype == MOE_VQ_BF16) {
+    uint16_t* to = static_cast<uint16_t*>(p) + i;
+    if constexpr (N == 8)
+      *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    else if constexpr (N == 4)
+      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+  } else if (wide) {
+#pragma unroll
+    for (int q = 0; q + 3 < N; q += 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
   } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < N; ++j)
       if (j < n) store_as(p, i + j, dtype, v[j]);
   }
 }
 
-// Epilogue of four consecutive output columns n.. of output row m: bias, z, activation,
-// residual, one rounding to the output's type.  v: the sums (SWIGLU: the gate's), u: the up
-// sums.  z keeps the values before the activation, rounded once to its type.
-template <bool GATED>
-__device__ __forceinline__ void epilogue4(const GemmArgs& g, int grp, size_t m, int n, float* v, float* u) {
+// Epilogue of N consecutive output columns n.. of output row m: bias, z, activation, residual, one
+// rounding to the output's type.  v: the sums (SWIGLU: the gate's), u: the up sums.  z keeps the
+// values before the activation, rounded once to its type.  wide: out_n is a multiple of N.
+template <bool GATED, int N>
+__device__ __forceinline__ void epilogue(const GemmArgs& g, int grp, size_t m, int n, bool wide, float* v, float* u) {
   const int left = g.ldo - n;
-  const bool wide = (g.ldo & 3) == 0;  // (then left >= 4, and every row starts on a multiple of four)
   const size_t wrows = GATED ? 2 * (size_t)g.ldo : (size_t)g.ldo;
   if (g.bias) {
     const float* b = g.bias + grp * wrows;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < N; ++j) {
       if (j < left) {
         v[j] += b[n + j];
         if (GATED) u[j] += b[(size_t)g.ldo + n + j];
@@ -161,27 +182,27 @@ __device__ __forceinline__ void epilogue4(const GemmArgs& g, int grp, size_t m, 
     }
   }
   if (g.z) {
-    store4(g.z, m * wrows + n, g.z_dtype, left, wide, v);
-    if (GATED) store4(g.z, m * wrows + g.ldo + n, g.z_dtype, left, wide, u);
+    store_n<N>(g.z, m * wrows + n, g.z_dtype, left, wide, v);
+    if (GATED) store_n<N>(g.z, m * wrows + g.ldo + n, g.z_dtype, left, wide, u);
   }
   if (GATED) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = swiglu(v[j], u[j], g.lim);
+    for (int j = 0; j < N; ++j) v[j] = swiglu(v[j], u[j], g.lim);
   } else if (g.act == MOE_VQ_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = silu_fast(v[j]);
+    for (int j = 0; j < N; ++j) v[j] = silu_fast(v[j]);
   } else if (g.act == MOE_VQ_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = gelu(v[j]);
+    for (int j = 0; j < N; ++j) v[j] = gelu(v[j]);
   }
   const size_t at = m * (size_t)g.ldo + n;
   if (g.res) {
-    float r[4];
-    load4(g.res, at, g.out_dtype, left, wide, r);
+    float r[N];
+    load_n<N>(g.res, at, g.out_dtype, left, wide, r);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += r[j];
+    for (int j = 0; j < N; ++j) v[j] += r[j];
   }
-  store4(g.out, at, g.out_dtype, left, wide, v);
+  store_n<N>(g.out, at, g.out_dtype, left, wide, v);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -196,17 +217,18 @@ __device__ __forceinline__ void group_rows(const GemmArgs& g, int grp, int& r0, 
   r1 = r1 < r0 ? r0 : (r1 > g.M ? g.M : r1);
 }
 
-// The workgroups of one XCD (every eighth) take neighbouring tiles, so that its L2 serves
-// the operands they share.
+// The workgroups of one XCD (every eighth) take neighbouring ones of n tiles, so that its L2 serves the
+// operands they share.
 __device__ __forceinline__ int xcd_order(int bid, int n) {
   const int x = bid & 7, q = n >> 3, r = n & 7;
   return x * q + (x < r ? x : r) + (bid >> 3);
 }
 
-// Tile id -> (row tile, column tile): bands of eight row tiles, column by column within a band,
-// so that 32 neighbouring tiles share eight row tiles and four column tiles.
+// Tile id -> (row tile, column tile): bands of BAND row tiles, column by column within a band, so that
+// 32 neighbouring tiles (one XCD's at a time) share eight row tiles and four column tiles, or four and
+// eight where the column operand is the smaller.
+template <int BAND>
 __device__ __forceinline__ void band_order(int id, int mt, int nt, int& im, int& in) {
-  constexpr int BAND = 8;
   const int band = id / (BAND * nt), rem = id - band * BAND * nt;
   const int h = mt - band * BAND < BAND ? mt - band * BAND : BAND;
   in = rem / h;
@@ -214,9 +236,11 @@ __device__ __forceinline__ void band_order(int id, int mt, int nt, int& im, int&
 }
 
 // LDS position of 16-byte chunk c (0..7) of an along operand's row: the chunks of a row are
-// exchanged by its number so that the 16 rows a matrix operand reads at one chunk column lie
-// in 16 different groups of four banks.
-__device__ __forceinline__ int along_swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// exchanged by its number, so that the lanes of each of a 16-byte read's four phases (lanes 0-3,
+// 12-15, 20-27 in the first) lie in 16 different groups of four banks.  Measured without
+// conflicts; exchanging rows 8 to 15 once more, which would suit phases of 16 consecutive lanes,
+// doubles the reads' time.
+__device__ __forceinline__ int along_swizzle(int row) { return row & 7; }
 
 // The same for an across operand's row, in units of 16 values (32 bytes of bf16, 64 of fp32):
 // the rows that one read touches spread over the units of a 256-byte bank window.
@@ -227,8 +251,16 @@ __device__ __forceinline__ int across_swizzle(int row) {
   return UNITS >= 8 ? (row & 3) | ((row >> 1) & 4) : (row & 3) ^ ((row >> 3) & 1);
 }
 
-// This wave's loads into LDS have landed (vmcnt 0; the barrier after it then covers every wave's).
-__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
+// A barrier behind which, for every wave, all but the last N of its loads into LDS have landed
+// (vmcnt N) and every read of LDS before it is done (lgkmcnt 0).  The empty asm keeps the
+// compiler from moving memory accesses over it.
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // One operand of a tile: B rows of output space (ALONG) or B columns (across), loaded by NW waves.
 template <typename E, int B, bool ALONG, int NW>
@@ -237,26 +269,26 @@ struct Operand {
   static constexpr int LOADS = BYTES / 1024 / NW;     // 1 KiB per wave and load
   static constexpr int ROWB = B * E::SIZE;            // bytes of an across row
   static constexpr int KT = STEP_BYTES / E::SIZE;     // contraction values per step
+  static constexpr int READS = ALONG ? 1 : E::SIZE;   // LDS reads of a matrix operand (2 of bf16, 4 of fp32 across)
   static_assert(LOADS >= 1 && LOADS * NW * 1024 == BYTES, "loads divide evenly over the waves");
   uint64_t base;    // address of this step's first byte
-  uint32_t left;    // bytes from base to the end of what may be read
-  uint32_t step, cut;  // bytes base advances per step; across: bytes of one row
+  uint32_t left;    // along: bytes from base to the end of what may be read; across: byte offset of the tile's first column
+  uint32_t step, cut;  // across: bytes of a step's rows, of one row
   uint32_t off[LOADS];
-  uint32_t tail[LOADS];  // along: first contraction value of the lane's chunk
+  int first;        // along: first contraction value of the lane's chunk
 
   // along: the rows start at p, `bytes` of them may be read; row r of the tile is row
   // r, or with half > 0 the r-th of blocks of 16 gate rows and 16 up rows (half rows apart).
   __device__ __forceinline__ void init_along(const char* p, uint64_t bytes, uint32_t pitch, int half, int lane, int wave) {
     base = (uint64_t)p;
     left = (uint32_t)bytes;
-    step = STEP_BYTES;
+    const int c = (lane & 7) ^ along_swizzle(lane >> 3);
+    first = c * (16 / E::SIZE);
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-      const int q = wave * LOADS + j, row = q * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ along_swizzle(row);
+      const int row = (wave * LOADS + j) * 8 + (lane >> 3);
       const int src = half ? ((row >> 4) & 1) * half + (row >> 5) * 16 + (row & 15) : row;
       off[j] = (uint32_t)src * pitch + c * 16;
-      tail[j] = c * (16 / E::SIZE);
     }
   }
   // across: contraction rows from p on, `rows` of them; col: byte offset of the tile's first column.
@@ -272,35 +304,30 @@ struct Operand {
       off[j] = (uint32_t)row * pitch + unit * E::UNIT + b % E::UNIT;
     }
   }
+  template <bool SHORT>
   __device__ __forceinline__ void issue(lds_char* lds, uint32_t avail, int rest, int wave) const {
     const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)avail, 0x00020000);
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
       // (a chunk behind the end of an along row is sent out of range, which reads as zero)
-      const uint32_t o = ALONG && (int)tail[j] >= rest ? 0x80000000u : off[j];
+      const uint32_t o = ALONG && SHORT && first >= rest ? 0x80000000u : off[j];
       __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * LOADS + j) * 1024), 16, o, 0, 0, 0);
     }
   }
-  // Load the step that has `rest` contraction values left (across: rows), and move on.
+  // Load the step that has `rest` contraction values left (across: rows; SHORT: fewer than a whole
+  // step's), and move on.
+  template <bool SHORT>
   __device__ __forceinline__ void load(lds_char* lds, int rest, int wave) {
-    if (ALONG) {
-      issue(lds, left, rest, wave);
-      base += step;
-      left -= left < step ? left : step;
-    } else {
-      const uint32_t rows = rest < KT ? rest : KT;
-      // (the descriptor starts at the tile's first column and ends with the last row)
-      issue(lds, rows * cut - left, rest, wave);
-      base += step;
-    }
+    // (an across descriptor starts at the tile's first column and ends with the last row)
+    issue<SHORT>(lds, ALONG ? left : (SHORT ? (uint32_t)rest * cut : step) - left, rest, wave);
+    base += ALONG ? STEP_BYTES : step;
+    if (ALONG) left -= STEP_BYTES;
   }
   // Matrix operand f (16 rows or columns of output space) of half-step s.
   static __device__ __forceinline__ u32x4_t frag(const lds_char* lds, int f, int s, int lane) {
     const int i = lane & 15, g = lane >> 4;
     if (ALONG) {
-      const int row = f * 16 + i;
-      const int c = (s * 4 + g) ^ along_swizzle(row);
-      return *(const __attribute__((address_space(3))) u32x4_t*)(lds + row * STEP_BYTES + c * 16);
+      return *(const __attribute__((address_space(3))) u32x4_t*)(lds + (f * 16 + i) * STEP_BYTES + ((s * 4 + g) ^ along_swizzle(i)) * 16);
     } else if (E::SIZE == 2) {
       u32x2_t v[2];
 #pragma unroll
@@ -322,7 +349,7 @@ struct Operand {
   }
 };
 
-template <typename E, int BM, int BN, int WM, int WN, int MODE>
+template <typename E, int BM, int BN, int WM, int WN, int NS, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   constexpr int NW = WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
@@ -331,7 +358,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   static_assert(!GATED || FN % 2 == 0, "a wave holds gate and up of its columns");
   using OpB = Operand<E, BN, FORWARD, NW>;
   constexpr int KT = OpA::KT;
-  __shared__ __align__(1024) char lds_mem[2 * (BM + BN) * STEP_BYTES];
+  constexpr int STAGE = (BM + BN) * STEP_BYTES;
+  __shared__ __align__(1024) char lds_mem[NS * STAGE];
   lds_char* lds = (lds_char*)lds_mem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -347,39 +375,41 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     split = bid / tiles;
     const int id = bid - split * tiles;
     grp = id / (mt * nt);
-    band_order(id - grp * mt * nt, mt, nt, im, in);
+    band_order<4>(id - grp * mt * nt, mt, nt, im, in);
     group_rows(g, grp, r0, r1);
     m0 = im * BM;
   } else {
-    // every lane counts the row tiles of its share of the groups
+    // Every lane counts the row tiles of its share of the groups.  A group's tiles are neighbours, so
+    // that its weights are read from memory once: its short last tile among them (run after all
+    // others instead, to even out the end, those tiles read the weights again and took longer).
     const int q = (g.G + 63) / 64;
     int cnt = 0;
     for (int i = 0; i < q; ++i) {
       const int e = lane * q + i;
       if (e < g.G) {
-        int a, b;
-        group_rows(g, e, a, b);
-        cnt += (b - a + BM - 1) / BM;
+        int lo, hi;
+        group_rows(g, e, lo, hi);
+        cnt += (hi - lo + BM - 1) / BM;
       }
     }
     const int inc = wave_incl_scan(cnt);
-    const int mt = __builtin_amdgcn_readlane(inc, 63);
-    const int tiles = mt * nt;
-    if ((int)blockIdx.x >= tiles * g.splits) return;
+    const int tiles = __builtin_amdgcn_readlane(inc, 63) * nt;
+    if ((int)blockIdx.x >= tiles * g.splits) return;  // (the grid is an upper bound)
     const int bid = xcd_order(blockIdx.x, tiles * g.splits);
     split = bid / tiles;
-    band_order(bid - split * tiles, mt, nt, im, in);
-    const int l = __popcll(__ballot(inc <= im));  // the lane whose groups hold row tile im
-    int rel = im - (__builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(cnt, l));
+    const int id = bid - split * tiles, row_tile = id / nt;
+    const int l = __popcll(__ballot(inc <= row_tile));  // the lane whose groups hold it
+    int before = __builtin_amdgcn_readlane(inc, l) - __builtin_amdgcn_readlane(cnt, l), n;
     grp = l * q;
     for (;;) {
       group_rows(g, grp, r0, r1);
-      const int n = (r1 - r0 + BM - 1) / BM;
-      if (rel < n || grp + 1 >= g.G) break;
-      rel -= n;
+      n = (r1 - r0 + BM - 1) / BM;
+      if (row_tile < before + n || grp + 1 >= g.G) break;
+      before += n;
       ++grp;
     }
-    m0 = r0 + rel * BM;
+    band_order<8>(id - before * nt, n, nt, im, in);
+    m0 = r0 + im * BM;
   }
   const int n0 = in * per_n;
 
@@ -422,85 +452,127 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // ---- the contraction: the next step's operands arrive while this step is multiplied
-  constexpr int STAGE = (BM + BN) * STEP_BYTES;
-  if (steps > 0) {
-    a.load(lds, rest, wave);
-    b.load(lds + OpA::BYTES, rest, wave);
+  // ---- the contraction: NS stages of LDS, so NS - 1 steps' operands are on their way while one is
+  // multiplied.  One barrier per step: behind it the step's operands are there for every wave, and
+  // every wave has done with the step before, whose stage takes the next load.
+  constexpr int LOADS = OpA::LOADS + OpB::LOADS;
+  auto load = [&](int stage) {
+    lds_char* to = lds + stage * STAGE;
+    if (rest >= KT) {
+      a.template load<false>(to, rest, wave);
+      b.template load<false>(to + OpA::BYTES, rest, wave);
+    } else {
+      a.template load<true>(to, rest, wave);
+      b.template load<true>(to + OpA::BYTES, rest, wave);
+    }
     rest -= KT;
-  }
-  wait_loads();
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    lds_char* cur = lds + (s & 1) * STAGE;
-    lds_char* nxt = lds + ((s + 1) & 1) * STAGE;
-    if (s + 1 < steps) {
-      a.load(nxt, rest, wave);
-      b.load(nxt + OpA::BYTES, rest, wave);
-      rest -= KT;
-    }
+  };
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      u32x4_t fa[FM], fb[FN];
-#pragma unroll
-      for (int i = 0; i < FM; ++i) fa[i] = OpA::frag(cur, wm * FM + i, h, lane);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = OpB::frag(cur + OpA::BYTES, wn * FN + j, h, lane);
-#pragma unroll
-      for (int i = 0; i < FM; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j) E::mma(fb[j], fa[i], acc[i][j]);
-    }
-    wait_loads();
-    __syncthreads();
-  }
+  for (int s = 0; s < NS - 1; ++s)
+    if (s < steps) load(s);
+  // Row block i of the wave is block i * WM + wm of the tile: the waves share the rows of a short tile
+  // (a group's last), and skip what lies behind them in pairs of blocks.
+  constexpr int Q = FM >= 2 ? 2 : 1, UNITS = FM / Q;
+  const int m_end = MODE == GEMM_DW ? g.out_m : r1;
+  const int blocks = (m_end - m0 + 15) / 16;
+  const int live = blocks >= BM / 16 ? FM : (blocks - wm + WM - 1) / WM;
+  const int units = blocks >= BM / 16 ? UNITS : ((blocks + WM - 1) / WM + Q - 1) / Q;
 
-  // ---- outputs, 16 rows at a time: lane (i, g) of matrix (fm, fn) holds row 16 fm + i, columns
-  // 16 fn + 4 g ..; through the wave's own part of LDS neighbouring lanes get neighbouring columns
-  // of one row, so that rows leave in long runs
+  // One step on `units` units of Q row operands, as a software pipeline: the next unit's reads of LDS go
+  // out before this unit's matrix instructions.
+  auto multiply = [&](auto live_units, const lds_char* at) {
+    constexpr int U = decltype(live_units)::value;
+    u32x4_t fa[2][Q], fb[2][FN];
+    static_for<0, FN>([&](auto j) { fb[0][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, 0, lane); });
+    static_for<0, Q>([&](auto i) { fa[0][i] = OpA::frag(at, i * WM + wm, 0, lane); });
+    __builtin_amdgcn_sched_group_barrier(0x100, FN * OpB::READS + Q * OpA::READS, 0);
+    static_for<0, 2 * U>([&](auto uu) {
+      constexpr int u = decltype(uu)::value, h = u / U, q = u % U, n = u + 1, nh = n / U, nq = n % U;
+      if constexpr (n < 2 * U) {
+        if constexpr (nq == 0) static_for<0, FN>([&](auto j) { fb[nh][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, nh, lane); });
+        static_for<0, Q>([&](auto i) { fa[n & 1][i] = OpA::frag(at, (nq * Q + i) * WM + wm, nh, lane); });
+        __builtin_amdgcn_sched_group_barrier(0x100, (nq == 0 ? FN * OpB::READS : 0) + Q * OpA::READS, 0);
+      }
+      static_for<0, Q>([&](auto i) {
+        static_for<0, FN>([&](auto j) { E::mma(fb[h][j], fa[u & 1][i], acc[q * Q + i][j]); });
+      });
+      __builtin_amdgcn_sched_group_barrier(0x008, Q * FN * E::MMAS, 0);
+    });
+  };
+  auto contract = [&](auto live_units) {
+    int cur = 0, fill = NS - 1;
+    for (int s = 0; s < steps; ++s) {
+      if (s + NS - 1 <= steps) step_barrier<(NS - 2) * LOADS>();
+      else step_barrier<0>();  // (the last steps: fewer younger ones are on their way)
+      if (s + NS - 1 < steps) load(fill);
+      multiply(live_units, lds + cur * STAGE);
+      cur = cur + 1 == NS ? 0 : cur + 1;
+      fill = fill + 1 == NS ? 0 : fill + 1;
+    }
+  };
+  if (units > UNITS / 2) contract(std::integral_constant<int, UNITS>{});
+  else contract(std::integral_constant<int, UNITS >= 2 ? UNITS / 2 : 1>{});
+  __syncthreads();  // (the outputs are staged where the operands were)
+
+  // ---- outputs, 16 rows at a time: lane (i, g) of a matrix operand holds row i, columns 4 g .. of its
+  // 16; through the wave's own part of LDS a lane gets eight neighbouring columns of one row, so that
+  // rows leave in long runs.  Two parts take turns, so one can fill while the other is read.
   constexpr int PITCH = FN * 16 + 4;
   constexpr int COLS = GATED ? FN * 8 : FN * 16;  // output columns of the wave
-  constexpr int QUADS = COLS / 4;
-  static_assert(NW * 16 * PITCH * 4 <= (int)sizeof(lds_mem), "output staging");
-  float* stage = reinterpret_cast<float*>(lds_mem) + wave * 16 * PITCH;
-  const int m_end = MODE == GEMM_DW ? g.out_m : r1;
+  static_assert(NW * 2 * 16 * PITCH * 4 <= (int)sizeof(lds_mem), "output staging");
+  float* stage = reinterpret_cast<float*>(lds_mem) + wave * 2 * 16 * PITCH;
   const size_t out_rows = MODE == GEMM_DW ? (size_t)g.G * g.out_m : (size_t)g.M;
-  static_for<0, FM>([&](auto fi) {
-    constexpr int i = decltype(fi)::value;
-    static_for<0, FN>([&](auto fj) {
-      constexpr int j = decltype(fj)::value;
-      *reinterpret_cast<f32x4_t*>(stage + (lane & 15) * PITCH + j * 16 + (lane >> 4) * 4) = acc[i][j];
-    });
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll 1
-    for (int t = lane; t < 16 * QUADS; t += 64) {
-      const int rr = t / QUADS, c = (t % QUADS) * 4;
-      const int m = m0 + (wm * FM + i) * 16 + rr, n = n0 + wn * COLS + c;
-      if (m >= m_end || n >= g.out_n) continue;
-      const size_t row = MODE == GEMM_DW ? (size_t)grp * g.out_m + m : (size_t)m;
-      float v[4], u[4];
-      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(stage + rr * PITCH + (GATED ? (c >> 4) * 32 + (c & 15) : c));
+  const size_t out_cols = GATED ? 2 * (size_t)g.out_n : (size_t)g.out_n;
+  // N columns of local row rr (of 16) from local column c
+  auto put = [&](auto width, const float* part, int i, int t, bool wide) {
+    constexpr int N = decltype(width)::value, PER = COLS / N;
+    const int rr = t / PER, c = (t % PER) * N;
+    const int m = m0 + (i * WM + wm) * 16 + rr, n = n0 + wn * COLS + c;
+    if (m >= m_end || n >= g.out_n) return;
+    const size_t row = MODE == GEMM_DW ? (size_t)grp * g.out_m + m : (size_t)m;
+    const float* from = part + rr * PITCH + (GATED ? (c >> 4) * 32 + (c & 15) : c);
+    float v[N], u[N];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v[q] = lo[q];
+    for (int q = 0; q < N; q += 4) {
+      const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(from + q);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[q + j] = lo[j];
       if (GATED) {
-        const f32x4_t up = *reinterpret_cast<const f32x4_t*>(stage + rr * PITCH + (c >> 4) * 32 + 16 + (c & 15));
+        const f32x4_t up = *reinterpret_cast<const f32x4_t*>(from + 16 + q);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) u[q] = up[q];
-      }
-      if (g.splits > 1) {
-        const size_t cols = GATED ? 2 * (size_t)g.out_n : (size_t)g.out_n;
-        float* p = g.part + ((size_t)split * out_rows + row) * cols;
-        store4(p, n, MOE_VQ_F32, g.out_n - n, (g.out_n & 3) == 0, v);
-        if (GATED) store4(p, (size_t)g.out_n + n, MOE_VQ_F32, g.out_n - n, (g.out_n & 3) == 0, u);
-      } else {
-        epilogue4<GATED>(g, grp, row, n, v, u);
+        for (int j = 0; j < 4; ++j) u[q + j] = up[j];
       }
     }
+    if (g.splits > 1) {
+      float* p = g.part + ((size_t)split * out_rows + row) * out_cols;
+      store_n<N>(p, n, MOE_VQ_F32, g.out_n - n, wide, v);
+      if (GATED) store_n<N>(p, (size_t)g.out_n + n, MOE_VQ_F32, g.out_n - n, wide, u);
+    } else if (FORWARD) {
+      epilogue<GATED, N>(g, grp, row, n, wide, v, u);
+    } else {
+      store_n<N>(g.out, row * (size_t)g.ldo + n, E::DTYPE, g.out_n - n, wide, v);
+    }
+  };
+  static_for<0, FM>([&](auto fi) {
+    constexpr int i = decltype(fi)::value;
+    if (i >= live) return;
+    float* part = stage + (i & 1) * 16 * PITCH;
+    static_for<0, FN>([&](auto fj) {
+      constexpr int j = decltype(fj)::value;
+      *reinterpret_cast<f32x4_t*>(part + (lane & 15) * PITCH + j * 16 + (lane >> 4) * 4) = acc[i][j];
+    });
+    // (the wave's LDS accesses complete in order; the fences keep the compiler to it)
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if ((g.out_n & 7) == 0) {
+#pragma unroll
+      for (int t = 0; t < 16 * COLS / 8; t += 64)
+        if (16 * COLS / 8 >= 64 || lane < 16 * COLS / 8) put(std::integral_constant<int, 8>{}, part, i, t + lane, true);
+    } else {
+#pragma unroll 1
+      for (int t = lane; t < 16 * COLS / 4; t += 64) put(std::integral_constant<int, 4>{}, part, i, t, (g.out_n & 3) == 0);
+    }
   });
 }
 
@@ -518,16 +590,16 @@ __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
   for (int s = 0; s < g.splits; ++s) {
     const float* p = g.part + ((size_t)s * rows + m) * cols;
     float t[4];
-    load4(p, n, MOE_VQ_F32, left, wide, t);
+    load_n<4>(p, n, MOE_VQ_F32, left, wide, t);
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] += t[j];
     if (GATED) {
-      load4(p, (size_t)g.ldo + n, MOE_VQ_F32, left, wide, t);
+      load_n<4>(p, (size_t)g.ldo + n, MOE_VQ_F32, left, wide, t);
 #pragma unroll
       for (int j = 0; j < 4; ++j) u[j] += t[j];
     }
   }
-  epilogue4<GATED>(g, 0, m, n, v, u);
+  epilogue<GATED, 4>(g, 0, m, n, wide, v, u);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -558,11 +630,40 @@ struct DzArgs {
   float lim;
 };
 
-constexpr int DZ_TX = 64, DZ_TY = 4;  // threads over columns, over rows
+constexpr int DZ_TX = 32, DZ_TY = 8;  // threads over columns, over rows
 
-// One workgroup: DZ_TX * V columns of one split of one group's rows.  Bound by reading dy and z and
-// writing dz, each once.  dz is rounded to the element type for the matrix products; the
-// column sums add the unrounded values in fp32, rows in a fixed order.
+// dz of V columns of one row: the gate's (or the only) factor in d[0], the up's in d[1].
+template <int V>
+__device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, const float* zg, const float* zu, float (*d)[V]) {
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    d[1][j] = 0.f;
+    if (a.act == MOE_VQ_ACT_NONE) {
+      d[0][j] = dy[j];
+    } else if (a.act == MOE_VQ_ACT_SILU) {
+      d[0][j] = dy[j] * silu_grad(zg[j]);
+    } else if (a.act == MOE_VQ_ACT_GELU) {
+      d[0][j] = dy[j] * gelu_grad(zg[j]);
+    } else {
+      // h = silu(min(g, L)) * clamp(u, -L, L): no gradient through a value that was clamped
+      float gv = zg[j], uv = zu[j];
+      bool gin = true, uin = true;
+      if (a.lim > 0.f) {
+        gin = !(gv > a.lim);
+        uin = !(uv > a.lim) && !(uv < -a.lim);
+        gv = gin ? gv : a.lim;
+        uv = uv > a.lim ? a.lim : (uv < -a.lim ? -a.lim : uv);
+      }
+      d[0][j] = gin ? dy[j] * uv * silu_grad(gv) : 0.f;
+      d[1][j] = uin ? dy[j] * silu_fast(gv) : 0.f;
+    }
+  }
+}
+
+// One workgroup: DZ_TX * V columns of one split of one group's rows, two rows of a thread at a time (their loads are
+// issued together).  Bound by reading dy and z and writing dz, each once.  dz is rounded to the
+// element type for the matrix products; the column sums add the unrounded values in fp32, rows in a
+// fixed order.
 template <int V>
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * V];
@@ -577,60 +678,37 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   }
   const int per = (r1 - r0 + a.splits - 1) / a.splits;
   const int m0 = r0 + split * per, m1 = m0 + per < r1 ? m0 + per : r1;
-  const bool two = a.act == MOE_VQ_ACT_SWIGLU;
+  const bool two = a.act == MOE_VQ_ACT_SWIGLU, any = a.act != MOE_VQ_ACT_NONE;
+  constexpr bool WIDE = V > 1;
   float sum[2][V];
 #pragma unroll
   for (int j = 0; j < V; ++j) sum[0][j] = sum[1][j] = 0.f;
+  auto put = [&](int m, float (*d)[V]) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) { sum[0][j] += d[0][j]; sum[1][j] += d[1][j]; }
+    if (!a.dz) return;
+    const size_t row = (size_t)m * a.pitch;
+    store_n<V>(a.dz, row + n, a.dtype, V, WIDE, d[0]);
+    if (two) store_n<V>(a.dz, row + a.N + n, a.dtype, V, WIDE, d[1]);
+    // (the pitch's last columns take part in dx's contraction as zeros)
+    if (n == 0)
+      for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, a.dtype, 0.f);
+  };
   if (n < a.N) {
-    for (int m = m0 + ty; m < m1; m += DZ_TY) {
-      float dy[V], zg[V], zu[V], dg[V], du[V];
-      const size_t zrow = (size_t)m * a.R + n;
-      if constexpr (V == 4) {
-        load4(a.dy, (size_t)m * a.N + n, a.dy_dtype, 4, true, dy);
-        if (a.act != MOE_VQ_ACT_NONE) load4(a.z, zrow, a.dtype, 4, true, zg);
-        if (two) load4(a.z, zrow + a.N, a.dtype, 4, true, zu);
-      } else {
-        dy[0] = load_as_f32(a.dy, (size_t)m * a.N + n, a.dy_dtype);
-        if (a.act != MOE_VQ_ACT_NONE) zg[0] = load_as_f32(a.z, zrow, a.dtype);
-        if (two) zu[0] = load_as_f32(a.z, zrow + a.N, a.dtype);
+    for (int m = m0 + ty; m < m1; m += 2 * DZ_TY) {
+      float dy[2][V], zg[2][V], zu[2][V], d[2][2][V];
+      const int next = m + DZ_TY < m1 ? m + DZ_TY : m;  // (a thread without a second row loads the first again)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const size_t r = i ? next : m;
+        load_n<V>(a.dy, r * a.N + n, a.dy_dtype, V, WIDE, dy[i]);
+        if (any) load_n<V>(a.z, r * a.R + n, a.dtype, V, WIDE, zg[i]);
+        if (two) load_n<V>(a.z, r * a.R + a.N + n, a.dtype, V, WIDE, zu[i]);
       }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        if (a.act == MOE_VQ_ACT_NONE) {
-          dg[j] = dy[j];
-        } else if (a.act == MOE_VQ_ACT_SILU) {
-          dg[j] = dy[j] * silu_grad(zg[j]);
-        } else if (a.act == MOE_VQ_ACT_GELU) {
-          dg[j] = dy[j] * gelu_grad(zg[j]);
-        } else {
-          // h = silu(min(g, L)) * clamp(u, -L, L): no gradient through a value that was clamped
-          float gv = zg[j], uv = zu[j];
-          bool gin = true, uin = true;
-          if (a.lim > 0.f) {
-            gin = !(gv > a.lim);
-            uin = !(uv > a.lim) && !(uv < -a.lim);
-            gv = gin ? gv : a.lim;
-            uv = uv > a.lim ? a.lim : (uv < -a.lim ? -a.lim : uv);
-          }
-          dg[j] = gin ? dy[j] * uv * silu_grad(gv) : 0.f;
-          du[j] = uin ? dy[j] * silu_fast(gv) : 0.f;
-          sum[1][j] += du[j];
-        }
-        sum[0][j] += dg[j];
-      }
-      if (a.dz) {
-        const size_t row = (size_t)m * a.pitch;
-        if constexpr (V == 4) {
-          store4(a.dz, row + n, a.dtype, 4, true, dg);
-          if (two) store4(a.dz, row + a.N + n, a.dtype, 4, true, du);
-        } else {
-          store_as(a.dz, row + n, a.dtype, dg[0]);
-          if (two) store_as(a.dz, row + a.N + n, a.dtype, du[0]);
-        }
-        // (the pitch's last columns take part in dx's contraction as zeros)
-        if (n == 0)
-          for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, a.dtype, 0.f);
-      }
+      for (int i = 0; i < 2; ++i) dz_values<V>(a, dy[i], zg[i], zu[i], d[i]);
+      put(m, d[0]);
+      if (m + DZ_TY < m1) put(next, d[1]);
     }
   }
   if (!a.bias) return;
@@ -652,44 +730,74 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   }
 }
 
+// The splits' column sums added up: 32 columns by 8 shares of the splits per workgroup, the shares in order.
 __global__ __launch_bounds__(256) void bias_sum_kernel(const float* part, float* out, int n, int splits) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= n) return;
+  __shared__ float red[8][32];
+  const int c = threadIdx.x & 31, share = threadIdx.x >> 5;
+  const int i = blockIdx.x * 32 + c;
+  const int per = (splits + 7) / 8, q0 = share * per, q1 = q0 + per < splits ? q0 + per : splits;
   float s = 0.f;
-  for (int q = 0; q < splits; ++q) s += part[(size_t)q * n + i];
-  out[i] = s;
+  if (i < n) {
+#pragma unroll 4
+    for (int q = q0; q < q1; ++q) s += part[(size_t)q * n + i];
+  }
+  red[share][c] = s;
+  __syncthreads();
+  if (share == 0 && i < n) {
+    float t = 0.f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) t += red[q][c];
+    out[i] = t;
+  }
 }
 
-constexpr int TARGET_TILES = 256;  // one workgroup per compute unit
+using Cut = LinearPlan::Cut;
+constexpr int CUS = 256;
 
-// Splits of a contraction of `steps` steps when `tiles` tiles leave compute units idle: enough to fill
-// the device, with at least eight steps each (a split's partial tile costs a write and a read).
-int pick_splits(long tiles, int steps) {
-  if (tiles <= 0 || tiles * 2 > TARGET_TILES) return 1;
-  long s = TARGET_TILES / tiles;
-  if (s > steps / 8) s = steps / 8;
-  return (int)(s < 1 ? 1 : (s > 32 ? 32 : s));
+// How a product is cut.  rows: output rows in all, of `groups` groups; cols: output columns (weight rows forward); steps: contraction steps;
+// split: whether the contraction may be split.
+//  - 256 x 256 tiles, one workgroup per CU, where they nearly fill the device: 1390 TFLOP/s at 8192^3 where
+//    128 x 128 tiles, which read LDS twice as often for their products, reach 1150.
+//  - 128 x 128, two workgroups per CU, if they fill it, or fill it once the contraction is split
+//    (eight steps per part at least: a part of a tile costs a write and a read of its sums).
+//  - 64 x 64 for what is left: small outputs and short contractions, and at most 64 rows, which
+//    leave more of a larger tile empty than they save.
+Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool split) {
+  const long per = (rows + groups - 1) / groups;
+  auto tiles = [&](long t) { return (per + t - 1) / t * groups * ((cols + t - 1) / t); };
+  auto parts = [&](long n) {
+    const long s = n < 1 ? 1 : 2 * CUS / n;
+    const long most = steps / 8;
+    return !split || s < 2 || most < 2 ? 1 : (int)(s < most ? (s < 32 ? s : 32) : (most < 32 ? most : 32));
+  };
+  if (dtype == MOE_VQ_BF16 && per >= 192 && tiles(256) >= 200) return {256, 1};
+  if (per > 64 && (tiles(128) >= CUS || parts(tiles(128)) > 1)) return {128, parts(tiles(128))};
+  return {64, parts(tiles(64))};
 }
 
-constexpr int TILE = 128;
 int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 
-template <typename E, int MODE>
-void gemm_go(const GemmArgs& g, int grid, hipStream_t st) {
-  gemm_kernel<E, TILE, TILE, 2, 2, MODE><<<grid, 256, 0, st>>>(g);
+template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS>
+void gemm_go(const GemmArgs& g, hipStream_t st) {
+  const int per_n = MODE == GEMM_GATED ? BN / 2 : BN;
+  const long nt = div_up(g.out_n, per_n);
+  // (each group of rows adds at most one partial row tile)
+  const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
+                                  : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
+  const long grid = nt * mt * g.splits;
+  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
 }
 
 template <int MODE>
-hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, hipStream_t st) {
-  const int per_n = MODE == GEMM_GATED ? TILE / 2 : TILE;
-  const long nt = div_up(g.out_n, per_n);
-  // (each group of rows adds at most one partial row tile)
-  const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, TILE) * g.G
-                                  : (g.group_start ? (long)g.M / TILE + (g.G < g.M ? g.G : g.M) : div_up(g.M, TILE));
-  const long grid = nt * mt * g.splits;
-  if (grid <= 0) return hipSuccess;
-  if (p.dtype == MOE_VQ_BF16) gemm_go<Bf16, MODE>(g, (int)grid, st);
-  else gemm_go<F32, MODE>(g, (int)grid, st);
+hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t st) {
+  if (p.dtype == MOE_VQ_BF16) {
+    if (tile == 256) gemm_go<Bf16, MODE, 256, 256, 2, 4, 2>(g, st);
+    else if (tile == 128) gemm_go<Bf16, MODE, 128, 128, 2, 2, 2>(g, st);
+    else gemm_go<Bf16, MODE, 64, 64, 2, 2, 4>(g, st);
+  } else {
+    if (tile == 128) gemm_go<F32, MODE, 128, 128, 2, 2, 2>(g, st);
+    else gemm_go<F32, MODE, 64, 64, 2, 2, 4>(g, st);
+  }
   if (g.splits > 1) {
     const int rows = MODE == GEMM_DW ? g.G * g.out_m : g.M;
     const size_t n = (size_t)rows * ((g.ldo + 3) / 4);
@@ -728,29 +836,36 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   p.xp = take(p.pack_k ? (size_t)p.M * p.Kp * p.size : 0);
   p.wp = take(p.pack_k ? (size_t)p.G * p.R * p.Kp * p.size : 0);
-  p.split_fwd = p.split_dx = p.split_dw = p.split_bias = 1;
+  // A row table may leave rows out, which the sum over the forward's or dx's parts would not know:
+  // those are split only where there can be no table (the launches ask again).
+  const bool one = p.G == 1;
+  p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt), one);
+  p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt), one);
+  p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G), true);
   size_t part = 0;
-  // (splits * tiles <= TARGET_TILES, at most 32 splits)
-  auto most = [&](int cols) {
-    const size_t a = (size_t)TARGET_TILES * TILE * TILE * 4, b = (size_t)32 * p.M * cols * 4;
+  // (parts * tiles <= 2 CUS of at most 128 x 128 sums, and at most 32 parts)
+  auto most = [&](size_t rows, int cols) {
+    const size_t a = (size_t)2 * CUS * 128 * 128 * 4, b = 32 * rows * cols * 4;
     return a < b ? a : b;
   };
   if (!backward) {
-    if (p.G == 1) p.split_fwd = pick_splits((long)div_up(p.M, TILE) * div_up(p.R, TILE), div_up(p.K, kt));
-    if (bound && p.G == 1) part = most(p.R);
-    else if (p.split_fwd > 1) part = (size_t)p.split_fwd * p.M * p.R * 4;
+    if (bound && one) part = most(p.M, p.R);
+    else if (p.fwd.splits > 1) part = (size_t)p.fwd.splits * p.M * p.R * 4;
   } else {
     p.dz = take((size_t)p.M * p.Rp * p.size);
-    const long strips = (long)div_up(p.N, DZ_TX * 4) * p.G;
-    const long want = 2048 / (strips < 1 ? 1 : strips), can = div_up(p.M, 16 * p.G);
+    // (as many workgroups as keep the device busy, each with 16 rows at least)
+    const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 1024 / strips, can = div_up(p.M, 16 * p.G);
     p.split_bias = (int)(want < 1 || can < 1 ? 1 : (want < can ? want : can));
     p.bias_part = take(p.split_bias > 1 ? (size_t)p.split_bias * p.G * p.R * 4 : 0);
-    if (p.G == 1) p.split_dx = pick_splits((long)div_up(p.M, TILE) * div_up(p.K, TILE), div_up(p.R, kt));
-    p.split_dw = pick_splits((long)p.G * div_up(p.R, TILE) * div_up(p.K, TILE), div_up(p.M, (long)kt * p.G));
-    if (bound && p.G == 1) part = most(p.K);
-    else if (p.split_dx > 1) part = (size_t)p.split_dx * p.M * p.K * 4;
-    const size_t dw = p.split_dw > 1 ? (size_t)p.split_dw * p.G * p.R * p.K * 4 : 0;
-    part = part > dw ? part : dw;
+    if (bound) {
+      part = one ? most(p.M, p.K) : 0;
+      const size_t dw = most((size_t)p.G * p.R, p.K);
+      part = part > dw ? part : dw;
+    } else {
+      part = p.dx.splits > 1 ? (size_t)p.dx.splits * p.M * p.K * 4 : 0;
+      const size_t dw = p.dw.splits > 1 ? (size_t)p.dw.splits * p.G * p.R * p.K * 4 : 0;
+      part = part > dw ? part : dw;
+    }
   }
   p.part = take(part);
   p.total = off < 256 ? 256 : off;
@@ -777,8 +892,7 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.G = p.G; g.M = p.M;
   g.kc = p.K;
   g.out_n = p.N;
-  // (a table of one group may leave rows out, which the sum over splits would not know)
-  g.splits = c.group_start ? 1 : p.split_fwd;
+  g.splits = c.group_start ? 1 : p.fwd.splits;
   g.part = at<float>(c.ws, p.part);
   g.bias = c.L->bias;
   g.res = c.residual;
@@ -789,7 +903,8 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.z_dtype = p.dtype;
   g.act = c.L->act;
   g.lim = c.L->swiglu_limit;
-  return c.L->act == MOE_VQ_ACT_SWIGLU ? launch_gemm<GEMM_GATED>(p, g, st) : launch_gemm<GEMM_FWD>(p, g, st);
+  return c.L->act == MOE_VQ_ACT_SWIGLU ? launch_gemm<GEMM_GATED>(p, g, p.fwd.tile, st)
+                                       : launch_gemm<GEMM_FWD>(p, g, p.fwd.tile, st);
 }
 
 hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipStream_t st) {
@@ -806,12 +921,15 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     d.group_start = c.group_start;
     d.M = p.M; d.N = p.N; d.R = p.R; d.G = p.G; d.pitch = p.Rp;
     d.dtype = p.dtype; d.dy_dtype = c.y_dtype; d.act = c.L->act; d.lim = c.L->swiglu_limit;
-    const bool vec = p.N % 4 == 0;
-    const dim3 grid(div_up(p.N, DZ_TX * (vec ? 4 : 1)), p.G, d.splits);
-    if (vec) dz_kernel<4><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
-    else dz_kernel<1><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+    auto go = [&](auto width) {
+      constexpr int V = decltype(width)::value;
+      dz_kernel<V><<<dim3(div_up(p.N, DZ_TX * V), p.G, d.splits), DZ_TX * DZ_TY, 0, st>>>(d);
+    };
+    if (p.N % 8 == 0) go(std::integral_constant<int, 8>{});
+    else if (p.N % 4 == 0) go(std::integral_constant<int, 4>{});
+    else go(std::integral_constant<int, 1>{});
     if (c.dbias && d.splits > 1)
-      bias_sum_kernel<<<div_up((long)p.G * p.R, 256), 256, 0, st>>>(d.bias, c.dbias, p.G * p.R, d.splits);
+      bias_sum_kernel<<<div_up((long)p.G * p.R, 32), 256, 0, st>>>(d.bias, c.dbias, p.G * p.R, d.splits);
   }
   const void* x = c.x;
   const void* w = c.L->w;
@@ -834,15 +952,15 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     g.b = static_cast<const char*>(w);
     g.kc = p.R;
     g.out = c.dx;
-    g.splits = c.group_start ? 1 : p.split_dx;
-    e = launch_gemm<GEMM_DX>(p, g, st);
+    g.splits = c.group_start ? 1 : p.dx.splits;
+    e = launch_gemm<GEMM_DX>(p, g, p.dx.tile, st);
   }
   if (e == hipSuccess && c.dw) {
     g.b = static_cast<const char*>(x);
     g.out_m = p.R;
     g.out = c.dw;
-    g.splits = p.split_dw;
-    e = launch_gemm<GEMM_DW>(p, g, st);
+    g.splits = p.dw.splits;
+    e = launch_gemm<GEMM_DW>(p, g, p.dw.tile, st);
   }
   return e;
 }
