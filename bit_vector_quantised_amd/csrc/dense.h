@@ -52,6 +52,7 @@ struct LinearPlan {
   struct Cut {
     int tile, splits;  // side of the square output tiles; parts of the contraction
   } fwd, dx, dw;
+  bool few;                  // forward by the few-rows kernel, unless rows are in a table
   int split_bias;            // parts of a group's rows in the sums of dbias
   size_t xp, wp, dz, bias_part, part, total;
 };

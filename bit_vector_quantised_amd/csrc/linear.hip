@@ -140,10 +140,6 @@ __device__ __forceinline__ void load_n(const void* p, size_t i, int dtype, int n
     for (int j = 0; j < N; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
   }
 }
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});  // (rounds to nearest even, NaN stays NaN)
-}
 template <int N>
 __device__ __forceinline__ void store_n(void* p, size_t i, int dtype, int n, bool wide, const float* v) {
   if (N == 1) wide = false;
@@ -576,6 +572,78 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   });
 }
 
+// ---------------------------------------------------------------------------------------
+// Few rows: the weights' bytes are what counts
+// ---------------------------------------------------------------------------------------
+
+// Forward product of at most 16 rows.  Bound by streaming W from HBM once; a 64 x 64 tile spends as much on
+// the parts of its split contraction and their sum (one row, 7168 -> 2048 gated, weights not in
+// any cache: 19 us) as on the weights (13 us here, of which the 59 MB take 10 to 11).  A workgroup
+// takes 16 weight rows (gated: eight gate rows and their up rows), its eight waves split the
+// contraction among them, and their sums meet in LDS in a fixed order: one launch.  W goes from
+// memory to the registers of the matrix operand, 16 rows of 64 bytes per load; the rows of x, which
+// every workgroup reads, come from L2.  Four loads ahead measured best of 4, 7, 8, 14 and 16
+// (13.4, 14.2, 15.3, 15.7, 18.3 us), eight waves best of 4, 8 and 16 (17.9, 13.4, 16.6).
+constexpr int FEW_ROWS = 16, FEW_WAVES = 8, FEW_STREAM = 4;
+
+template <typename E, bool GATED>
+__global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(GemmArgs g) {
+  constexpr int STEP = 64, VALS = 16 / E::SIZE;  // bytes of a row per load of its 16 rows; values of a lane
+  constexpr int PITCH = 20;                      // floats between the columns of the staged sums
+  __shared__ __align__(16) float red[FEW_WAVES][FEW_ROWS][PITCH];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int i = lane & 15, q = lane >> 4;
+  constexpr int PER = GATED ? 8 : 16;  // output columns
+  const int n0 = (int)blockIdx.x * PER;
+  // this lane's weight row (rows behind the last repeat it; their sums are dropped)
+  int col = GATED ? n0 + (i & 7) : n0 + i;
+  col = col < g.out_n ? col : g.out_n - 1;
+  const int wrow = GATED && i >= 8 ? g.out_n + col : col;
+  const char* w = g.b + (size_t)wrow * g.b_pitch + q * 16;
+  const char* x = g.a + (size_t)(i < g.M ? i : g.M - 1) * g.a_pitch + q * 16;
+  const int bytes = g.kc * E::SIZE;  // of a row; chunks behind it count as zeros
+  const int steps = (bytes + STEP - 1) / STEP, per = (steps + FEW_WAVES - 1) / FEW_WAVES;
+  const int s0 = wave * per, s1 = s0 + per < steps ? s0 + per : steps;
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+  for (int s = s0; s < s1; s += FEW_STREAM) {
+    u32x4_t wv[FEW_STREAM], xv[FEW_STREAM];
+#pragma unroll
+    for (int j = 0; j < FEW_STREAM; ++j) {
+      // (a load behind this wave's share repeats its last one, a chunk behind the row's end its first one;
+      // both are replaced by zeros below)
+      const int at = (s + j < s1 ? s + j : s1 - 1) * STEP;
+      const int off = at + q * 16 < bytes ? at : -q * 16;
+      wv[j] = *reinterpret_cast<const u32x4_t*>(w + off);
+      xv[j] = *reinterpret_cast<const u32x4_t*>(x + off);
+    }
+#pragma unroll
+    for (int j = 0; j < FEW_STREAM; ++j) {
+      const bool ok = s + j < s1 && (s + j) * STEP + q * 16 < bytes;
+      const u32x4_t none = {0, 0, 0, 0};
+      E::mma(ok ? wv[j] : none, ok ? xv[j] : none, acc);
+    }
+  }
+  // lane (i, q) holds row i of x, weight rows 4 q .. of the 16
+  *reinterpret_cast<f32x4_t*>(&red[wave][i][q * 4]) = acc;
+  __syncthreads();
+  const int m = threadIdx.x / (PER / 4), c = (threadIdx.x % (PER / 4)) * 4;
+  if (m < g.M && n0 + c < g.out_n) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < FEW_WAVES; ++k) {
+      const f32x4_t p = *reinterpret_cast<const f32x4_t*>(&red[k][m][c]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += p[j];
+      if (GATED) {
+        const f32x4_t pu = *reinterpret_cast<const f32x4_t*>(&red[k][m][8 + c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) up[j] += pu[j];
+      }
+    }
+    epilogue<GATED, 4>(g, 0, m, n0 + c, (g.ldo & 3) == 0, v, up);
+  }
+}
+
 // The sum of the splits' parts in order, then the epilogue: four columns per thread.
 template <bool GATED>
 __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
@@ -771,7 +839,7 @@ Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool split
     return !split || s < 2 || most < 2 ? 1 : (int)(s < most ? (s < 32 ? s : 32) : (most < 32 ? most : 32));
   };
   if (dtype == MOE_VQ_BF16 && per >= 192 && tiles(256) >= 200) return {256, 1};
-  if (per > 64 && (tiles(128) >= CUS || parts(tiles(128)) > 1)) return {128, parts(tiles(128))};
+  if (per > 64 && tiles(128) * parts(tiles(128)) >= CUS) return {128, parts(tiles(128))};
   return {64, parts(tiles(64))};
 }
 
@@ -804,6 +872,13 @@ hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t s
     split_sum_kernel<MODE == GEMM_GATED><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, rows);
   }
   return hipGetLastError();
+}
+
+template <typename E>
+void few_go(const GemmArgs& g, bool gated, hipStream_t st) {
+  const unsigned grid = (unsigned)div_up(g.out_n, gated ? 8 : 16);
+  if (gated) few_rows_kernel<E, true><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  else few_rows_kernel<E, false><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
 }
 
 void pack_rows(const LinearPlan& p, const void* src, void* dst, size_t rows, hipStream_t st) {
@@ -840,6 +915,7 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   // those are split only where there can be no table (the launches ask again).
   const bool one = p.G == 1;
   p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt), one);
+  p.few = one && p.M <= FEW_ROWS;
   p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt), one);
   p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G), true);
   size_t part = 0;
@@ -854,7 +930,7 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   } else {
     p.dz = take((size_t)p.M * p.Rp * p.size);
     // (as many workgroups as keep the device busy, each with 16 rows at least)
-    const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 1024 / strips, can = div_up(p.M, 16 * p.G);
+    const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 2048 / strips, can = div_up(p.M, 16 * p.G);
     p.split_bias = (int)(want < 1 || can < 1 ? 1 : (want < can ? want : can));
     p.bias_part = take(p.split_bias > 1 ? (size_t)p.split_bias * p.G * p.R * 4 : 0);
     if (bound) {
@@ -903,6 +979,11 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.z_dtype = p.dtype;
   g.act = c.L->act;
   g.lim = c.L->swiglu_limit;
+  if (p.few && !c.group_start) {
+    if (p.dtype == MOE_VQ_BF16) few_go<Bf16>(g, c.L->act == MOE_VQ_ACT_SWIGLU, st);
+    else few_go<F32>(g, c.L->act == MOE_VQ_ACT_SWIGLU, st);
+    return hipGetLastError();
+  }
   return c.L->act == MOE_VQ_ACT_SWIGLU ? launch_gemm<GEMM_GATED>(p, g, p.fwd.tile, st)
                                        : launch_gemm<GEMM_FWD>(p, g, p.fwd.tile, st);
 }

@@ -140,6 +140,12 @@ __device__ __forceinline__ uint16_t f32_to_bf16_rne(float f) {
   return (uint16_t)(u >> 16);
 }
 
+// Two fp32 -> two bf16 (low half first), round to nearest even (one v_cvt_pk_bf16_f32; a NaN stays NaN).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
 // E8M0 shared exponent -> 2^(e-127) as fp32 (e = 0 gives the subnormal 2^-127, 255 NaN).
 // v_ldexp_f32 of 1.0 needs no literal constants; 255 gives 2^128 = inf, and inf - inf
 // is the NaN that code encodes.

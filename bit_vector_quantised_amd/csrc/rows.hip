@@ -91,10 +91,18 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(SortArgs a) {
   int before = 0, all = mine;
   if (MODE == SORT_PLACE && tid < E) {
     all = 0;
-    for (int b = 0; b < (int)gridDim.x; ++b) {
-      const int c = a.hist[(size_t)b * E + tid];
-      if (b < (int)blockIdx.x) before += c;
-      all += c;
+    for (int b0 = 0; b0 < (int)gridDim.x; b0 += 8) {  // (eight loads at once; behind the last, its count again)
+      int c[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int b = b0 + i < (int)gridDim.x ? b0 + i : (int)gridDim.x - 1;
+        c[i] = a.hist[(size_t)b * E + tid];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (b0 + i < (int)blockIdx.x) before += c[i];
+        if (b0 + i < (int)gridDim.x) all += c[i];
+      }
     }
   }
   const int inc = wave_incl_scan(all);
@@ -128,7 +136,43 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(SortArgs a) {
   }
 }
 
+// At most 64 pairs: every lane holds one and counts the pairs before it (smaller expert, or the same and an
+// earlier pair); the rest of the work, the experts' first rows, is counted the same way.
+// Measured 2.7 us for one token's eight pairs, where the counting sort takes 5.0.
+constexpr int SORT_FEW = 64;
+
+__global__ __launch_bounds__(256) void sort_few_kernel(SortArgs a) {
+  const int tid = threadIdx.x, lane = tid & 63, E = a.E, P = a.P;
+  const int id = lane < P ? a.ids[lane] : -1;
+  const bool ok = (uint32_t)id < (uint32_t)E;
+  const int key = ok ? id : E;
+  const int total = __popcll(__ballot(ok));
+  if (tid < 64) {
+    int row = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) {
+      const int k = __builtin_amdgcn_readlane(key, j);
+      row += (k < key || (k == key && j < lane)) ? 1 : 0;
+    }
+    if (lane < P) {
+      a.pair_row[lane] = ok ? row : -1;
+      if (ok) a.row_pair[row] = lane;
+      if (lane >= total) a.row_pair[lane] = -1;
+    }
+  }
+  for (int e0 = 0; e0 <= E; e0 += 256) {
+    int first = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j) first += __builtin_amdgcn_readlane(key, j) < e0 + tid ? 1 : 0;
+    if (e0 + tid <= E) a.start[e0 + tid] = first;
+  }
+}
+
 hipError_t launch_sort(const SortArgs& a, hipStream_t st) {
+  if (a.P <= SORT_FEW) {
+    sort_few_kernel<<<1, 256, 0, st>>>(a);
+    return hipGetLastError();
+  }
   const int nb = sort_blocks(a.P);
   const bool few = sort_steps(a.P) == 4;
   if (nb <= 1) {
@@ -150,72 +194,112 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t st) {
 // Rows
 // ---------------------------------------------------------------------------------------
 
-// N consecutive elements of a bf16 (uint16_t) or fp32 row, as fp32.  N > 1: the address is
-// a multiple of N elements' bytes, at most 16.
-template <int N>
-__device__ __forceinline__ void load_n(const uint16_t* p, float* v) {
-  if constexpr (N == 8) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) { v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu); v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u); }
-  } else if constexpr (N == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    v[0] = bf16_bits_to_f32(u.x & 0xFFFFu); v[1] = __builtin_bit_cast(float, u.x & 0xFFFF0000u);
-    v[2] = bf16_bits_to_f32(u.y & 0xFFFFu); v[3] = __builtin_bit_cast(float, u.y & 0xFFFF0000u);
-  } else {
-    static_assert(N == 1, "elements per load");
+// N consecutive elements of a bf16 (uint16_t) or fp32 row, the first `left` of them valid, as fp32.  A
+// row of an odd width starts at any multiple of its element, and so may these addresses: the vector
+// accesses are declared with the element's alignment (the device takes them at any address).
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// STREAM: the vector accesses bypass the caches' usual replacement (nontemporal), for rows that
+// no cache would hold until they are read again.
+template <bool STREAM, typename V>
+__device__ __forceinline__ V load_vec(const V* p) {
+  if constexpr (STREAM) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_vec(V* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
+template <int N, bool STREAM>
+__device__ __forceinline__ void load_n(const uint16_t* p, int left, float* v) {
+  if constexpr (N == 1) {
     v[0] = bf16_bits_to_f32(*p);
+  } else if (left >= N) {
+    uint32_t w[N / 2];
+    if constexpr (N == 8) {
+      const u32x4_any u = load_vec<STREAM>(reinterpret_cast<const u32x4_any*>(p));
+      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else {
+      const u32x2_any u = load_vec<STREAM>(reinterpret_cast<const u32x2_any*>(p));
+      w[0] = u.x; w[1] = u.y;
+    }
+#pragma unroll
+    for (int q = 0; q < N / 2; ++q) {
+      v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu);
+      v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = q < left ? bf16_bits_to_f32(p[q]) : 0.f;
   }
 }
-template <int N>
-__device__ __forceinline__ void load_n(const float* p, float* v) {
+template <int N, bool STREAM>
+__device__ __forceinline__ void load_n(const float* p, int left, float* v) {
   if constexpr (N == 1) {
     v[0] = *p;
-  } else {
-    static_assert(N % 4 == 0, "elements per load");
+  } else if (left >= N) {
 #pragma unroll
-    for (int q = 0; q < N / 4; ++q) {
-      const float4 u = reinterpret_cast<const float4*>(p)[q];
-      v[4 * q] = u.x; v[4 * q + 1] = u.y; v[4 * q + 2] = u.z; v[4 * q + 3] = u.w;
+    for (int q = 0; q < N; q += 4) {
+      const f32x4_any u = load_vec<STREAM>(reinterpret_cast<const f32x4_any*>(p + q));
+      v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
     }
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = q < left ? p[q] : 0.f;
   }
 }
-template <int N>
-__device__ __forceinline__ void store_n(uint16_t* p, const float* v) {
+template <int N, bool STREAM>
+__device__ __forceinline__ void store_n(uint16_t* p, int left, const float* v) {
   if constexpr (N == 1) {
     *p = f32_to_bf16_rne(v[0]);
-  } else {
+  } else if (left >= N) {
     uint32_t w[N / 2];
 #pragma unroll
     for (int q = 0; q < N / 2; ++q)
-      w[q] = (uint32_t)f32_to_bf16_rne(v[2 * q]) | ((uint32_t)f32_to_bf16_rne(v[2 * q + 1]) << 16);
-    if constexpr (N == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  }
-}
-template <int N>
-__device__ __forceinline__ void store_n(float* p, const float* v) {
-  if constexpr (N == 1) {
-    *p = v[0];
+      w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+    if constexpr (N == 8) store_vec<STREAM>(reinterpret_cast<u32x4_any*>(p), u32x4_any{w[0], w[1], w[2], w[3]});
+    else store_vec<STREAM>(reinterpret_cast<u32x2_any*>(p), u32x2_any{w[0], w[1]});
   } else {
 #pragma unroll
-    for (int q = 0; q < N / 4; ++q)
-      reinterpret_cast<float4*>(p)[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+    for (int q = 0; q < N; ++q)
+      if (q < left) p[q] = f32_to_bf16_rne(v[q]);
+  }
+}
+template <int N, bool STREAM>
+__device__ __forceinline__ void store_n(float* p, int left, const float* v) {
+  if constexpr (N == 1) {
+    *p = v[0];
+  } else if (left >= N) {
+#pragma unroll
+    for (int q = 0; q < N; q += 4) store_vec<STREAM>(reinterpret_cast<f32x4_any*>(p + q), f32x4_any{v[q], v[q + 1], v[q + 2], v[q + 3]});
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      if (q < left) p[q] = v[q];
   }
 }
 
-constexpr int ROW_THREADS = 256;
+// 128 threads: for 4096 tokens of 7168 columns, top-8, gather takes 94 us (256 threads: 99, 512: 106)
+// and combine 97 (106, 122).
+constexpr int ROW_THREADS = 128, ROW_THREADS_LOG = 7;
+
+// Rows of more bytes than the memory-side cache holds are streamed: gather 94 us instead of 105,
+// combine 97 instead of 109 (470 MB of rows); smaller ones stay where the next kernel finds them.
+static bool streamed(const RowsArgs& a, size_t size) { return (size_t)a.T * a.k * a.C * size > ((size_t)256 << 20); }
 
 // Units of a row over a workgroup's threads: TX of them side by side on one token (a power
-// of two, so a narrow row does not leave lanes idle), 256 / TX tokens.
+// of two, so a narrow row does not leave lanes idle), ROW_THREADS / TX tokens.
 struct RowGrid {
   int tx_log, nbx;
   unsigned grid;
 };
 static RowGrid row_grid(int units, int T) {
   RowGrid g{};
-  while (g.tx_log < 8 && (1 << g.tx_log) < units) ++g.tx_log;
+  while (g.tx_log < ROW_THREADS_LOG && (1 << g.tx_log) < units) ++g.tx_log;
   g.nbx = (units + (1 << g.tx_log) - 1) >> g.tx_log;
   const int ty = ROW_THREADS >> g.tx_log;
   g.grid = (unsigned)g.nbx * (unsigned)((T + ty - 1) / ty);
@@ -227,53 +311,59 @@ __device__ __forceinline__ void row_pos(int tx_log, int nbx, int& t, int& u) {
   u = (bx << tx_log) + ((int)threadIdx.x & ((1 << tx_log) - 1));
 }
 
-// xs[row(t,i)] = x[t] for the token's k pairs, in units of type U.  Bound by the k row
-// writes; the token's row is read once.
-template <typename U>
-__global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowsArgs a, int units, int tx_log, int nbx) {
+// xs[row(t,i)] = x[t] for the token's k pairs, 16 bytes per thread (the row's last ones by element).  Bound by
+// the k row writes; the token's row is read once.
+template <bool STREAM>
+__global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowsArgs a, size_t bytes, int units, int tx_log, int nbx) {
   int t, u;
   row_pos(tx_log, nbx, t, u);
   if (t >= a.T || u >= units) return;
-  const U v = static_cast<const U*>(a.x)[(size_t)t * units + u];
-  const int32_t* at = a.pair_row + (size_t)t * a.k;
+  const size_t at = (size_t)u * 16;
+  const char* from = static_cast<const char*>(a.x) + (size_t)t * bytes + at;
+  char* to = static_cast<char*>(a.y) + at;
+  const int32_t* row = a.pair_row + (size_t)t * a.k;
   const int P = a.T * a.k;
-  for (int i = 0; i < a.k; ++i) {
-    const int r = at[i];
-    if ((uint32_t)r < (uint32_t)P) static_cast<U*>(a.y)[(size_t)r * units + u] = v;
+  if (at + 16 <= bytes) {
+    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from);  // (streaming the loads too takes 105 us)
+    for (int i = 0; i < a.k; ++i) {
+      const int r = row[i];
+      if ((uint32_t)r < (uint32_t)P) store_vec<STREAM>(reinterpret_cast<u32x4_any*>(to + (size_t)r * bytes), v);
+    }
+  } else {
+    const int n = (int)(bytes - at) / 2;  // (an element is two bytes, or four)
+    for (int i = 0; i < a.k; ++i) {
+      const int r = row[i];
+      if ((uint32_t)r >= (uint32_t)P) continue;
+      for (int j = 0; j < n; ++j)
+        reinterpret_cast<uint16_t*>(to + (size_t)r * bytes)[j] = reinterpret_cast<const uint16_t*>(from)[j];
+    }
   }
 }
 
 hipError_t launch_gather(const RowsArgs& a, int dtype, hipStream_t st) {
   const size_t bytes = (size_t)a.C * (dtype == MOE_VQ_BF16 ? 2 : 4);
-  auto go = [&](auto unit) {
-    using U = decltype(unit);
-    const int units = (int)(bytes / sizeof(U));
-    const RowGrid g = row_grid(units, a.T);
-    gather_kernel<U><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
-  };
-  // (a row of an odd width starts anywhere: the widest unit that divides its bytes)
-  if (bytes % 16 == 0) go(uint4{});
-  else if (bytes % 4 == 0) go(uint32_t{});
-  else go(uint16_t{});
+  const int units = (int)((bytes + 15) / 16);
+  const RowGrid g = row_grid(units, a.T);
+  if (streamed(a, bytes / a.C)) gather_kernel<true><<<g.grid, ROW_THREADS, 0, st>>>(a, bytes, units, g.tx_log, g.nbx);
+  else gather_kernel<false><<<g.grid, ROW_THREADS, 0, st>>>(a, bytes, units, g.tx_log, g.nbx);
   return hipGetLastError();
 }
 
 // y[t] = add[t] + sum_i w_i rows[row_i], N columns per thread, fp32 sums in the order of i.
 // Eight rows' loads are issued before the first is used; a dropped pair's load is
 // redirected to row 0 and its value dropped (selected, not multiplied: it may hold NaN).
-template <typename TR, typename TY, int N>
-__global__ __launch_bounds__(ROW_THREADS) void combine_rows_kernel(RowsArgs a, int units, int tx_log, int nbx) {
-  int t, u;
-  row_pos(tx_log, nbx, t, u);
-  if (t >= a.T || u >= units) return;
+// left: columns of the thread's N that the row has (the whole N for all but a row's last thread,
+// which takes a branch of its own, so that the loads of the others stay together).
+template <typename TR, typename TY, int N, bool STREAM>
+__device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t col, int left) {
   const int k = a.k, P = a.T * k;
-  const size_t C = (size_t)a.C, col = (size_t)u * N;
+  const size_t C = (size_t)a.C;
   const TR* rows = static_cast<const TR*>(a.x);
   const int32_t* at = a.pair_row + (size_t)t * k;
   const float* wt = a.pair_w ? a.pair_w + (size_t)t * k : nullptr;
   float acc[N];
   if (a.add) {
-    load_n<N>(static_cast<const TY*>(a.add) + (size_t)t * C + col, acc);
+    load_n<N, STREAM>(static_cast<const TY*>(a.add) + (size_t)t * C + col, left, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < N; ++q) acc[q] = 0.f;
@@ -287,24 +377,35 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_rows_kernel(RowsArgs a, i
       const int r = at[j];
       ok[i] = i0 + i < k && (uint32_t)r < (uint32_t)P;
       w[i] = wt ? wt[j] : 1.f;
-      load_n<N>(rows + (ok[i] ? (size_t)r : 0) * C + col, v[i]);
+      load_n<N, STREAM>(rows + (ok[i] ? (size_t)r : 0) * C + col, left, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int q = 0; q < N; ++q) acc[q] = ok[i] ? fmaf(w[i], v[i][q], acc[q]) : acc[q];
   }
-  store_n<N>(static_cast<TY*>(a.y) + (size_t)t * C + col, acc);
+  store_n<N, STREAM>(static_cast<TY*>(a.y) + (size_t)t * C + col, left, acc);
+}
+
+template <typename TR, typename TY, int N, bool STREAM>
+__global__ __launch_bounds__(ROW_THREADS) void combine_rows_kernel(RowsArgs a, int units, int tx_log, int nbx) {
+  int t, u;
+  row_pos(tx_log, nbx, t, u);
+  if (t >= a.T || u >= units) return;
+  const size_t col = (size_t)u * N;
+  const int left = a.C - (int)col;
+  if (left >= N) combine_columns<TR, TY, N, STREAM>(a, t, col, N);
+  else
+    for (int q = 0; q < left; ++q) combine_columns<TR, TY, 1, STREAM>(a, t, col + q, 1);
 }
 
 template <typename TR, typename TY>
 static void combine_go(const RowsArgs& a, hipStream_t st) {
   constexpr int N = 16 / sizeof(TR);
-  const bool vec = a.C % N == 0;
-  const int units = vec ? a.C / N : a.C;
+  const int units = (a.C + N - 1) / N;
   const RowGrid g = row_grid(units, a.T);
-  if (vec) combine_rows_kernel<TR, TY, N><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
-  else combine_rows_kernel<TR, TY, 1><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
+  if (streamed(a, sizeof(TR))) combine_rows_kernel<TR, TY, N, true><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
+  else combine_rows_kernel<TR, TY, N, false><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
 }
 
 hipError_t launch_combine_rows(const RowsArgs& a, int dtype, int y_dtype, hipStream_t st) {
@@ -321,9 +422,11 @@ hipError_t launch_combine_rows(const RowsArgs& a, int dtype, int y_dtype, hipStr
 // Gradients of combine for PG pairs of one token: drows[row_i] = w_i dy[t] and
 // dw_i = <dy[t], rows[row_i]>, so dy[t] is read once for PG rows.  One workgroup walks the
 // columns; the PG sums of each thread meet in LDS at the end.
-template <typename TR, typename TY, int N, int PG>
-__global__ __launch_bounds__(ROW_THREADS) void combine_rows_bwd_kernel(RowsArgs a) {
-  __shared__ float red[ROW_THREADS / 64][PG];
+constexpr int BWD_THREADS = 256;
+
+template <typename TR, typename TY, int N, int PG, bool STREAM>
+__global__ __launch_bounds__(BWD_THREADS) void combine_rows_bwd_kernel(RowsArgs a) {
+  __shared__ float red[BWD_THREADS / 64][PG];
   const int ng = (a.k + PG - 1) / PG;
   const int t = blockIdx.x / ng, i0 = (blockIdx.x % ng) * PG;
   const int k = a.k, P = a.T * k;
@@ -343,28 +446,38 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_rows_bwd_kernel(RowsArgs 
     w[i] = a.pair_w ? a.pair_w[(size_t)t * k + j] : 1.f;
     sum[i] = 0.f;
   }
-  for (int c = threadIdx.x * N; c < a.C; c += ROW_THREADS * N) {
-    float g[N];
-    load_n<N>(dy + c, g);
-    if (a.dw) {
-      float v[PG][N];
+  // W columns from c on: all loads first, then the sums, then the stores
+  auto columns = [&](auto width, auto with_dw, int c) {
+    constexpr int W = decltype(width)::value;
+    constexpr bool DW = decltype(with_dw)::value;
+    float g[W], v[PG][W];
+    load_n<W, STREAM>(dy + c, W, g);
+    if constexpr (DW) {
 #pragma unroll
-      for (int i = 0; i < PG; ++i) load_n<N>(rows + off[i] + c, v[i]);
+      for (int i = 0; i < PG; ++i) load_n<W, STREAM>(rows + off[i] + c, W, v[i]);
+      __builtin_amdgcn_sched_group_barrier(0x020, 2 * PG + 2, 0);
 #pragma unroll
       for (int i = 0; i < PG; ++i)
 #pragma unroll
-        for (int q = 0; q < N; ++q) sum[i] = fmaf(g[q], v[i][q], sum[i]);
+        for (int q = 0; q < W; ++q) sum[i] = fmaf(g[q], v[i][q], sum[i]);
     }
     if (drows) {
 #pragma unroll
       for (int i = 0; i < PG; ++i) {
-        float v[N];
+        float d[W];
 #pragma unroll
-        for (int q = 0; q < N; ++q) v[q] = w[i] * g[q];
-        if (ok[i]) store_n<N>(drows + off[i] + c, v);
+        for (int q = 0; q < W; ++q) d[q] = w[i] * g[q];
+        if (ok[i]) store_n<W, STREAM>(drows + off[i] + c, W, d);
       }
     }
-  }
+  };
+  auto all = [&](auto with_dw) {
+    for (int c = threadIdx.x * N; c + N <= a.C; c += BWD_THREADS * N) columns(std::integral_constant<int, N>{}, with_dw, c);
+    const int last = a.C / N * N + threadIdx.x;  // the columns behind the last N, one per thread
+    if (last < a.C) columns(std::integral_constant<int, 1>{}, with_dw, last);
+  };
+  if (a.dw) all(std::true_type{});
+  else all(std::false_type{});
   if (!a.dw) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -376,7 +489,7 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_rows_bwd_kernel(RowsArgs 
   if (threadIdx.x < PG && i0 + (int)threadIdx.x < k) {
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < ROW_THREADS / 64; ++v) s += red[v][threadIdx.x];
+    for (int v = 0; v < BWD_THREADS / 64; ++v) s += red[v][threadIdx.x];
     const size_t p = (size_t)t * k + i0 + threadIdx.x;
     a.dw[p] = (uint32_t)a.pair_row[p] < (uint32_t)P ? s : 0.f;  // (a dropped pair's weight moved nothing)
   }
@@ -385,16 +498,14 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_rows_bwd_kernel(RowsArgs 
 template <typename TR, typename TY>
 static void combine_bwd_go(const RowsArgs& a, hipStream_t st) {
   constexpr int N = 16 / sizeof(TR);
-  const bool vec = a.C % N == 0;
   // Eight pairs share one read of dy; a small batch takes one pair per workgroup instead,
   // so that it still fills the device.
   const bool wide = (long)a.T * ((a.k + 7) / 8) >= 512;
   const int ng = wide ? (a.k + 7) / 8 : a.k;
   const unsigned grid = (unsigned)a.T * (unsigned)ng;
-  if (vec && wide) combine_rows_bwd_kernel<TR, TY, N, 8><<<grid, ROW_THREADS, 0, st>>>(a);
-  else if (vec) combine_rows_bwd_kernel<TR, TY, N, 1><<<grid, ROW_THREADS, 0, st>>>(a);
-  else if (wide) combine_rows_bwd_kernel<TR, TY, 1, 8><<<grid, ROW_THREADS, 0, st>>>(a);
-  else combine_rows_bwd_kernel<TR, TY, 1, 1><<<grid, ROW_THREADS, 0, st>>>(a);
+  if (wide && streamed(a, sizeof(TR))) combine_rows_bwd_kernel<TR, TY, N, 8, true><<<grid, BWD_THREADS, 0, st>>>(a);
+  else if (wide) combine_rows_bwd_kernel<TR, TY, N, 8, false><<<grid, BWD_THREADS, 0, st>>>(a);
+  else combine_rows_bwd_kernel<TR, TY, N, 1, false><<<grid, BWD_THREADS, 0, st>>>(a);
 }
 
 hipError_t launch_combine_rows_backward(const RowsArgs& a, int dtype, int dy_dtype, hipStream_t st) {

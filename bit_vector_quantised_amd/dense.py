@@ -39,11 +39,12 @@ class _OnDevice:
         self.device = device
 
     def _call(self, fn, *args) -> None:
-        if torch.cuda.current_device() == self.device.index:
-            fn(*args, torch.cuda.current_stream(self.device).cuda_stream)
+        index = self.device.index
+        if torch.cuda.current_device() == index:
+            fn(*args, torch.cuda.current_stream(index).cuda_stream)
         else:
-            with torch.cuda.device(self.device):
-                fn(*args, torch.cuda.current_stream(self.device).cuda_stream)
+            with torch.cuda.device(index):
+                fn(*args, torch.cuda.current_stream(index).cuda_stream)
 
 
 class ExpertRows(_OnDevice):
