@@ -69,13 +69,11 @@ struct GemmArgs {
 // ---------------------------------------------------------------------------------------
 
 __device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); }
-__device__ __forceinline__ float sigmoid_fast(float z) { return 1.0f / (1.0f + __expf(-z)); }
+// (v_rcp_f32: within one unit in the last place)
+__device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
-// d silu(z) / dz = s + z s (1 - s)
-__device__ __forceinline__ float silu_grad(float z) {
-  const float s = sigmoid_fast(z);
-  return s * (1.0f + z * (1.0f - s));
-}
+// d silu(z) / dz = s + z s (1 - s), s = sigmoid(z)
+__device__ __forceinline__ float silu_grad(float z, float s) { return s * (1.0f + z * (1.0f - s)); }
 // d gelu(z) / dz = Phi(z) + z phi(z)
 __device__ __forceinline__ float gelu_grad(float z) {
   return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
@@ -140,19 +138,25 @@ __device__ __forceinline__ void load_n(const void* p, size_t i, int dtype, int n
     for (int j = 0; j < N; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
   }
 }
-template <int N>
+// STREAM: nontemporal stores, which leave the L2 to the operands that other tiles share.
+template <bool STREAM, typename V>
+__device__ __forceinline__ void store_vec(void* p, V v) {
+  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<V*>(p));
+  else *static_cast<V*>(p) = v;
+}
+template <int N, bool STREAM = false>
 __device__ __forceinline__ void store_n(void* p, size_t i, int dtype, int n, bool wide, const float* v) {
   if (N == 1) wide = false;
   if (wide && dtype == MOE_VQ_BF16) {
     uint16_t* to = static_cast<uint16_t*>(p) + i;
     if constexpr (N == 8)
-      *reinterpret_cast<uint4*>(to) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      store_vec<STREAM>(to, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
     else if constexpr (N == 4)
-      *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      store_vec<STREAM>(to, u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
   } else if (wide) {
 #pragma unroll
     for (int q = 0; q + 3 < N; q += 4)
-      *reinterpret_cast<float4*>(static_cast<float*>(p) + i + q) = make_float4(v[q], v[q + 1], v[q + 2], v[q + 3]);
+      store_vec<STREAM>(static_cast<float*>(p) + i + q, f32x4_t{v[q], v[q + 1], v[q + 2], v[q + 3]});
   } else {
 #pragma unroll
     for (int j = 0; j < N; ++j)
@@ -163,7 +167,7 @@ __device__ __forceinline__ void store_n(void* p, size_t i, int dtype, int n, boo
 // Epilogue of N consecutive output columns n.. of output row m: bias, z, activation, residual, one
 // rounding to the output's type.  v: the sums (SWIGLU: the gate's), u: the up sums.  z keeps the
 // values before the activation, rounded once to its type.  wide: out_n is a multiple of N.
-template <bool GATED, int N>
+template <bool GATED, int N, bool STREAM = false>
 __device__ __forceinline__ void epilogue(const GemmArgs& g, int grp, size_t m, int n, bool wide, float* v, float* u) {
   const int left = g.ldo - n;
   const size_t wrows = GATED ? 2 * (size_t)g.ldo : (size_t)g.ldo;
@@ -178,8 +182,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, int grp, size_t m, i
     }
   }
   if (g.z) {
-    store_n<N>(g.z, m * wrows + n, g.z_dtype, left, wide, v);
-    if (GATED) store_n<N>(g.z, m * wrows + g.ldo + n, g.z_dtype, left, wide, u);
+    store_n<N, STREAM>(g.z, m * wrows + n, g.z_dtype, left, wide, v);
+    if (GATED) store_n<N, STREAM>(g.z, m * wrows + g.ldo + n, g.z_dtype, left, wide, u);
   }
   if (GATED) {
 #pragma unroll
@@ -198,7 +202,7 @@ __device__ __forceinline__ void epilogue(const GemmArgs& g, int grp, size_t m, i
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] += r[j];
   }
-  store_n<N>(g.out, at, g.out_dtype, left, wide, v);
+  store_n<N, STREAM>(g.out, at, g.out_dtype, left, wide, v);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -259,12 +263,13 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // One operand of a tile: B rows of output space (ALONG) or B columns (across), loaded by NW waves.
-template <typename E, int B, bool ALONG, int NW>
+template <typename E, int B, bool ALONG, int NW, int KB>
 struct Operand {
-  static constexpr int BYTES = B * STEP_BYTES;
+  static_assert(!ALONG || KB == STEP_BYTES, "an along operand is loaded by whole cache lines");
+  static constexpr int BYTES = B * KB;
   static constexpr int LOADS = BYTES / 1024 / NW;     // 1 KiB per wave and load
   static constexpr int ROWB = B * E::SIZE;            // bytes of an across row
-  static constexpr int KT = STEP_BYTES / E::SIZE;     // contraction values per step
+  static constexpr int KT = KB / E::SIZE;             // contraction values per step
   static constexpr int READS = ALONG ? 1 : E::SIZE;   // LDS reads of a matrix operand (2 of bf16, 4 of fp32 across)
   static_assert(LOADS >= 1 && LOADS * NW * 1024 == BYTES, "loads divide evenly over the waves");
   uint64_t base;    // address of this step's first byte
@@ -345,16 +350,16 @@ struct Operand {
   }
 };
 
-template <typename E, int BM, int BN, int WM, int WN, int NS, int MODE>
+template <typename E, int BM, int BN, int WM, int WN, int NS, int KB, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   constexpr int NW = WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  using OpA = Operand<E, BM, MODE != GEMM_DW, NW>;
+  using OpA = Operand<E, BM, MODE != GEMM_DW, NW, KB>;
   constexpr bool GATED = MODE == GEMM_GATED, FORWARD = MODE == GEMM_FWD || GATED;
   static_assert(!GATED || FN % 2 == 0, "a wave holds gate and up of its columns");
-  using OpB = Operand<E, BN, FORWARD, NW>;
+  using OpB = Operand<E, BN, FORWARD, NW, KB>;
   constexpr int KT = OpA::KT;
-  constexpr int STAGE = (BM + BN) * STEP_BYTES;
+  constexpr int STAGE = (BM + BN) * KB;
   __shared__ __align__(1024) char lds_mem[NS * STAGE];
   lds_char* lds = (lds_char*)lds_mem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -477,14 +482,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   // One step on `units` units of Q row operands, as a software pipeline: the next unit's reads of LDS go
   // out before this unit's matrix instructions.
   auto multiply = [&](auto live_units, const lds_char* at) {
-    constexpr int U = decltype(live_units)::value;
+    constexpr int U = decltype(live_units)::value, HALVES = KB / 64;  // (a matrix instruction takes 64 bytes of a row)
     u32x4_t fa[2][Q], fb[2][FN];
     static_for<0, FN>([&](auto j) { fb[0][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, 0, lane); });
     static_for<0, Q>([&](auto i) { fa[0][i] = OpA::frag(at, i * WM + wm, 0, lane); });
     __builtin_amdgcn_sched_group_barrier(0x100, FN * OpB::READS + Q * OpA::READS, 0);
-    static_for<0, 2 * U>([&](auto uu) {
+    static_for<0, HALVES * U>([&](auto uu) {
       constexpr int u = decltype(uu)::value, h = u / U, q = u % U, n = u + 1, nh = n / U, nq = n % U;
-      if constexpr (n < 2 * U) {
+      if constexpr (n < HALVES * U) {
         if constexpr (nq == 0) static_for<0, FN>([&](auto j) { fb[nh][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, nh, lane); });
         static_for<0, Q>([&](auto i) { fa[n & 1][i] = OpA::frag(at, (nq * Q + i) * WM + wm, nh, lane); });
         __builtin_amdgcn_sched_group_barrier(0x100, (nq == 0 ? FN * OpB::READS : 0) + Q * OpA::READS, 0);
@@ -516,6 +521,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   constexpr int PITCH = FN * 16 + 4;
   constexpr int COLS = GATED ? FN * 8 : FN * 16;  // output columns of the wave
   static_assert(NW * 2 * 16 * PITCH * 4 <= (int)sizeof(lds_mem), "output staging");
+  // The largest tiles' outputs exceed the L2s many times over: streamed, dw of 16 experts' 512 rows each takes
+  // 779 us instead of 924, and 8192^3 reaches 1256 (dx) and 1212 TFLOP/s (dw) instead of 1152 and 1112.
+  constexpr bool STREAM = BM * BN >= 256 * 256;
   float* stage = reinterpret_cast<float*>(lds_mem) + wave * 2 * 16 * PITCH;
   const size_t out_rows = MODE == GEMM_DW ? (size_t)g.G * g.out_m : (size_t)g.M;
   const size_t out_cols = GATED ? 2 * (size_t)g.out_n : (size_t)g.out_n;
@@ -544,9 +552,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
       store_n<N>(p, n, MOE_VQ_F32, g.out_n - n, wide, v);
       if (GATED) store_n<N>(p, (size_t)g.out_n + n, MOE_VQ_F32, g.out_n - n, wide, u);
     } else if (FORWARD) {
-      epilogue<GATED, N>(g, grp, row, n, wide, v, u);
+      epilogue<GATED, N, STREAM>(g, grp, row, n, wide, v, u);
     } else {
-      store_n<N>(g.out, row * (size_t)g.ldo + n, E::DTYPE, g.out_n - n, wide, v);
+      store_n<N, STREAM>(g.out, row * (size_t)g.ldo + n, E::DTYPE, g.out_n - n, wide, v);
     }
   };
   static_for<0, FM>([&](auto fi) {
@@ -709,7 +717,7 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
     if (a.act == MOE_VQ_ACT_NONE) {
       d[0][j] = dy[j];
     } else if (a.act == MOE_VQ_ACT_SILU) {
-      d[0][j] = dy[j] * silu_grad(zg[j]);
+      d[0][j] = dy[j] * silu_grad(zg[j], sigmoid_fast(zg[j]));
     } else if (a.act == MOE_VQ_ACT_GELU) {
       d[0][j] = dy[j] * gelu_grad(zg[j]);
     } else {
@@ -722,8 +730,9 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
         gv = gin ? gv : a.lim;
         uv = uv > a.lim ? a.lim : (uv < -a.lim ? -a.lim : uv);
       }
-      d[0][j] = gin ? dy[j] * uv * silu_grad(gv) : 0.f;
-      d[1][j] = uin ? dy[j] * silu_fast(gv) : 0.f;
+      const float sg = sigmoid_fast(gv);
+      d[0][j] = gin ? dy[j] * uv * silu_grad(gv, sg) : 0.f;
+      d[1][j] = uin ? dy[j] * gv * sg : 0.f;
     }
   }
 }
@@ -845,7 +854,7 @@ Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool split
 
 int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 
-template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS>
+template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS, int KB = STEP_BYTES>
 void gemm_go(const GemmArgs& g, hipStream_t st) {
   const int per_n = MODE == GEMM_GATED ? BN / 2 : BN;
   const long nt = div_up(g.out_n, per_n);
@@ -853,7 +862,7 @@ void gemm_go(const GemmArgs& g, hipStream_t st) {
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
   const long grid = nt * mt * g.splits;
-  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
+  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, KB, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
 }
 
 template <int MODE>

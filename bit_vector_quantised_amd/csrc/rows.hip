@@ -283,38 +283,37 @@ __device__ __forceinline__ void store_n(float* p, int left, const float* v) {
   }
 }
 
-// 128 threads: for 4096 tokens of 7168 columns, top-8, gather takes 94 us (256 threads: 99, 512: 106)
-// and combine 97 (106, 122).
-constexpr int ROW_THREADS = 128, ROW_THREADS_LOG = 7;
-
 // Rows of more bytes than the memory-side cache holds are streamed: gather 94 us instead of 105,
 // combine 97 instead of 109 (470 MB of rows); smaller ones stay where the next kernel finds them.
+// Streamed rows are fastest with workgroups of 128 threads (gather 94 us, 256 threads 99; combine 97, 106),
+// rows that a cache holds with 256 (combine of 1021 tokens of 2047 fp32 columns, top-6: 15 us, 22 with 128).
+constexpr int row_threads_log(bool stream) { return stream ? 7 : 8; }
 static bool streamed(const RowsArgs& a, size_t size) { return (size_t)a.T * a.k * a.C * size > ((size_t)256 << 20); }
 
 // Units of a row over a workgroup's threads: TX of them side by side on one token (a power
-// of two, so a narrow row does not leave lanes idle), ROW_THREADS / TX tokens.
+// of two, so a narrow row does not leave lanes idle), and the other threads on other tokens.
 struct RowGrid {
   int tx_log, nbx;
   unsigned grid;
 };
-static RowGrid row_grid(int units, int T) {
+static RowGrid row_grid(int units, int T, bool stream) {
   RowGrid g{};
-  while (g.tx_log < ROW_THREADS_LOG && (1 << g.tx_log) < units) ++g.tx_log;
+  while (g.tx_log < row_threads_log(stream) && (1 << g.tx_log) < units) ++g.tx_log;
   g.nbx = (units + (1 << g.tx_log) - 1) >> g.tx_log;
-  const int ty = ROW_THREADS >> g.tx_log;
+  const int ty = 1 << (row_threads_log(stream) - g.tx_log);
   g.grid = (unsigned)g.nbx * (unsigned)((T + ty - 1) / ty);
   return g;
 }
 __device__ __forceinline__ void row_pos(int tx_log, int nbx, int& t, int& u) {
   const int bx = blockIdx.x % nbx, bt = blockIdx.x / nbx;
-  t = bt * (ROW_THREADS >> tx_log) + ((int)threadIdx.x >> tx_log);
+  t = bt * ((int)blockDim.x >> tx_log) + ((int)threadIdx.x >> tx_log);
   u = (bx << tx_log) + ((int)threadIdx.x & ((1 << tx_log) - 1));
 }
 
 // xs[row(t,i)] = x[t] for the token's k pairs, 16 bytes per thread (the row's last ones by element).  Bound by
 // the k row writes; the token's row is read once.
 template <bool STREAM>
-__global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowsArgs a, size_t bytes, int units, int tx_log, int nbx) {
+__global__ __launch_bounds__(1 << row_threads_log(STREAM)) void gather_kernel(RowsArgs a, size_t bytes, int units, int tx_log, int nbx) {
   int t, u;
   row_pos(tx_log, nbx, t, u);
   if (t >= a.T || u >= units) return;
@@ -343,9 +342,13 @@ __global__ __launch_bounds__(ROW_THREADS) void gather_kernel(RowsArgs a, size_t 
 hipError_t launch_gather(const RowsArgs& a, int dtype, hipStream_t st) {
   const size_t bytes = (size_t)a.C * (dtype == MOE_VQ_BF16 ? 2 : 4);
   const int units = (int)((bytes + 15) / 16);
-  const RowGrid g = row_grid(units, a.T);
-  if (streamed(a, bytes / a.C)) gather_kernel<true><<<g.grid, ROW_THREADS, 0, st>>>(a, bytes, units, g.tx_log, g.nbx);
-  else gather_kernel<false><<<g.grid, ROW_THREADS, 0, st>>>(a, bytes, units, g.tx_log, g.nbx);
+  auto go = [&](auto stream) {
+    constexpr bool S = decltype(stream)::value;
+    const RowGrid g = row_grid(units, a.T, S);
+    gather_kernel<S><<<g.grid, 1 << row_threads_log(S), 0, st>>>(a, bytes, units, g.tx_log, g.nbx);
+  };
+  if (streamed(a, bytes / a.C)) go(std::true_type{});
+  else go(std::false_type{});
   return hipGetLastError();
 }
 
@@ -388,7 +391,7 @@ __device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t
 }
 
 template <typename TR, typename TY, int N, bool STREAM>
-__global__ __launch_bounds__(ROW_THREADS) void combine_rows_kernel(RowsArgs a, int units, int tx_log, int nbx) {
+__global__ __launch_bounds__(1 << row_threads_log(STREAM)) void combine_rows_kernel(RowsArgs a, int units, int tx_log, int nbx) {
   int t, u;
   row_pos(tx_log, nbx, t, u);
   if (t >= a.T || u >= units) return;
@@ -403,9 +406,13 @@ template <typename TR, typename TY>
 static void combine_go(const RowsArgs& a, hipStream_t st) {
   constexpr int N = 16 / sizeof(TR);
   const int units = (a.C + N - 1) / N;
-  const RowGrid g = row_grid(units, a.T);
-  if (streamed(a, sizeof(TR))) combine_rows_kernel<TR, TY, N, true><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
-  else combine_rows_kernel<TR, TY, N, false><<<g.grid, ROW_THREADS, 0, st>>>(a, units, g.tx_log, g.nbx);
+  auto go = [&](auto stream) {
+    constexpr bool S = decltype(stream)::value;
+    const RowGrid g = row_grid(units, a.T, S);
+    combine_rows_kernel<TR, TY, N, S><<<g.grid, 1 << row_threads_log(S), 0, st>>>(a, units, g.tx_log, g.nbx);
+  };
+  if (streamed(a, sizeof(TR))) go(std::true_type{});
+  else go(std::false_type{});
 }
 
 hipError_t launch_combine_rows(const RowsArgs& a, int dtype, int y_dtype, hipStream_t st) {
