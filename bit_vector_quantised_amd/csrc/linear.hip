@@ -108,101 +108,85 @@ __device__ __forceinline__ void store_as(void* p, size_t i, int dtype, float v) 
   if (dtype == MOE_VQ_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16_rne(v);
   else static_cast<float*>(p)[i] = v;
 }
-// N consecutive values (1, 4 or 8) from index i, the first `n` of them valid.  wide: all are, and i is a
-// multiple of N, so that they go as one or two accesses.
-template <int N>
-__device__ __forceinline__ void load_n(const void* p, size_t i, int dtype, int n, bool wide, float* v) {
-  if (N == 1) wide = false;
-  if (wide && dtype == MOE_VQ_BF16) {
-    uint32_t w[N == 1 ? 1 : N / 2];
-    if constexpr (N == 8) {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
-      w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-    } else if constexpr (N == 4) {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-      w[0] = u.x; w[1] = u.y;
-    }
+// Eight consecutive values from index i, the first `n` of them valid: as one or two accesses where all are.
+__device__ __forceinline__ void load8(const void* p, size_t i, int dtype, int n, float* v) {
+  if (n >= 8 && dtype == MOE_VQ_BF16) {
+    const u32x4_any u = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int q = 0; q < N / 2; ++q) {
+    for (int q = 0; q < 4; ++q) {
       v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu);
       v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u);
     }
-  } else if (wide) {
+  } else if (n >= 8) {
 #pragma unroll
-    for (int q = 0; q + 3 < N; q += 4) {
-      const float4 u = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i + q);
+    for (int q = 0; q < 8; q += 4) {
+      const f32x4_any u = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i + q);
       v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
+    for (int j = 0; j < 8; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
   }
 }
 // STREAM: nontemporal stores, which leave the L2 to the operands that other tiles share.
-template <bool STREAM, typename V>
-__device__ __forceinline__ void store_vec(void* p, V v) {
-  if constexpr (STREAM) __builtin_nontemporal_store(v, static_cast<V*>(p));
-  else *static_cast<V*>(p) = v;
-}
-template <int N, bool STREAM = false>
-__device__ __forceinline__ void store_n(void* p, size_t i, int dtype, int n, bool wide, const float* v) {
-  if (N == 1) wide = false;
-  if (wide && dtype == MOE_VQ_BF16) {
-    uint16_t* to = static_cast<uint16_t*>(p) + i;
-    if constexpr (N == 8)
-      store_vec<STREAM>(to, u32x4_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
-    else if constexpr (N == 4)
-      store_vec<STREAM>(to, u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
-  } else if (wide) {
+template <bool STREAM = false>
+__device__ __forceinline__ void store8(void* p, size_t i, int dtype, int n, const float* v) {
+  if (n >= 8 && dtype == MOE_VQ_BF16) {
+    store_vec<STREAM>(reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i),
+                      u32x4_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
+  } else if (n >= 8) {
 #pragma unroll
-    for (int q = 0; q + 3 < N; q += 4)
-      store_vec<STREAM>(static_cast<float*>(p) + i + q, f32x4_t{v[q], v[q + 1], v[q + 2], v[q + 3]});
+    for (int q = 0; q < 8; q += 4)
+      store_vec<STREAM>(reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i + q), f32x4_any{v[q], v[q + 1], v[q + 2], v[q + 3]});
   } else {
 #pragma unroll
-    for (int j = 0; j < N; ++j)
+    for (int j = 0; j < 8; ++j)
       if (j < n) store_as(p, i + j, dtype, v[j]);
   }
 }
 
-// Epilogue of N consecutive output columns n.. of output row m: bias, z, activation, residual, one
+// Epilogue of eight consecutive output columns n.. of output row m: bias, z, activation, residual, one
 // rounding to the output's type.  v: the sums (SWIGLU: the gate's), u: the up sums.  z keeps the
-// values before the activation, rounded once to its type.  wide: out_n is a multiple of N.
-template <bool GATED, int N, bool STREAM = false>
-__device__ __forceinline__ void epilogue(const GemmArgs& g, int grp, size_t m, int n, bool wide, float* v, float* u) {
+// values before the activation, rounded once to its type.
+template <bool GATED, bool STREAM = false>
+__device__ __forceinline__ void epilogue8(const GemmArgs& g, int grp, size_t m, int n, float* v, float* u) {
   const int left = g.ldo - n;
   const size_t wrows = GATED ? 2 * (size_t)g.ldo : (size_t)g.ldo;
   if (g.bias) {
     const float* b = g.bias + grp * wrows;
+    float t[8];
+    load8(b, n, MOE_VQ_F32, left, t);
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      if (j < left) {
-        v[j] += b[n + j];
-        if (GATED) u[j] += b[(size_t)g.ldo + n + j];
-      }
+    for (int j = 0; j < 8; ++j) v[j] += t[j];
+    if (GATED) {
+      load8(b, (size_t)g.ldo + n, MOE_VQ_F32, left, t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] += t[j];
     }
   }
   if (g.z) {
-    store_n<N, STREAM>(g.z, m * wrows + n, g.z_dtype, left, wide, v);
-    if (GATED) store_n<N, STREAM>(g.z, m * wrows + g.ldo + n, g.z_dtype, left, wide, u);
+    store8<STREAM>(g.z, m * wrows + n, g.z_dtype, left, v);
+    if (GATED) store8<STREAM>(g.z, m * wrows + g.ldo + n, g.z_dtype, left, u);
   }
   if (GATED) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = swiglu(v[j], u[j], g.lim);
+    for (int j = 0; j < 8; ++j) v[j] = swiglu(v[j], u[j], g.lim);
   } else if (g.act == MOE_VQ_ACT_SILU) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = silu_fast(v[j]);
+    for (int j = 0; j < 8; ++j) v[j] = silu_fast(v[j]);
   } else if (g.act == MOE_VQ_ACT_GELU) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = gelu(v[j]);
+    for (int j = 0; j < 8; ++j) v[j] = gelu(v[j]);
   }
   const size_t at = m * (size_t)g.ldo + n;
   if (g.res) {
-    float r[N];
-    load_n<N>(g.res, at, g.out_dtype, left, wide, r);
+    float r[8];
+    load8(g.res, at, g.out_dtype, left, r);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] += r[j];
+    for (int j = 0; j < 8; ++j) v[j] += r[j];
   }
-  store_n<N, STREAM>(g.out, at, g.out_dtype, left, wide, v);
+  store8<STREAM>(g.out, at, g.out_dtype, left, v);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -527,17 +511,17 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   float* stage = reinterpret_cast<float*>(lds_mem) + wave * 2 * 16 * PITCH;
   const size_t out_rows = MODE == GEMM_DW ? (size_t)g.G * g.out_m : (size_t)g.M;
   const size_t out_cols = GATED ? 2 * (size_t)g.out_n : (size_t)g.out_n;
-  // N columns of local row rr (of 16) from local column c
-  auto put = [&](auto width, const float* part, int i, int t, bool wide) {
-    constexpr int N = decltype(width)::value, PER = COLS / N;
-    const int rr = t / PER, c = (t % PER) * N;
+  // eight columns of the 16 rows: unit t of row block i
+  auto put = [&](const float* part, int i, int t) __attribute__((always_inline)) {
+    constexpr int PER = COLS / 8;
+    const int rr = t / PER, c = (t % PER) * 8;
     const int m = m0 + (i * WM + wm) * 16 + rr, n = n0 + wn * COLS + c;
     if (m >= m_end || n >= g.out_n) return;
     const size_t row = MODE == GEMM_DW ? (size_t)grp * g.out_m + m : (size_t)m;
     const float* from = part + rr * PITCH + (GATED ? (c >> 4) * 32 + (c & 15) : c);
-    float v[N], u[N];
+    float v[8], u[8];
 #pragma unroll
-    for (int q = 0; q < N; q += 4) {
+    for (int q = 0; q < 8; q += 4) {
       const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(from + q);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[q + j] = lo[j];
@@ -549,15 +533,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     }
     if (g.splits > 1) {
       float* p = g.part + ((size_t)split * out_rows + row) * out_cols;
-      store_n<N>(p, n, MOE_VQ_F32, g.out_n - n, wide, v);
-      if (GATED) store_n<N>(p, (size_t)g.out_n + n, MOE_VQ_F32, g.out_n - n, wide, u);
+      store8(p, n, MOE_VQ_F32, g.out_n - n, v);
+      if (GATED) store8(p, (size_t)g.out_n + n, MOE_VQ_F32, g.out_n - n, u);
     } else if (FORWARD) {
-      epilogue<GATED, N, STREAM>(g, grp, row, n, wide, v, u);
+      epilogue8<GATED, STREAM>(g, grp, row, n, v, u);
     } else {
-      store_n<N, STREAM>(g.out, row * (size_t)g.ldo + n, E::DTYPE, g.out_n - n, wide, v);
+      store8<STREAM>(g.out, row * (size_t)g.ldo + n, E::DTYPE, g.out_n - n, v);
     }
   };
-  static_for<0, FM>([&](auto fi) {
+  static_for<0, FM>([&](auto fi) __attribute__((always_inline)) {
     constexpr int i = decltype(fi)::value;
     if (i >= live) return;
     float* part = stage + (i & 1) * 16 * PITCH;
@@ -569,14 +553,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    if ((g.out_n & 7) == 0) {
 #pragma unroll
-      for (int t = 0; t < 16 * COLS / 8; t += 64)
-        if (16 * COLS / 8 >= 64 || lane < 16 * COLS / 8) put(std::integral_constant<int, 8>{}, part, i, t + lane, true);
-    } else {
-#pragma unroll 1
-      for (int t = lane; t < 16 * COLS / 4; t += 64) put(std::integral_constant<int, 4>{}, part, i, t, (g.out_n & 3) == 0);
-    }
+    for (int t = 0; t < 16 * COLS / 8; t += 64)
+      if (16 * COLS / 8 >= 64 || lane < 16 * COLS / 8) put(part, i, t + lane);
   });
 }
 
@@ -634,48 +613,64 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(GemmArgs g) {
   // lane (i, q) holds row i of x, weight rows 4 q .. of the 16
   *reinterpret_cast<f32x4_t*>(&red[wave][i][q * 4]) = acc;
   __syncthreads();
-  const int m = threadIdx.x / (PER / 4), c = (threadIdx.x % (PER / 4)) * 4;
+  const int m = threadIdx.x / (PER / 8), c = (threadIdx.x % (PER / 8)) * 8;
   if (m < g.M && n0 + c < g.out_n) {
-    float v[4] = {0.f, 0.f, 0.f, 0.f}, up[4] = {0.f, 0.f, 0.f, 0.f};
+    float v[8], up[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = up[j] = 0.f;
 #pragma unroll
     for (int k = 0; k < FEW_WAVES; ++k) {
-      const f32x4_t p = *reinterpret_cast<const f32x4_t*>(&red[k][m][c]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += p[j];
-      if (GATED) {
-        const f32x4_t pu = *reinterpret_cast<const f32x4_t*>(&red[k][m][8 + c]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) up[j] += pu[j];
+      for (int j = 0; j < 8; ++j) {
+        v[j] += red[k][m][c + j];
+        if (GATED) up[j] += red[k][m][8 + c + j];
       }
     }
-    epilogue<GATED, 4>(g, 0, m, n0 + c, (g.ldo & 3) == 0, v, up);
+    epilogue8<GATED>(g, 0, m, n0 + c, v, up);
   }
 }
 
-// The sum of the splits' parts in order, then the epilogue: four columns per thread.
-template <bool GATED>
+// The group whose rows hold row m, or -1: the last one that starts at or before it, if it reaches that far.
+__device__ __forceinline__ int group_of(const GemmArgs& g, int m) {
+  if (!g.group_start) return 0;
+  int lo = 0, hi = g.G;  // (group_start[lo] <= m < group_start[hi] inside the table)
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (g.group_start[mid] <= m) lo = mid;
+    else hi = mid;
+  }
+  return g.group_start[lo] <= m && m < g.group_start[lo + 1] ? lo : -1;
+}
+
+// The sum of the splits' parts in order, then the epilogue: eight columns per thread.  ROWS: of forward or dx,
+// whose rows in no group have no sums and are left as they were.
+template <bool GATED, bool ROWS>
 __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
-  const int units = (g.ldo + 3) / 4;
+  const int units = (g.ldo + 7) / 8;
   const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
   if (at >= (size_t)rows * units) return;
   const size_t m = at / units;
-  const int n = (int)(at - m * units) * 4, left = g.ldo - n;
+  const int n = (int)(at - m * units) * 8, left = g.ldo - n;
+  const int grp = ROWS ? group_of(g, (int)m) : 0;
+  if (grp < 0) return;
   const size_t cols = GATED ? 2 * (size_t)g.ldo : (size_t)g.ldo;
-  const bool wide = (g.ldo & 3) == 0;
-  float v[4] = {0.f, 0.f, 0.f, 0.f}, u[4] = {0.f, 0.f, 0.f, 0.f};
+  float v[8], u[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.f;
+#pragma unroll 2
   for (int s = 0; s < g.splits; ++s) {
     const float* p = g.part + ((size_t)s * rows + m) * cols;
-    float t[4];
-    load_n<4>(p, n, MOE_VQ_F32, left, wide, t);
+    float t[8];
+    load8(p, n, MOE_VQ_F32, left, t);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] += t[j];
+    for (int j = 0; j < 8; ++j) v[j] += t[j];
     if (GATED) {
-      load_n<4>(p, (size_t)g.ldo + n, MOE_VQ_F32, left, wide, t);
+      load8(p, (size_t)g.ldo + n, MOE_VQ_F32, left, t);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) u[j] += t[j];
+      for (int j = 0; j < 8; ++j) u[j] += t[j];
     }
   }
-  epilogue<GATED, 4>(g, 0, m, n, wide, v, u);
+  epilogue8<GATED>(g, grp, m, n, v, u);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -708,11 +703,10 @@ struct DzArgs {
 
 constexpr int DZ_TX = 32, DZ_TY = 8;  // threads over columns, over rows
 
-// dz of V columns of one row: the gate's (or the only) factor in d[0], the up's in d[1].
-template <int V>
-__device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, const float* zg, const float* zu, float (*d)[V]) {
+// dz of eight columns of one row: the gate's (or the only) factor in d[0], the up's in d[1].
+__device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, const float* zg, const float* zu, float (*d)[8]) {
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
+  for (int j = 0; j < 8; ++j) {
     d[1][j] = 0.f;
     if (a.act == MOE_VQ_ACT_NONE) {
       d[0][j] = dy[j];
@@ -737,15 +731,14 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
   }
 }
 
-// One workgroup: DZ_TX * V columns of one split of one group's rows, two rows of a thread at a time (their loads are
+// One workgroup: 8 DZ_TX columns of one split of one group's rows, two rows of a thread at a time (their loads are
 // issued together).  Bound by reading dy and z and writing dz, each once.  dz is rounded to the
 // element type for the matrix products; the column sums add the unrounded values in fp32, rows in a
 // fixed order.
-template <int V>
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
-  __shared__ float red[DZ_TY][2][DZ_TX * V];
+  __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
-  const int n = (blockIdx.x * DZ_TX + tx) * V;
+  const int n = (blockIdx.x * DZ_TX + tx) * 8;
   const int grp = blockIdx.y, split = blockIdx.z;
   int r0 = 0, r1 = a.M;
   if (a.group_start) {
@@ -756,7 +749,8 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   const int per = (r1 - r0 + a.splits - 1) / a.splits;
   const int m0 = r0 + split * per, m1 = m0 + per < r1 ? m0 + per : r1;
   const bool two = a.act == MOE_VQ_ACT_SWIGLU, any = a.act != MOE_VQ_ACT_NONE;
-  constexpr bool WIDE = V > 1;
+  constexpr int V = 8;
+  const int left = a.N - n;
   float sum[2][V];
 #pragma unroll
   for (int j = 0; j < V; ++j) sum[0][j] = sum[1][j] = 0.f;
@@ -765,8 +759,8 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
     for (int j = 0; j < V; ++j) { sum[0][j] += d[0][j]; sum[1][j] += d[1][j]; }
     if (!a.dz) return;
     const size_t row = (size_t)m * a.pitch;
-    store_n<V>(a.dz, row + n, a.dtype, V, WIDE, d[0]);
-    if (two) store_n<V>(a.dz, row + a.N + n, a.dtype, V, WIDE, d[1]);
+    store8(a.dz, row + n, a.dtype, left, d[0]);
+    if (two) store8(a.dz, row + a.N + n, a.dtype, left, d[1]);
     // (the pitch's last columns take part in dx's contraction as zeros)
     if (n == 0)
       for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, a.dtype, 0.f);
@@ -778,12 +772,12 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const size_t r = i ? next : m;
-        load_n<V>(a.dy, r * a.N + n, a.dy_dtype, V, WIDE, dy[i]);
-        if (any) load_n<V>(a.z, r * a.R + n, a.dtype, V, WIDE, zg[i]);
-        if (two) load_n<V>(a.z, r * a.R + a.N + n, a.dtype, V, WIDE, zu[i]);
+        load8(a.dy, r * a.N + n, a.dy_dtype, left, dy[i]);
+        if (any) load8(a.z, r * a.R + n, a.dtype, left, zg[i]);
+        if (two) load8(a.z, r * a.R + a.N + n, a.dtype, left, zu[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) dz_values<V>(a, dy[i], zg[i], zu[i], d[i]);
+      for (int i = 0; i < 2; ++i) dz_values(a, dy[i], zg[i], zu[i], d[i]);
       put(m, d[0]);
       if (m + DZ_TY < m1) put(next, d[1]);
     }
@@ -802,7 +796,7 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
       float s = 0.f;
 #pragma unroll
       for (int y = 0; y < DZ_TY; ++y) s += red[y][ty][tx * V + j];
-      out[j] = s;
+      if (j < left) out[j] = s;
     }
   }
 }
@@ -831,25 +825,41 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float* part, float*
 using Cut = LinearPlan::Cut;
 constexpr int CUS = 256;
 
-// How a product is cut.  rows: output rows in all, of `groups` groups; cols: output columns (weight rows forward); steps: contraction steps;
-// split: whether the contraction may be split.
-//  - 256 x 256 tiles, one workgroup per CU, where they nearly fill the device: 1390 TFLOP/s at 8192^3 where
-//    128 x 128 tiles, which read LDS twice as often for their products, reach 1150.
-//  - 128 x 128, two workgroups per CU, if they fill it, or fill it once the contraction is split
-//    (eight steps per part at least: a part of a tile costs a write and a read of its sums).
-//  - 64 x 64 for what is left: small outputs and short contractions, and at most 64 rows, which
-//    leave more of a larger tile empty than they save.
-Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool split) {
+// A kind of tile: its side, how many workgroups of it a CU holds, and what a workgroup takes (microseconds, measured): per
+// contraction step with its CU full, per step if it has the CU to itself, and before and after them.
+struct TileKind {
+  int side, per_cu;
+  float step, step_alone, rest;
+};
+constexpr TileKind BF16_TILES[] = {{256, 1, 1.95f, 1.95f, 8.f}, {128, 2, 1.2f, 0.8f, 6.f}, {64, 2, 0.6f, 0.45f, 5.f}};
+constexpr TileKind F32_TILES[] = {{128, 2, 3.9f, 2.1f, 6.f}, {64, 2, 1.0f, 0.6f, 5.f}};
+
+// How a product is cut.  rows: output rows in all, of `groups` groups; cols: output columns (weight rows forward);
+// steps: contraction steps.  The cut with the smallest estimate is taken: rounds of workgroups over the device, times a workgroup's time, and for a split
+// contraction the write and read of its parts (from the caches: 10 TB/s) and one more launch.  Large
+// products so take 256 x 256 tiles (1400 TFLOP/s at 8192^3, 128 x 128 tiles, which read LDS twice as
+// often for their products, 1150) unless the last round would be nearly empty; small outputs with
+// long contractions are split, and outputs too small for that take small tiles.
+Cut pick_cut(int dtype, long rows, long groups, long cols, int steps) {
   const long per = (rows + groups - 1) / groups;
-  auto tiles = [&](long t) { return (per + t - 1) / t * groups * ((cols + t - 1) / t); };
-  auto parts = [&](long n) {
-    const long s = n < 1 ? 1 : 2 * CUS / n;
-    const long most = steps / 8;
-    return !split || s < 2 || most < 2 ? 1 : (int)(s < most ? (s < 32 ? s : 32) : (most < 32 ? most : 32));
+  Cut best{64, 1};
+  float least = 3.0e38f;
+  auto consider = [&](const TileKind& k) {
+    const long tiles = (per + k.side - 1) / k.side * groups * ((cols + k.side - 1) / k.side);
+    for (int parts = 1; parts <= 32; parts *= 2) {
+      // (at most two workgroups per CU are split ones, of at least four steps)
+      if (parts > 1 && (k.side > 128 || tiles * parts > 2 * CUS || steps < 4 * parts)) break;
+      const long n = tiles * parts, slots = (long)k.per_cu * CUS;
+      const float rounds = n <= slots ? 1.f : (n < 3 * slots ? (float)((n + slots - 1) / slots) : (float)n / slots + 0.5f);
+      const int each = (steps + parts - 1) / parts;
+      float t = rounds * (each * (n <= CUS ? k.step_alone : k.step) + k.rest);
+      if (parts > 1) t += 3.f + 8.f * parts * rows * cols / 10.0e6f;
+      if (t < least) { least = t; best = {k.side, parts}; }
+    }
   };
-  if (dtype == MOE_VQ_BF16 && per >= 192 && tiles(256) >= 200) return {256, 1};
-  if (per > 64 && tiles(128) * parts(tiles(128)) >= CUS) return {128, parts(tiles(128))};
-  return {64, parts(tiles(64))};
+  if (dtype == MOE_VQ_BF16) for (const TileKind& k : BF16_TILES) consider(k);
+  else for (const TileKind& k : F32_TILES) consider(k);
+  return best;
 }
 
 int div_up(long a, long b) { return (int)((a + b - 1) / b); }
@@ -877,8 +887,8 @@ hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t s
   }
   if (g.splits > 1) {
     const int rows = MODE == GEMM_DW ? g.G * g.out_m : g.M;
-    const size_t n = (size_t)rows * ((g.ldo + 3) / 4);
-    split_sum_kernel<MODE == GEMM_GATED><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, rows);
+    const size_t n = (size_t)rows * ((g.ldo + 7) / 8);
+    split_sum_kernel<MODE == GEMM_GATED, MODE != GEMM_DW><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, rows);
   }
   return hipGetLastError();
 }
@@ -920,13 +930,10 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   p.xp = take(p.pack_k ? (size_t)p.M * p.Kp * p.size : 0);
   p.wp = take(p.pack_k ? (size_t)p.G * p.R * p.Kp * p.size : 0);
-  // A row table may leave rows out, which the sum over the forward's or dx's parts would not know:
-  // those are split only where there can be no table (the launches ask again).
-  const bool one = p.G == 1;
-  p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt), one);
-  p.few = one && p.M <= FEW_ROWS;
-  p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt), one);
-  p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G), true);
+  p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt));
+  p.few = p.G == 1 && p.M <= FEW_ROWS;
+  p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt));
+  p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G));
   size_t part = 0;
   // (parts * tiles <= 2 CUS of at most 128 x 128 sums, and at most 32 parts)
   auto most = [&](size_t rows, int cols) {
@@ -934,7 +941,7 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
     return a < b ? a : b;
   };
   if (!backward) {
-    if (bound && one) part = most(p.M, p.R);
+    if (bound) part = most(p.M, p.R);
     else if (p.fwd.splits > 1) part = (size_t)p.fwd.splits * p.M * p.R * 4;
   } else {
     p.dz = take((size_t)p.M * p.Rp * p.size);
@@ -943,7 +950,7 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
     p.split_bias = (int)(want < 1 || can < 1 ? 1 : (want < can ? want : can));
     p.bias_part = take(p.split_bias > 1 ? (size_t)p.split_bias * p.G * p.R * 4 : 0);
     if (bound) {
-      part = one ? most(p.M, p.K) : 0;
+      part = most(p.M, p.K);
       const size_t dw = most((size_t)p.G * p.R, p.K);
       part = part > dw ? part : dw;
     } else {
@@ -977,7 +984,7 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.G = p.G; g.M = p.M;
   g.kc = p.K;
   g.out_n = p.N;
-  g.splits = c.group_start ? 1 : p.fwd.splits;
+  g.splits = p.fwd.splits;
   g.part = at<float>(c.ws, p.part);
   g.bias = c.L->bias;
   g.res = c.residual;
@@ -1011,13 +1018,7 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     d.group_start = c.group_start;
     d.M = p.M; d.N = p.N; d.R = p.R; d.G = p.G; d.pitch = p.Rp;
     d.dtype = p.dtype; d.dy_dtype = c.y_dtype; d.act = c.L->act; d.lim = c.L->swiglu_limit;
-    auto go = [&](auto width) {
-      constexpr int V = decltype(width)::value;
-      dz_kernel<V><<<dim3(div_up(p.N, DZ_TX * V), p.G, d.splits), DZ_TX * DZ_TY, 0, st>>>(d);
-    };
-    if (p.N % 8 == 0) go(std::integral_constant<int, 8>{});
-    else if (p.N % 4 == 0) go(std::integral_constant<int, 4>{});
-    else go(std::integral_constant<int, 1>{});
+    dz_kernel<<<dim3(div_up(p.N, DZ_TX * 8), p.G, d.splits), DZ_TX * DZ_TY, 0, st>>>(d);
     if (c.dbias && d.splits > 1)
       bias_sum_kernel<<<div_up((long)p.G * p.R, 32), 256, 0, st>>>(d.bias, c.dbias, p.G * p.R, d.splits);
   }
@@ -1042,7 +1043,7 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     g.b = static_cast<const char*>(w);
     g.kc = p.R;
     g.out = c.dx;
-    g.splits = c.group_start ? 1 : p.dx.splits;
+    g.splits = p.dx.splits;
     e = launch_gemm<GEMM_DX>(p, g, p.dx.tile, st);
   }
   if (e == hipSuccess && c.dw) {

@@ -194,26 +194,8 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t st) {
 // Rows
 // ---------------------------------------------------------------------------------------
 
-// N consecutive elements of a bf16 (uint16_t) or fp32 row, the first `left` of them valid, as fp32.  A
-// row of an odd width starts at any multiple of its element, and so may these addresses: the vector
-// accesses are declared with the element's alignment (the device takes them at any address).
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-// STREAM: the vector accesses bypass the caches' usual replacement (nontemporal), for rows that
-// no cache would hold until they are read again.
-template <bool STREAM, typename V>
-__device__ __forceinline__ V load_vec(const V* p) {
-  if constexpr (STREAM) return __builtin_nontemporal_load(p);
-  else return *p;
-}
-template <bool STREAM, typename V>
-__device__ __forceinline__ void store_vec(V* p, V v) {
-  if constexpr (STREAM) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
-
+// N consecutive elements of a bf16 (uint16_t) or fp32 row, the first `left` of them valid, as fp32.
+// STREAM: for rows that no cache would hold until they are read again.
 template <int N, bool STREAM>
 __device__ __forceinline__ void load_n(const uint16_t* p, int left, float* v) {
   if constexpr (N == 1) {
