@@ -289,22 +289,19 @@ struct Operand {
       off[j] = (uint32_t)row * pitch + unit * E::UNIT + b % E::UNIT;
     }
   }
-  template <bool SHORT>
-  __device__ __forceinline__ void issue(lds_char* lds, uint32_t avail, int rest, int wave) const {
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)avail, 0x00020000);
-#pragma unroll
-    for (int j = 0; j < LOADS; ++j) {
-      // (a chunk behind the end of an along row is sent out of range, which reads as zero)
-      const uint32_t o = ALONG && SHORT && first >= rest ? 0x80000000u : off[j];
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * LOADS + j) * 1024), 16, o, 0, 0, 0);
-    }
-  }
-  // Load the step that has `rest` contraction values left (across: rows; SHORT: fewer than a whole
-  // step's), and move on.
-  template <bool SHORT>
-  __device__ __forceinline__ void load(lds_char* lds, int rest, int wave) {
+  // One of the LOADS loads (1 KiB per wave) of the step that has `rest` contraction values (across: rows) left,
+  // or of none with rest <= 0: what is out of range reads as zero.  WHOLE: a whole step is left.
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(lds_char* lds, int rest, int wave, int j) const {
     // (an across descriptor starts at the tile's first column and ends with the last row)
-    issue<SHORT>(lds, ALONG ? left : (SHORT ? (uint32_t)rest * cut : step) - left, rest, wave);
+    const uint32_t bytes = WHOLE || rest >= KT ? step : (uint32_t)rest * cut;
+    const uint32_t avail = !WHOLE && rest <= 0 ? 0u : (ALONG ? left : bytes - left);
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)avail, 0x00020000);
+    // (a chunk behind the end of an along row is sent out of range)
+    const uint32_t o = ALONG && !WHOLE && first >= rest ? 0x80000000u : off[j];
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(lds + (wave * LOADS + j) * 1024), 16, o, 0, 0, 0);
+  }
+  __device__ __forceinline__ void next() {
     base += ALONG ? STEP_BYTES : step;
     if (ALONG) left -= STEP_BYTES;
   }
@@ -441,20 +438,28 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   // multiplied.  One barrier per step: behind it the step's operands are there for every wave, and
   // every wave has done with the step before, whose stage takes the next load.
   constexpr int LOADS = OpA::LOADS + OpB::LOADS;
-  auto load = [&](int stage) {
-    lds_char* to = lds + stage * STAGE;
-    if (rest >= KT) {
-      a.template load<false>(to, rest, wave);
-      b.template load<false>(to + OpA::BYTES, rest, wave);
-    } else {
-      a.template load<true>(to, rest, wave);
-      b.template load<true>(to + OpA::BYTES, rest, wave);
-    }
+  auto load = [&](lds_char* to, auto piece, auto whole) {  // load `piece` of the step's, A's first
+    constexpr int P = decltype(piece)::value;
+    constexpr bool W = decltype(whole)::value;
+    if constexpr (P < OpA::LOADS) a.template load<W>(to, rest, wave, P);
+    else b.template load<W>(to + OpA::BYTES, rest, wave, P - OpA::LOADS);
+  };
+  auto load_all = [&](lds_char* to) {
+    if (rest >= KT) static_for<0, LOADS>([&](auto p) { load(to, p, std::true_type{}); });
+    else static_for<0, LOADS>([&](auto p) { load(to, p, std::false_type{}); });
+  };
+  auto next = [&]() {
+    a.next();
+    b.next();
     rest -= KT;
   };
 #pragma unroll
-  for (int s = 0; s < NS - 1; ++s)
-    if (s < steps) load(s);
+  for (int s = 0; s < NS - 1; ++s) {
+    if (s < steps) {
+      load_all(lds + s * STAGE);
+      next();
+    }
+  }
   // Row block i of the wave is block i * WM + wm of the tile: the waves share the rows of a short tile
   // (a group's last), and skip what lies behind them in pairs of blocks.
   constexpr int Q = FM >= 2 ? 2 : 1, UNITS = FM / Q;
@@ -465,7 +470,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 
   // One step on `units` units of Q row operands, as a software pipeline: the next unit's reads of LDS go
   // out before this unit's matrix instructions.
-  auto multiply = [&](auto live_units, const lds_char* at) {
+  // The loads of a later step go out over the first SPREAD units, or (0) before them.  Measured at 8192^3, all before / over
+  // 1 / 2 / 3 / 4 / 6 units: forward 863 / 877 / 872 / 839 / 848 / 886 us, dx 936 / 853 / 850 / 854 / 827 / 832,
+  // dw 965 / 925 / 932 / 942 / 953 / 1022.  The smaller tiles, two workgroups on a CU, lose by it
+  // (2000 x 7168 -> 2048 gated 121 / 129 / 133 / 135 / 139 us).
+  constexpr int SPREAD = BM * BN < 256 * 256 ? 0 : (FORWARD ? 3 : (MODE == GEMM_DX ? 4 : 1));
+  auto multiply = [&](auto live_units, const lds_char* at, lds_char* to) {
     constexpr int U = decltype(live_units)::value, HALVES = KB / 64;  // (a matrix instruction takes 64 bytes of a row)
     u32x4_t fa[2][Q], fb[2][FN];
     static_for<0, FN>([&](auto j) { fb[0][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, 0, lane); });
@@ -478,6 +488,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
         static_for<0, Q>([&](auto i) { fa[n & 1][i] = OpA::frag(at, (nq * Q + i) * WM + wm, nh, lane); });
         __builtin_amdgcn_sched_group_barrier(0x100, (nq == 0 ? FN * OpB::READS : 0) + Q * OpA::READS, 0);
       }
+      if constexpr (SPREAD > 0) {
+        constexpr int OVER = HALVES * U < SPREAD ? HALVES * U : SPREAD;
+        constexpr int FIRST = u < OVER ? LOADS * u / OVER : LOADS, LAST = u < OVER ? LOADS * (u + 1) / OVER : LOADS;
+        static_for<FIRST, LAST>([&](auto p) { load(to, p, std::false_type{}); });
+        __builtin_amdgcn_sched_group_barrier(0x020, LAST - FIRST, 0);
+      }
       static_for<0, Q>([&](auto i) {
         static_for<0, FN>([&](auto j) { E::mma(fb[h][j], fa[u & 1][i], acc[q * Q + i][j]); });
       });
@@ -489,15 +505,16 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     for (int s = 0; s < steps; ++s) {
       if (s + NS - 1 <= steps) step_barrier<(NS - 2) * LOADS>();
       else step_barrier<0>();  // (the last steps: fewer younger ones are on their way)
-      if (s + NS - 1 < steps) load(fill);
-      multiply(live_units, lds + cur * STAGE);
+      if (SPREAD == 0 && s + NS - 1 < steps) load_all(lds + fill * STAGE);
+      multiply(live_units, lds + cur * STAGE, lds + fill * STAGE);
+      next();
       cur = cur + 1 == NS ? 0 : cur + 1;
       fill = fill + 1 == NS ? 0 : fill + 1;
     }
   };
   if (units > UNITS / 2) contract(std::integral_constant<int, UNITS>{});
   else contract(std::integral_constant<int, UNITS >= 2 ? UNITS / 2 : 1>{});
-  __syncthreads();  // (the outputs are staged where the operands were)
+  step_barrier<0>();  // (the outputs are staged where the operands were, and where the last, empty loads go)
 
   // ---- outputs, 16 rows at a time: lane (i, g) of a matrix operand holds row i, columns 4 g .. of its
   // 16; through the wave's own part of LDS a lane gets eight neighbouring columns of one row, so that

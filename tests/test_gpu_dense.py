@@ -191,6 +191,16 @@ LINEAR_CASES = [  # M, K, N, start (None: one matrix), act, dtype, y_dtype, bias
     (130, 64, 24, [0, 130], "swiglu", BF16, BF16, True, False),
     (20, 64, 24, [0] * 71, "none", BF16, BF16, False, False),             # every group empty
     (260, 64, 40, list(range(0, 261, 2)), "silu", BF16, F32, True, False),  # 130 groups of two rows
+    (130, 2000, 70, [0, 3, 40, 40, 121], "swiglu", BF16, BF16, True, True),  # a split contraction of grouped rows
+    (300, 2048, 40, [2, 150, 299], "swiglu", F32, F32, True, True),          # the same in fp32
+    (700, 1001, 333, [0, 100, 357, 613, 700], "gelu", BF16, BF16, True, True),
+    # large enough for the large tiles, in each product, with short last tiles and odd widths
+    (4500, 264, 1100, [7, 1500, 1501, 4490], "swiglu", BF16, BF16, True, True),
+    (4099, 2056, 2050, None, "none", BF16, F32, True, True),
+    (300, 4100, 4104, None, "silu", BF16, BF16, True, False),
+    (2060, 4104, 300, None, "gelu", BF16, BF16, True, True),
+    (4099, 200, 2053, None, "swiglu", BF16, F32, False, True),
+    (2500, 1000, 1200, None, "none", F32, F32, True, True),
 ]
 
 
