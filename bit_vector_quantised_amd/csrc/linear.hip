@@ -13,9 +13,10 @@
 //   "along"   the contraction runs along its rows (x and W forward, dz for dx)
 //   "across"  the contraction runs across its rows (W for dx, dz and x for dw)
 // A contraction step takes 128 bytes of an along operand's row (a cache line: 64 bf16 or 32 fp32
-// values, two matrix instructions deep) and as many rows of an across operand.  Both go from memory to LDS without passing through
-// registers (16 bytes per lane).  The buffer descriptor ends at the last valid row, so what
-// lies behind reads as zero: rows of the next group never enter a sum.
+// values, two matrix instructions deep; 64 bytes measured 10 % slower) and as many rows of an across
+// operand.  Both go from memory to LDS without passing through registers (16 bytes per lane).  The
+// buffer descriptor ends at the last valid row, so what lies behind reads as zero: rows of the next
+// group never enter a sum.
 //
 // Matrix instructions: bf16 v_mfma_f32_16x16x32_bf16; fp32 four v_mfma_f32_16x16x4_f32 per
 // 16-byte chunk, chunk element j feeding the j-th, which permutes the contraction index
@@ -84,14 +85,13 @@ __device__ __forceinline__ float gelu_grad(float z) {
 // ---------------------------------------------------------------------------------------
 
 struct Bf16 {
-  using T = uint16_t;
-  static constexpr int SIZE = 2, DTYPE = MOE_VQ_BF16, UNIT = 32, MMAS = 1;  // UNIT: bytes of 16 values; MMAS: instructions of mma
+  // UNIT: bytes of 16 values; MMAS: instructions of one mma
+  static constexpr int SIZE = 2, DTYPE = MOE_VQ_BF16, UNIT = 32, MMAS = 1;
   static __device__ __forceinline__ void mma(const u32x4_t& a, const u32x4_t& b, f32x4_t& c) {
     c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
   }
 };
 struct F32 {
-  using T = float;
   static constexpr int SIZE = 4, DTYPE = MOE_VQ_F32, UNIT = 64, MMAS = 4;
   static __device__ __forceinline__ void mma(const u32x4_t& a, const u32x4_t& b, f32x4_t& c) {
     const uint32_t av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -247,17 +247,17 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // One operand of a tile: B rows of output space (ALONG) or B columns (across), loaded by NW waves.
-template <typename E, int B, bool ALONG, int NW, int KB>
+template <typename E, int B, bool ALONG, int NW>
 struct Operand {
-  static_assert(!ALONG || KB == STEP_BYTES, "an along operand is loaded by whole cache lines");
-  static constexpr int BYTES = B * KB;
+  static constexpr int BYTES = B * STEP_BYTES;
   static constexpr int LOADS = BYTES / 1024 / NW;     // 1 KiB per wave and load
   static constexpr int ROWB = B * E::SIZE;            // bytes of an across row
-  static constexpr int KT = KB / E::SIZE;             // contraction values per step
+  static constexpr int KT = STEP_BYTES / E::SIZE;     // contraction values per step
   static constexpr int READS = ALONG ? 1 : E::SIZE;   // LDS reads of a matrix operand (2 of bf16, 4 of fp32 across)
   static_assert(LOADS >= 1 && LOADS * NW * 1024 == BYTES, "loads divide evenly over the waves");
   uint64_t base;    // address of this step's first byte
-  uint32_t left;    // along: bytes from base to the end of what may be read; across: byte offset of the tile's first column
+  uint32_t left;    // along: bytes from base to the end of what may be read; across: byte offset of the
+                    // tile's first column
   uint32_t step, cut;  // across: bytes of a step's rows, of one row
   uint32_t off[LOADS];
   int first;        // along: first contraction value of the lane's chunk
@@ -289,8 +289,8 @@ struct Operand {
       off[j] = (uint32_t)row * pitch + unit * E::UNIT + b % E::UNIT;
     }
   }
-  // One of the LOADS loads (1 KiB per wave) of the step that has `rest` contraction values (across: rows) left,
-  // or of none with rest <= 0: what is out of range reads as zero.  WHOLE: a whole step is left.
+  // One of the LOADS loads (1 KiB per wave) of the step that has `rest` contraction values (across: rows)
+  // left, or of none with rest <= 0: what is out of range reads as zero.  WHOLE: a whole step is left.
   template <bool WHOLE>
   __device__ __forceinline__ void load(lds_char* lds, int rest, int wave, int j) const {
     // (an across descriptor starts at the tile's first column and ends with the last row)
@@ -331,16 +331,16 @@ struct Operand {
   }
 };
 
-template <typename E, int BM, int BN, int WM, int WN, int NS, int KB, int MODE>
+template <typename E, int BM, int BN, int WM, int WN, int NS, int MODE>
 __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   constexpr int NW = WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
-  using OpA = Operand<E, BM, MODE != GEMM_DW, NW, KB>;
+  using OpA = Operand<E, BM, MODE != GEMM_DW, NW>;
   constexpr bool GATED = MODE == GEMM_GATED, FORWARD = MODE == GEMM_FWD || GATED;
   static_assert(!GATED || FN % 2 == 0, "a wave holds gate and up of its columns");
-  using OpB = Operand<E, BN, FORWARD, NW, KB>;
+  using OpB = Operand<E, BN, FORWARD, NW>;
   constexpr int KT = OpA::KT;
-  constexpr int STAGE = (BM + BN) * KB;
+  constexpr int STAGE = (BM + BN) * STEP_BYTES;
   __shared__ __align__(1024) char lds_mem[NS * STAGE];
   lds_char* lds = (lds_char*)lds_mem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -469,14 +469,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   const int units = blocks >= BM / 16 ? UNITS : ((blocks + WM - 1) / WM + Q - 1) / Q;
 
   // One step on `units` units of Q row operands, as a software pipeline: the next unit's reads of LDS go
-  // out before this unit's matrix instructions.
-  // The loads of a later step go out over the first SPREAD units, or (0) before them.  Measured at 8192^3, all before / over
-  // 1 / 2 / 3 / 4 / 6 units: forward 863 / 877 / 872 / 839 / 848 / 886 us, dx 936 / 853 / 850 / 854 / 827 / 832,
-  // dw 965 / 925 / 932 / 942 / 953 / 1022.  The smaller tiles, two workgroups on a CU, lose by it
-  // (2000 x 7168 -> 2048 gated 121 / 129 / 133 / 135 / 139 us).
+  // out before this unit's matrix instructions (8192^3 forward 836 us, all reads of a half first 862).
+  // The loads of a later step go out over the first SPREAD units, or (0) before them.  Measured at
+  // 8192^3, before / over 1 / 2 / 3 / 4 / 6 units: forward 863 / 877 / 872 / 839 / 848 / 886 us, dx 936 / 853 /
+  // 850 / 854 / 827 / 832, dw 965 / 925 / 932 / 942 / 953 / 1022.  The smaller tiles, two workgroups on a CU,
+  // lose by it (2000 x 7168 -> 2048 gated 121 / 129 / 133 / 135 / 139 us).
   constexpr int SPREAD = BM * BN < 256 * 256 ? 0 : (FORWARD ? 3 : (MODE == GEMM_DX ? 4 : 1));
   auto multiply = [&](auto live_units, const lds_char* at, lds_char* to) {
-    constexpr int U = decltype(live_units)::value, HALVES = KB / 64;  // (a matrix instruction takes 64 bytes of a row)
+    constexpr int U = decltype(live_units)::value, HALVES = STEP_BYTES / 64;  // (a matrix instruction takes 64 bytes of a row)
     u32x4_t fa[2][Q], fb[2][FN];
     static_for<0, FN>([&](auto j) { fb[0][j] = OpB::frag(at + OpA::BYTES, wn * FN + j, 0, lane); });
     static_for<0, Q>([&](auto i) { fa[0][i] = OpA::frag(at, i * WM + wm, 0, lane); });
@@ -522,8 +522,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   constexpr int PITCH = FN * 16 + 4;
   constexpr int COLS = GATED ? FN * 8 : FN * 16;  // output columns of the wave
   static_assert(NW * 2 * 16 * PITCH * 4 <= (int)sizeof(lds_mem), "output staging");
-  // The largest tiles' outputs exceed the L2s many times over: streamed, dw of 16 experts' 512 rows each takes
-  // 779 us instead of 924, and 8192^3 reaches 1256 (dx) and 1212 TFLOP/s (dw) instead of 1152 and 1112.
+  // The largest tiles' outputs exceed the L2s many times over: streamed, dw of 16 experts' 512 rows each
+  // takes 779 us instead of 924, and at 8192^3 dx gains 9 % and dw 9 %.
   constexpr bool STREAM = BM * BN >= 256 * 256;
   float* stage = reinterpret_cast<float*>(lds_mem) + wave * 2 * 16 * PITCH;
   const size_t out_rows = MODE == GEMM_DW ? (size_t)g.G * g.out_m : (size_t)g.M;
@@ -592,8 +592,8 @@ constexpr int FEW_ROWS = 16, FEW_WAVES = 8, FEW_STREAM = 4;
 
 template <typename E, bool GATED>
 __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(GemmArgs g) {
-  constexpr int STEP = 64, VALS = 16 / E::SIZE;  // bytes of a row per load of its 16 rows; values of a lane
-  constexpr int PITCH = 20;                      // floats between the columns of the staged sums
+  constexpr int STEP = 64;   // bytes of a row per load of its 16 rows
+  constexpr int PITCH = 20;  // floats between the staged rows
   __shared__ __align__(16) float red[FEW_WAVES][FEW_ROWS][PITCH];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int i = lane & 15, q = lane >> 4;
@@ -694,13 +694,23 @@ __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
 // Repacking rows whose width is no multiple of 16 bytes (dst pitch: the next one, zero-filled)
 // ---------------------------------------------------------------------------------------
 
+// 16 bytes of dst per thread and turn; the turns cover any number of rows with a bounded grid.
 template <typename T>
 __global__ __launch_bounds__(256) void pack_rows_kernel(const T* src, T* dst, size_t rows, int cols, int pitch) {
-  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= rows * (size_t)pitch) return;
-  const size_t r = at / pitch;
-  const int c = (int)(at - r * pitch);
-  dst[at] = c < cols ? src[r * cols + c] : T(0);
+  constexpr int N = 16 / sizeof(T);
+  const size_t per = pitch / N, all = rows * per;
+  for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (size_t)gridDim.x * 256) {
+    const size_t r = at / per;
+    const int c = (int)(at - r * per) * N;
+    const T* from = src + r * cols + c;
+    if (c + N <= cols) {
+      const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from);
+      *reinterpret_cast<u32x4_t*>(dst + at * N) = u32x4_t{v.x, v.y, v.z, v.w};
+    } else {
+#pragma unroll
+      for (int j = 0; j < N; ++j) dst[at * N + j] = c + j < cols ? from[j] : T(0);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -748,10 +758,10 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
   }
 }
 
-// One workgroup: 8 DZ_TX columns of one split of one group's rows, two rows of a thread at a time (their loads are
-// issued together).  Bound by reading dy and z and writing dz, each once.  dz is rounded to the
-// element type for the matrix products; the column sums add the unrounded values in fp32, rows in a
-// fixed order.
+// One workgroup: 8 DZ_TX columns of one split of one group's rows, two rows of a thread at a time (their loads
+// are issued together).  Bound by reading dy and z and writing dz, each once (8192 rows of 16 groups, 2 x 2048
+// columns: 168 MB in 38 us).  dz is rounded to the element type for the matrix products; the column
+// sums add the unrounded values in fp32, rows in a fixed order.
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
@@ -842,35 +852,40 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float* part, float*
 using Cut = LinearPlan::Cut;
 constexpr int CUS = 256;
 
-// A kind of tile: its side, how many workgroups of it a CU holds, and what a workgroup takes (microseconds, measured): per
-// contraction step with its CU full, per step if it has the CU to itself, and before and after them.
+// A kind of tile: its side, how many workgroups of it a CU holds, and what a workgroup takes (microseconds,
+// measured): per contraction step with its CU full, per step if it has the CU to itself, and before
+// and after them.
 struct TileKind {
   int side, per_cu;
   float step, step_alone, rest;
 };
 constexpr TileKind BF16_TILES[] = {{256, 1, 1.95f, 1.95f, 8.f}, {128, 2, 1.2f, 0.8f, 6.f}, {64, 2, 0.6f, 0.45f, 5.f}};
-constexpr TileKind F32_TILES[] = {{128, 2, 3.9f, 2.1f, 6.f}, {64, 2, 1.0f, 0.6f, 5.f}};
+constexpr TileKind F32_TILES[] = {{128, 2, 3.9f, 2.1f, 6.f}, {64, 2, 1.0f, 0.75f, 5.f}};
 
 // How a product is cut.  rows: output rows in all, of `groups` groups; cols: output columns (weight rows forward);
-// steps: contraction steps.  The cut with the smallest estimate is taken: rounds of workgroups over the device, times a workgroup's time, and for a split
-// contraction the write and read of its parts (from the caches: 10 TB/s) and one more launch.  Large
-// products so take 256 x 256 tiles (1400 TFLOP/s at 8192^3, 128 x 128 tiles, which read LDS twice as
+// steps: contraction steps.  The cut with the smallest estimate is taken: rounds of workgroups over the
+// device, times a workgroup's time, and for a split contraction the write and read of its parts (from
+// the caches: 10 TB/s) and one more launch.  Large products so take 256 x 256 tiles (1400 TFLOP/s at 8192^3, 128 x 128 tiles, which read LDS twice as
 // often for their products, 1150) unless the last round would be nearly empty; small outputs with
 // long contractions are split, and outputs too small for that take small tiles.
-Cut pick_cut(int dtype, long rows, long groups, long cols, int steps) {
+Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool forward) {
   const long per = (rows + groups - 1) / groups;
   Cut best{64, 1};
   float least = 3.0e38f;
   auto consider = [&](const TileKind& k) {
+    // (few rows wait for weights: forward, where those lie along, small tiles have more loads on their way: 64
+    // rows of 32 groups, 2048 -> 7168, 126 us by 64 x 64 tiles, 151 by 128 x 128.  For dx they lie across,
+    // where wide tiles read longer runs: 358 rows of 21 groups, 3328 -> 5376, 148 us by 128 x 128, 200 by 64 x 64)
+    if (forward && k.side > 64 && k.side >= 2 * per) return;
     const long tiles = (per + k.side - 1) / k.side * groups * ((cols + k.side - 1) / k.side);
     for (int parts = 1; parts <= 32; parts *= 2) {
-      // (at most two workgroups per CU are split ones, of at least four steps)
-      if (parts > 1 && (k.side > 128 || tiles * parts > 2 * CUS || steps < 4 * parts)) break;
+      // (at most two workgroups per CU are split ones, of at least eight steps)
+      if (parts > 1 && (k.side > 128 || tiles * parts > 2 * CUS || steps < 8 * parts)) break;
       const long n = tiles * parts, slots = (long)k.per_cu * CUS;
       const float rounds = n <= slots ? 1.f : (n < 3 * slots ? (float)((n + slots - 1) / slots) : (float)n / slots + 0.5f);
       const int each = (steps + parts - 1) / parts;
       float t = rounds * (each * (n <= CUS ? k.step_alone : k.step) + k.rest);
-      if (parts > 1) t += 3.f + 8.f * parts * rows * cols / 10.0e6f;
+      if (parts > 1) t += 4.f + 0.5f * parts + 8.f * parts * rows * cols / 10.0e6f;
       if (t < least) { least = t; best = {k.side, parts}; }
     }
   };
@@ -881,7 +896,7 @@ Cut pick_cut(int dtype, long rows, long groups, long cols, int steps) {
 
 int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 
-template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS, int KB = STEP_BYTES>
+template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS>
 void gemm_go(const GemmArgs& g, hipStream_t st) {
   const int per_n = MODE == GEMM_GATED ? BN / 2 : BN;
   const long nt = div_up(g.out_n, per_n);
@@ -889,7 +904,7 @@ void gemm_go(const GemmArgs& g, hipStream_t st) {
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
   const long grid = nt * mt * g.splits;
-  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, KB, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
+  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
 }
 
 template <int MODE>
@@ -918,9 +933,9 @@ void few_go(const GemmArgs& g, bool gated, hipStream_t st) {
 }
 
 void pack_rows(const LinearPlan& p, const void* src, void* dst, size_t rows, hipStream_t st) {
-  const size_t n = rows * p.Kp;
-  const unsigned grid = (unsigned)((n + 255) / 256);
-  if (n == 0) return;
+  const size_t blocks = (rows * p.Kp * p.size / 16 + 255) / 256;
+  if (blocks == 0) return;
+  const unsigned grid = (unsigned)(blocks < 64 * CUS ? blocks : 64 * CUS);
   if (p.size == 2)
     pack_rows_kernel<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, p.K, p.Kp);
   else
@@ -947,10 +962,10 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
   p.xp = take(p.pack_k ? (size_t)p.M * p.Kp * p.size : 0);
   p.wp = take(p.pack_k ? (size_t)p.G * p.R * p.Kp * p.size : 0);
-  p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt));
+  p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt), true);
   p.few = p.G == 1 && p.M <= FEW_ROWS;
-  p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt));
-  p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G));
+  p.dx = pick_cut(p.dtype, p.M, p.G, p.K, div_up(p.R, kt), false);
+  p.dw = pick_cut(p.dtype, (long)p.G * p.R, p.G, p.K, div_up(p.M, (long)kt * p.G), false);
   size_t part = 0;
   // (parts * tiles <= 2 CUS of at most 128 x 128 sums, and at most 32 parts)
   auto most = [&](size_t rows, int cols) {

@@ -21,7 +21,7 @@ ACTS = {"none": _lib.ACT_NONE, "silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "sw
 
 def _need(t: torch.Tensor, what: str, shape, dtype, device) -> int:
     """The address of t, which must be a contiguous tensor of this shape, type and device."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{what}: need a contiguous {tuple(shape)} {dtype} tensor on {device}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()
@@ -36,6 +36,8 @@ class _OnDevice:
     """Calls run on the current stream of the object's device, whichever device is current."""
 
     def __init__(self, device: torch.device):
+        if device.type != "cuda":
+            raise ValueError(f"need a GPU tensor or device, got {device}")
         self.device = device
 
     def _call(self, fn, *args) -> None:

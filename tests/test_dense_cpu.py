@@ -104,3 +104,23 @@ def test_linear_refusals(backward):
         assert call(dx=None, dw=None, db=None) == _lib.OK
     else:
         assert call(M=0) == _lib.OK
+
+
+def test_python_refuses_what_the_library_cannot_see():
+    import torch
+
+    from bit_vector_quantised_amd.dense import DenseExperts, ExpertRows, Linear, _need
+    with pytest.raises(ValueError):
+        ExpertRows(8, 2, 4, device="cpu")
+    with pytest.raises(ValueError):
+        Linear(torch.zeros(4, 8))  # weights in host memory
+    with pytest.raises(ValueError):
+        Linear(torch.zeros(4, 8), act="relu")
+    with pytest.raises(ValueError):
+        DenseExperts(torch.zeros(2, 8, 16), torch.zeros(2, 16, 5), 1, 4)
+    cpu = torch.device("cpu")
+    t = torch.zeros(4, 6)
+    assert _need(t, "t", (4, 6), torch.float32, cpu) == t.data_ptr()
+    for bad in (t.t(), t[:, :3], t.bfloat16(), t[:3]):
+        with pytest.raises(ValueError):
+            _need(bad, "t", (4, 6), torch.float32, cpu)
