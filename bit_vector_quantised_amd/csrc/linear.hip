@@ -760,12 +760,14 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
 
 // One workgroup: 8 DZ_TX columns of one split of one group's rows, two rows of a thread at a time (their loads
 // are issued together).  Bound by reading dy and z and writing dz, each once (8192 rows of 16 groups, 2 x 2048
-// columns: 168 MB in 38 us).  dz is rounded to the element type for the matrix products; the column
+// columns: 168 MB in 63 us).  dz is rounded to the element type for the matrix products; the column
 // sums add the unrounded values in fp32, rows in a fixed order.
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
-  const int n = (blockIdx.x * DZ_TX + tx) * 8;
+  // (a row's last eight columns may overlap the eight before them: both threads write the same values)
+  int n = (blockIdx.x * DZ_TX + tx) * 8;
+  if (n < a.N && n > a.N - 8 && a.N >= 8) n = a.N - 8;
   const int grp = blockIdx.y, split = blockIdx.z;
   int r0 = 0, r1 = a.M;
   if (a.group_start) {
@@ -977,8 +979,8 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
     else if (p.fwd.splits > 1) part = (size_t)p.fwd.splits * p.M * p.R * 4;
   } else {
     p.dz = take((size_t)p.M * p.Rp * p.size);
-    // (as many workgroups as keep the device busy, each with 16 rows at least)
-    const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 2048 / strips, can = div_up(p.M, 16 * p.G);
+    // (as many workgroups as keep the device busy, each with a row per thread at least)
+    const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 2048 / strips, can = div_up(p.M, DZ_TY * p.G);
     p.split_bias = (int)(want < 1 || can < 1 ? 1 : (want < can ? want : can));
     p.bias_part = take(p.split_bias > 1 ? (size_t)p.split_bias * p.G * p.R * 4 : 0);
     if (bound) {

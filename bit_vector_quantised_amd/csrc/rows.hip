@@ -194,13 +194,13 @@ hipError_t launch_sort(const SortArgs& a, hipStream_t st) {
 // Rows
 // ---------------------------------------------------------------------------------------
 
-// N consecutive elements of a bf16 (uint16_t) or fp32 row, the first `left` of them valid, as fp32.
-// STREAM: for rows that no cache would hold until they are read again.
+// N consecutive elements of a bf16 (uint16_t) or fp32 row, as fp32.  STREAM: for rows that no cache would
+// hold until they are read again.
 template <int N, bool STREAM>
-__device__ __forceinline__ void load_n(const uint16_t* p, int left, float* v) {
+__device__ __forceinline__ void load_n(const uint16_t* p, float* v) {
   if constexpr (N == 1) {
     v[0] = bf16_bits_to_f32(*p);
-  } else if (left >= N) {
+  } else {
     uint32_t w[N / 2];
     if constexpr (N == 8) {
       const u32x4_any u = load_vec<STREAM>(reinterpret_cast<const u32x4_any*>(p));
@@ -214,54 +214,40 @@ __device__ __forceinline__ void load_n(const uint16_t* p, int left, float* v) {
       v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu);
       v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u);
     }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = q < left ? bf16_bits_to_f32(p[q]) : 0.f;
   }
 }
 template <int N, bool STREAM>
-__device__ __forceinline__ void load_n(const float* p, int left, float* v) {
+__device__ __forceinline__ void load_n(const float* p, float* v) {
   if constexpr (N == 1) {
     v[0] = *p;
-  } else if (left >= N) {
+  } else {
 #pragma unroll
     for (int q = 0; q < N; q += 4) {
       const f32x4_any u = load_vec<STREAM>(reinterpret_cast<const f32x4_any*>(p + q));
       v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
     }
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; ++q) v[q] = q < left ? p[q] : 0.f;
   }
 }
 template <int N, bool STREAM>
-__device__ __forceinline__ void store_n(uint16_t* p, int left, const float* v) {
+__device__ __forceinline__ void store_n(uint16_t* p, const float* v) {
   if constexpr (N == 1) {
     *p = f32_to_bf16_rne(v[0]);
-  } else if (left >= N) {
+  } else {
     uint32_t w[N / 2];
 #pragma unroll
-    for (int q = 0; q < N / 2; ++q)
-      w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+    for (int q = 0; q < N / 2; ++q) w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
     if constexpr (N == 8) store_vec<STREAM>(reinterpret_cast<u32x4_any*>(p), u32x4_any{w[0], w[1], w[2], w[3]});
     else store_vec<STREAM>(reinterpret_cast<u32x2_any*>(p), u32x2_any{w[0], w[1]});
-  } else {
-#pragma unroll
-    for (int q = 0; q < N; ++q)
-      if (q < left) p[q] = f32_to_bf16_rne(v[q]);
   }
 }
 template <int N, bool STREAM>
-__device__ __forceinline__ void store_n(float* p, int left, const float* v) {
+__device__ __forceinline__ void store_n(float* p, const float* v) {
   if constexpr (N == 1) {
     *p = v[0];
-  } else if (left >= N) {
-#pragma unroll
-    for (int q = 0; q < N; q += 4) store_vec<STREAM>(reinterpret_cast<f32x4_any*>(p + q), f32x4_any{v[q], v[q + 1], v[q + 2], v[q + 3]});
   } else {
 #pragma unroll
-    for (int q = 0; q < N; ++q)
-      if (q < left) p[q] = v[q];
+    for (int q = 0; q < N; q += 4)
+      store_vec<STREAM>(reinterpret_cast<f32x4_any*>(p + q), f32x4_any{v[q], v[q + 1], v[q + 2], v[q + 3]});
   }
 }
 
@@ -337,10 +323,8 @@ hipError_t launch_gather(const RowsArgs& a, int dtype, hipStream_t st) {
 // y[t] = add[t] + sum_i w_i rows[row_i], N columns per thread, fp32 sums in the order of i.
 // Eight rows' loads are issued before the first is used; a dropped pair's load is
 // redirected to row 0 and its value dropped (selected, not multiplied: it may hold NaN).
-// left: columns of the thread's N that the row has (the whole N for all but a row's last thread,
-// which takes a branch of its own, so that the loads of the others stay together).
 template <typename TR, typename TY, int N, bool STREAM>
-__device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t col, int left) {
+__device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t col) {
   const int k = a.k, P = a.T * k;
   const size_t C = (size_t)a.C;
   const TR* rows = static_cast<const TR*>(a.x);
@@ -348,7 +332,7 @@ __device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t
   const float* wt = a.pair_w ? a.pair_w + (size_t)t * k : nullptr;
   float acc[N];
   if (a.add) {
-    load_n<N, STREAM>(static_cast<const TY*>(a.add) + (size_t)t * C + col, left, acc);
+    load_n<N, STREAM>(static_cast<const TY*>(a.add) + (size_t)t * C + col, acc);
   } else {
 #pragma unroll
     for (int q = 0; q < N; ++q) acc[q] = 0.f;
@@ -362,14 +346,14 @@ __device__ __forceinline__ void combine_columns(const RowsArgs& a, int t, size_t
       const int r = at[j];
       ok[i] = i0 + i < k && (uint32_t)r < (uint32_t)P;
       w[i] = wt ? wt[j] : 1.f;
-      load_n<N, STREAM>(rows + (ok[i] ? (size_t)r : 0) * C + col, left, v[i]);
+      load_n<N, STREAM>(rows + (ok[i] ? (size_t)r : 0) * C + col, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int q = 0; q < N; ++q) acc[q] = ok[i] ? fmaf(w[i], v[i][q], acc[q]) : acc[q];
   }
-  store_n<N, STREAM>(static_cast<TY*>(a.y) + (size_t)t * C + col, left, acc);
+  store_n<N, STREAM>(static_cast<TY*>(a.y) + (size_t)t * C + col, acc);
 }
 
 template <typename TR, typename TY, int N, bool STREAM>
@@ -377,17 +361,15 @@ __global__ __launch_bounds__(1 << row_threads_log(STREAM)) void combine_rows_ker
   int t, u;
   row_pos(tx_log, nbx, t, u);
   if (t >= a.T || u >= units) return;
-  const size_t col = (size_t)u * N;
-  const int left = a.C - (int)col;
-  if (left >= N) combine_columns<TR, TY, N, STREAM>(a, t, col, N);
-  else
-    for (int q = 0; q < left; ++q) combine_columns<TR, TY, 1, STREAM>(a, t, col + q, 1);
+  const int whole = a.C / N;  // units of N columns; the first threads take one more column each behind them
+  if (u < whole) combine_columns<TR, TY, N, STREAM>(a, t, (size_t)u * N);
+  if (u < a.C - whole * N) combine_columns<TR, TY, 1, STREAM>(a, t, (size_t)whole * N + u);
 }
 
 template <typename TR, typename TY>
 static void combine_go(const RowsArgs& a, hipStream_t st) {
   constexpr int N = 16 / sizeof(TR);
-  const int units = (a.C + N - 1) / N;
+  const int units = a.C / N > a.C % N ? a.C / N : a.C % N;
   auto go = [&](auto stream) {
     constexpr bool S = decltype(stream)::value;
     const RowGrid g = row_grid(units, a.T, S);
@@ -440,10 +422,10 @@ __global__ __launch_bounds__(BWD_THREADS) void combine_rows_bwd_kernel(RowsArgs 
     constexpr int W = decltype(width)::value;
     constexpr bool DW = decltype(with_dw)::value;
     float g[W], v[PG][W];
-    load_n<W, STREAM>(dy + c, W, g);
+    load_n<W, STREAM>(dy + c, g);
     if constexpr (DW) {
 #pragma unroll
-      for (int i = 0; i < PG; ++i) load_n<W, STREAM>(rows + off[i] + c, W, v[i]);
+      for (int i = 0; i < PG; ++i) load_n<W, STREAM>(rows + off[i] + c, v[i]);
       __builtin_amdgcn_sched_group_barrier(0x020, 2 * PG + 2, 0);
 #pragma unroll
       for (int i = 0; i < PG; ++i)
@@ -456,7 +438,7 @@ __global__ __launch_bounds__(BWD_THREADS) void combine_rows_bwd_kernel(RowsArgs 
         float d[W];
 #pragma unroll
         for (int q = 0; q < W; ++q) d[q] = w[i] * g[q];
-        if (ok[i]) store_n<W, STREAM>(drows + off[i] + c, W, d);
+        if (ok[i]) store_n<W, STREAM>(drows + off[i] + c, d);
       }
     }
   };

@@ -510,6 +510,41 @@ def test_on_another_stream():
     assert torch.equal(got, want)
 
 
+def test_two_products_at_once():
+    """Two objects on two streams, large enough to overlap, with and without a split contraction: each gives
+    what it gives alone."""
+    say("two products at once")
+    g = gen(21)
+    cases = []
+    for M, K, N, act in ((1500, 512, 1024, "swiglu"), (96, 4096, 256, "gelu")):
+        R = 2 * N if act == "swiglu" else N
+        w = randn(g, R, K, dtype=BF16, scale=K ** -0.5).cuda()
+        x, dy = randn(g, M, K, dtype=BF16).cuda(), randn(g, M, N, dtype=BF16).cuda()
+        lin = Linear(w, act=act, max_rows=M, backward=True)
+        new = lambda: (torch.empty(M, N, dtype=BF16, device="cuda"), torch.empty(M, R, dtype=BF16, device="cuda"),  # noqa: E731
+                       torch.empty_like(x), torch.empty_like(w))
+        cases.append((lin, x, dy, new(), new()))
+
+    def run(c, out):
+        lin, x, dy = c[:3]
+        y, z, dx, dw = out
+        lin.forward(x, out=y, z=z)
+        lin.backward(x, dy, z, dx=dx, dw=dw)
+
+    for c in cases:
+        run(c, c[3])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for s, c in zip(streams, cases):
+            with torch.cuda.stream(s):
+                run(c, c[4])
+    torch.cuda.synchronize()
+    for c in cases:
+        for a, b in zip(c[3], c[4]):
+            assert torch.equal(a, b)
+
+
 def test_same_routing_as_the_coded_step():
     """The unquantised layer behind Step.route: the experts' own decoded weights give the coded
     step's output (held to the coded step's own tolerance, 1e-2 of the largest value, plus bf16
