@@ -13,6 +13,13 @@ bool dtype_ok(int d) { return d == MOE_VQ_F32 || d == MOE_VQ_BF16; }
 bool off16(const void* p) { return ((uintptr_t)p & 15) != 0; }
 bool off4(const void* p) { return ((uintptr_t)p & 3) != 0; }
 
+// Buffers [p, p + n) and [q, q + m) share a byte.  An output that overlaps an input would be written by
+// one workgroup while another still reads it.
+bool overlap(const void* p, size_t n, const void* q, size_t m) {
+  return p && q && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+}
+size_t size_of(int d) { return d == MOE_VQ_BF16 ? 2 : 4; }
+
 bool rows_dims_ok(int n_tokens, int top_k, int n_cols) {
   return n_tokens >= 0 && n_tokens <= MAX_T && top_k >= 1 && top_k <= MAX_K && n_cols >= 1 && n_cols <= MAX_COLS;
 }
@@ -77,6 +84,8 @@ int moe_vq_gather_rows(const void* x, int dtype, int n_tokens, int top_k, int n_
   if (!rows_dims_ok(n_tokens, top_k, n_cols) || !dtype_ok(dtype)) return MOE_VQ_EINVAL;
   if (n_tokens == 0) return MOE_VQ_OK;
   if (!x || !pair_row || !xs || off16(x) || off16(xs) || off4(pair_row)) return MOE_VQ_EINVAL;
+  const size_t bytes = (size_t)n_tokens * n_cols * size_of(dtype);
+  if (overlap(xs, bytes * top_k, x, bytes)) return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.x = x;
@@ -91,6 +100,9 @@ int moe_vq_combine_rows(const void* rows, int dtype, int n_tokens, int top_k, in
   if (n_tokens == 0) return MOE_VQ_OK;
   if (!rows || !pair_row || !y || off16(rows) || off16(y) || off16(residual)) return MOE_VQ_EINVAL;
   if (off4(pair_row) || off4(w)) return MOE_VQ_EINVAL;
+  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * size_of(y_dtype);
+  if (overlap(y, bytes, rows, cells * top_k * size_of(dtype))) return MOE_VQ_EINVAL;
+  if (y != residual && overlap(y, bytes, residual, bytes)) return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.pair_w = w;
@@ -108,6 +120,8 @@ int moe_vq_combine_rows_backward(const void* dy, int dy_dtype, int n_tokens, int
   if (n_tokens == 0 || (!drows && !dw)) return MOE_VQ_OK;
   if (!dy || !pair_row || (dw && !rows) || off16(dy) || off16(rows) || off16(drows)) return MOE_VQ_EINVAL;
   if (off4(pair_row) || off4(w) || off4(dw)) return MOE_VQ_EINVAL;
+  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * top_k * size_of(dtype);
+  if (overlap(drows, bytes, rows, bytes) || overlap(drows, bytes, dy, cells * size_of(dy_dtype))) return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.pair_w = w;
@@ -134,6 +148,9 @@ int moe_vq_linear_forward(const moe_vq_linear* L, const void* x, int n_rows, con
   if (!x || !y || off16(x) || off16(y) || off16(residual) || off16(z)) return MOE_VQ_EINVAL;
   const LinearPlan p = linear_plan(L, n_rows, false);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
+  const size_t xb = (size_t)p.M * p.K * p.size, zb = (size_t)p.M * p.R * p.size, yb = (size_t)p.M * p.N * size_of(y_dtype);
+  if (overlap(y, yb, x, xb) || (y != residual && overlap(y, yb, residual, yb))) return MOE_VQ_EINVAL;
+  if (overlap(z, zb, x, xb) || overlap(z, zb, y, yb) || overlap(z, zb, residual, yb)) return MOE_VQ_EINVAL;
   LinearCall c{};
   c.L = L;
   c.x = x;
@@ -157,6 +174,10 @@ int moe_vq_linear_backward(const moe_vq_linear* L, const void* x, int n_rows, co
   if (n_rows > 0 && (!dy || (dw && !x) || (L->act != MOE_VQ_ACT_NONE && !z))) return MOE_VQ_EINVAL;
   const LinearPlan p = linear_plan(L, n_rows, true);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
+  const size_t xb = (size_t)p.M * p.K * p.size, wb = (size_t)p.G * p.R * p.K * p.size;
+  const size_t zb = (size_t)p.M * p.R * p.size, yb = (size_t)p.M * p.N * size_of(dy_dtype);
+  if (overlap(dx, xb, x, xb) || overlap(dx, xb, z, zb) || overlap(dx, xb, dy, yb) || overlap(dx, xb, dw, wb)) return MOE_VQ_EINVAL;
+  if (overlap(dw, wb, x, xb) || overlap(dw, wb, z, zb) || overlap(dw, wb, dy, yb)) return MOE_VQ_EINVAL;
   LinearCall c{};
   c.L = L;
   c.x = x;

@@ -582,7 +582,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 
 // Forward product of at most 16 rows.  Bound by streaming W from HBM once; a 64 x 64 tile spends as much on
 // the parts of its split contraction and their sum (one row, 7168 -> 2048 gated, weights not in
-// any cache: 19 us) as on the weights (13 us here, of which the 59 MB take 10 to 11).  A workgroup
+// any cache: 19 us) as on the weights (11 to 12 us here, of which the 59 MB take 10).  A workgroup
 // takes 16 weight rows (gated: eight gate rows and their up rows), its eight waves split the
 // contraction among them, and their sums meet in LDS in a fixed order: one launch.  W goes from
 // memory to the registers of the matrix operand, 16 rows of 64 bytes per load; the rows of x, which

@@ -106,6 +106,44 @@ def test_linear_refusals(backward):
         assert call(M=0) == _lib.OK
 
 
+def test_overlapping_buffers_are_refused():
+    """A workgroup would read what another has overwritten.  (Buffers far apart are let through to the launch,
+    so only refusals are tried here: one byte of overlap from either side.)"""
+    far = [A + (i << 30) for i in range(1, 8)]
+
+    def fwd(x=far[0], res=None, y=far[1], z=far[2]):
+        d = lin(n_in=64, n_out=32, act=_lib.ACT_SWIGLU)  # 4 rows: x 512 bytes, y 512, z 512
+        return RAW.moe_vq_linear_forward(ctypes.byref(d), x, 4, None, res, y, _lib.F32, z, far[6], 1 << 40, None)
+
+    def bwd(x=far[0], z=far[1], dy=far[2], dx=far[3], dw=far[4]):
+        d = lin(n_in=64, n_out=32, act=_lib.ACT_SWIGLU)  # dw 64 x 64: 8192 bytes
+        return RAW.moe_vq_linear_backward(ctypes.byref(d), x, 4, None, z, dy, _lib.F32, dx, dw, None, far[6], 1 << 40, None)
+
+    for off in (-496, 0, 496):
+        assert fwd(y=far[0] + off) == fwd(z=far[0] + off) == fwd(z=far[1] + off) == _lib.EINVAL
+        assert fwd(res=far[2] + off) == _lib.EINVAL  # z over the residual
+        assert bwd(dx=far[0] + off) == bwd(dx=far[1] + off) == bwd(dx=far[2] + off) == _lib.EINVAL
+        assert bwd(dw=far[0] + off) == bwd(dw=far[1] + off) == bwd(dw=far[2] + off) == bwd(dw=far[3] + off) == _lib.EINVAL
+    for off in (-496, 496):
+        assert fwd(res=far[1] + off) == _lib.EINVAL  # y may be residual, but not part of it
+
+    def gather(x, xs):  # x 512 bytes, xs 1024
+        return RAW.moe_vq_gather_rows(x, _lib.BF16, 4, 2, 64, far[4], xs, None)
+
+    def combine(rows, res, y):  # rows 1024, y 1024
+        return RAW.moe_vq_combine_rows(rows, _lib.BF16, 4, 2, 64, far[4], None, res, y, _lib.F32, None)
+
+    def back(dy, rows, drows):
+        return RAW.moe_vq_combine_rows_backward(dy, _lib.F32, 4, 2, 64, far[4], None, rows, _lib.BF16, drows, far[5], None)
+
+    for off in (-1008, 0, 496):
+        assert gather(far[0], far[0] + off) == _lib.EINVAL
+        assert combine(far[0], None, far[0] + off) == _lib.EINVAL
+        assert back(far[0], far[1], far[0] + off) == back(far[0], far[1], far[1] + off) == _lib.EINVAL
+    for off in (-1008, 1008):
+        assert combine(far[0], far[1] + off, far[1]) == _lib.EINVAL
+
+
 def test_python_refuses_what_the_library_cannot_see():
     import torch
 
