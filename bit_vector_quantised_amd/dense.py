@@ -223,13 +223,15 @@ class DenseExperts:
             raise ValueError("made without backward")
         if add and y is None:
             raise ValueError("add needs y")
+        self._kept = None  # (from here on the buffers are another pass's, even if a call below is refused)
         P = x.shape[0] * self.rows.top_k
         start = self.rows.sort(ids)
         self.rows.gather(x, self.xs[:P])
         self.fc1.forward(self.xs[:P], start, out=self.h[:P], z=self.z[:P] if keep else None)
         self.fc2.forward(self.h[:P], start, out=self.o[:P])
+        out = self.rows.combine(self.o[:P], w, y if add else None, y)
         self._kept = (x, w) if keep else None
-        return self.rows.combine(self.o[:P], w, y if add else None, y)
+        return out
 
     def backward(self, dy: torch.Tensor, dx: torch.Tensor, dw: torch.Tensor, dw1: torch.Tensor,
                  dw2: torch.Tensor) -> None:
@@ -237,6 +239,7 @@ class DenseExperts:
         if self._kept is None:
             raise ValueError("the last forward kept nothing")
         x, w = self._kept
+        self._kept = None
         P = x.shape[0] * self.rows.top_k
         start = self.rows.expert_start
         self.rows.combine_backward(dy, w, self.o[:P], self.do[:P], dw)
@@ -244,4 +247,3 @@ class DenseExperts:
         # (do and o have been read: o takes the gradient of the gathered rows)
         self.fc1.backward(self.xs[:P], self.dh[:P], self.z[:P], start, dx=self.o[:P], dw=dw1)
         self.rows.gather_backward(self.o[:P], dx)
-        self._kept = None

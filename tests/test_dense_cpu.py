@@ -144,6 +144,33 @@ def test_overlapping_buffers_are_refused():
         assert combine(far[0], far[1] + off, far[1]) == _lib.EINVAL
 
 
+def test_a_refused_experts_call_keeps_nothing():
+    """After a call that failed on the way, backward must not mix two passes' buffers."""
+    import torch
+
+    from bit_vector_quantised_amd.dense import DenseExperts
+
+    class Refusing:
+        top_k = 1
+        expert_start = None
+
+        def sort(self, ids):
+            raise ValueError("refused")
+
+        def combine_backward(self, *a):
+            raise ValueError("refused")
+
+    step = DenseExperts.__new__(DenseExperts)
+    step.rows, step.z, x = Refusing(), torch.zeros(2, 4), torch.zeros(2, 4)
+    step.o = step.do = x
+    for call in (lambda: step.forward(x, x, x, keep=True), lambda: step.backward(x, x, x, x, x)):
+        step._kept = (x, x)
+        with pytest.raises(ValueError, match="refused"):
+            call()
+        with pytest.raises(ValueError, match="kept nothing"):
+            step.backward(x, x, x, x, x)
+
+
 def test_python_refuses_what_the_library_cannot_see():
     import torch
 
