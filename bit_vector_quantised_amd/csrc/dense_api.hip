@@ -175,9 +175,11 @@ int moe_vq_linear_backward(const moe_vq_linear* L, const void* x, int n_rows, co
   const LinearPlan p = linear_plan(L, n_rows, true);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
   const size_t xb = (size_t)p.M * p.K * p.size, wb = (size_t)p.G * p.R * p.K * p.size;
-  const size_t zb = (size_t)p.M * p.R * p.size, yb = (size_t)p.M * p.N * size_of(dy_dtype);
-  if (overlap(dx, xb, x, xb) || overlap(dx, xb, z, zb) || overlap(dx, xb, dy, yb) || overlap(dx, xb, dw, wb)) return MOE_VQ_EINVAL;
-  if (overlap(dw, wb, x, xb) || overlap(dw, wb, z, zb) || overlap(dw, wb, dy, yb)) return MOE_VQ_EINVAL;
+  const size_t yb = (size_t)p.M * p.N * size_of(dy_dtype);
+  // (z, and dy where there is an activation, are read by dz's kernel, before dx and dw are written; x is
+  // read for dw only)
+  if (overlap(dx, xb, dw, wb) || (dw && (overlap(dx, xb, x, xb) || overlap(dw, wb, x, xb)))) return MOE_VQ_EINVAL;
+  if (L->act == MOE_VQ_ACT_NONE && (overlap(dx, xb, dy, yb) || overlap(dw, wb, dy, yb))) return MOE_VQ_EINVAL;
   LinearCall c{};
   c.L = L;
   c.x = x;

@@ -724,22 +724,22 @@ struct DzArgs {
   float* bias;     // [splits][G][R] column sums, or null
   const int32_t* group_start;
   int M, N, R, G, pitch, splits;
-  int dtype, dy_dtype, act;
   float lim;
 };
 
 constexpr int DZ_TX = 32, DZ_TY = 8;  // threads over columns, over rows
 
 // dz of eight columns of one row: the gate's (or the only) factor in d[0], the up's in d[1].
+template <int ACT>
 __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, const float* zg, const float* zu, float (*d)[8]) {
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     d[1][j] = 0.f;
-    if (a.act == MOE_VQ_ACT_NONE) {
+    if (ACT == MOE_VQ_ACT_NONE) {
       d[0][j] = dy[j];
-    } else if (a.act == MOE_VQ_ACT_SILU) {
+    } else if (ACT == MOE_VQ_ACT_SILU) {
       d[0][j] = dy[j] * silu_grad(zg[j], sigmoid_fast(zg[j]));
-    } else if (a.act == MOE_VQ_ACT_GELU) {
+    } else if (ACT == MOE_VQ_ACT_GELU) {
       d[0][j] = dy[j] * gelu_grad(zg[j]);
     } else {
       // h = silu(min(g, L)) * clamp(u, -L, L): no gradient through a value that was clamped
@@ -760,8 +760,11 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
 
 // One workgroup: 8 DZ_TX columns of one split of one group's rows, two rows of a thread at a time (their loads
 // are issued together).  Bound by reading dy and z and writing dz, each once (8192 rows of 16 groups, 2 x 2048
-// columns: 168 MB in 63 us).  dz is rounded to the element type for the matrix products; the column
+// columns: 168 MB in 46 us; 64 with types and activation chosen per value at run time, which keeps loads from
+// overlapping; rows of 1024 bytes, streamed loads or stores and half or twice the workgroups change
+// nothing or cost 2 to 3 us).  dz is rounded to the element type for the matrix products; the column
 // sums add the unrounded values in fp32, rows in a fixed order.
+template <int DTYPE, int DY_DTYPE, int ACT>
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
@@ -777,7 +780,7 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   }
   const int per = (r1 - r0 + a.splits - 1) / a.splits;
   const int m0 = r0 + split * per, m1 = m0 + per < r1 ? m0 + per : r1;
-  const bool two = a.act == MOE_VQ_ACT_SWIGLU, any = a.act != MOE_VQ_ACT_NONE;
+  constexpr bool two = ACT == MOE_VQ_ACT_SWIGLU, any = ACT != MOE_VQ_ACT_NONE;
   constexpr int V = 8;
   const int left = a.N - n;
   float sum[2][V];
@@ -788,11 +791,11 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
     for (int j = 0; j < V; ++j) { sum[0][j] += d[0][j]; sum[1][j] += d[1][j]; }
     if (!a.dz) return;
     const size_t row = (size_t)m * a.pitch;
-    store8(a.dz, row + n, a.dtype, left, d[0]);
-    if (two) store8(a.dz, row + a.N + n, a.dtype, left, d[1]);
+    store8(a.dz, row + n, DTYPE, left, d[0]);
+    if (two) store8(a.dz, row + a.N + n, DTYPE, left, d[1]);
     // (the pitch's last columns take part in dx's contraction as zeros)
     if (n == 0)
-      for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, a.dtype, 0.f);
+      for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, DTYPE, 0.f);
   };
   if (n < a.N) {
     for (int m = m0 + ty; m < m1; m += 2 * DZ_TY) {
@@ -801,12 +804,12 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const size_t r = i ? next : m;
-        load8(a.dy, r * a.N + n, a.dy_dtype, left, dy[i]);
-        if (any) load8(a.z, r * a.R + n, a.dtype, left, zg[i]);
-        if (two) load8(a.z, r * a.R + a.N + n, a.dtype, left, zu[i]);
+        load8(a.dy, r * a.N + n, DY_DTYPE, left, dy[i]);
+        if (any) load8(a.z, r * a.R + n, DTYPE, left, zg[i]);
+        if (two) load8(a.z, r * a.R + a.N + n, DTYPE, left, zu[i]);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) dz_values(a, dy[i], zg[i], zu[i], d[i]);
+      for (int i = 0; i < 2; ++i) dz_values<ACT>(a, dy[i], zg[i], zu[i], d[i]);
       put(m, d[0]);
       if (m + DZ_TY < m1) put(next, d[1]);
     }
@@ -934,6 +937,25 @@ void few_go(const GemmArgs& g, bool gated, hipStream_t st) {
   else few_rows_kernel<E, false><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
 }
 
+template <int DTYPE, int DY_DTYPE>
+void dz_go(const LinearPlan& p, const DzArgs& d, int act, hipStream_t st) {
+  const dim3 grid(div_up(p.N, DZ_TX * 8), p.G, d.splits);
+  if (act == MOE_VQ_ACT_NONE) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_NONE><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  else if (act == MOE_VQ_ACT_SILU) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_SILU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  else if (act == MOE_VQ_ACT_GELU) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_GELU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  else dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_SWIGLU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+}
+
+void launch_dz(const LinearPlan& p, const DzArgs& d, int dy_dtype, int act, hipStream_t st) {
+  if (p.dtype == MOE_VQ_BF16) {
+    if (dy_dtype == MOE_VQ_BF16) dz_go<MOE_VQ_BF16, MOE_VQ_BF16>(p, d, act, st);
+    else dz_go<MOE_VQ_BF16, MOE_VQ_F32>(p, d, act, st);
+  } else {
+    if (dy_dtype == MOE_VQ_BF16) dz_go<MOE_VQ_F32, MOE_VQ_BF16>(p, d, act, st);
+    else dz_go<MOE_VQ_F32, MOE_VQ_F32>(p, d, act, st);
+  }
+}
+
 void pack_rows(const LinearPlan& p, const void* src, void* dst, size_t rows, hipStream_t st) {
   const size_t blocks = (rows * p.Kp * p.size / 16 + 255) / 256;
   if (blocks == 0) return;
@@ -1051,8 +1073,8 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     d.bias = !c.dbias ? nullptr : (d.splits > 1 ? at<float>(c.ws, p.bias_part) : c.dbias);
     d.group_start = c.group_start;
     d.M = p.M; d.N = p.N; d.R = p.R; d.G = p.G; d.pitch = p.Rp;
-    d.dtype = p.dtype; d.dy_dtype = c.y_dtype; d.act = c.L->act; d.lim = c.L->swiglu_limit;
-    dz_kernel<<<dim3(div_up(p.N, DZ_TX * 8), p.G, d.splits), DZ_TX * DZ_TY, 0, st>>>(d);
+    d.lim = c.L->swiglu_limit;
+    launch_dz(p, d, c.y_dtype, c.L->act, st);
     if (c.dbias && d.splits > 1)
       bias_sum_kernel<<<div_up((long)p.G * p.R, 32), 256, 0, st>>>(d.bias, c.dbias, p.G * p.R, d.splits);
   }

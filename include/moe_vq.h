@@ -467,7 +467,8 @@ int moe_vq_linear_forward(const moe_vq_linear *lin, const void *x, int n_rows, c
  * no gradient.  dz is rounded to dtype once for the products (dbias adds it unrounded); every
  * output is summed in fp32 and rounded once.  Groups without rows get zeros in dw and dbias (with
  * n_rows = 0 all of them); rows in no group are neither read nor written.  The residual's
- * gradient is dy.  dx and dw must overlap neither each other nor x, z or dy (MOE_VQ_EINVAL).
+ * gradient is dy.  dx and dw must not overlap each other, nor x if dw is asked for, nor dy
+ * for MOE_VQ_ACT_NONE (MOE_VQ_EINVAL).
  * Alignment and errors as moe_vq_linear_forward. */
 int moe_vq_linear_backward(const moe_vq_linear *lin, const void *x, int n_rows, const int32_t *group_start,
                            const void *z, const void *dy, int dy_dtype, void *dx, void *dw, float *dbias,

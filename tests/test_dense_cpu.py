@@ -115,15 +115,17 @@ def test_overlapping_buffers_are_refused():
         d = lin(n_in=64, n_out=32, act=_lib.ACT_SWIGLU)  # 4 rows: x 512 bytes, y 512, z 512
         return RAW.moe_vq_linear_forward(ctypes.byref(d), x, 4, None, res, y, _lib.F32, z, far[6], 1 << 40, None)
 
-    def bwd(x=far[0], z=far[1], dy=far[2], dx=far[3], dw=far[4]):
-        d = lin(n_in=64, n_out=32, act=_lib.ACT_SWIGLU)  # dw 64 x 64: 8192 bytes
+    def bwd(x=far[0], z=far[1], dy=far[2], dx=far[3], dw=far[4], act=_lib.ACT_NONE):
+        d = lin(n_in=64, n_out=32, act=act)  # dw 32 x 64: 4096 bytes, or 8192
         return RAW.moe_vq_linear_backward(ctypes.byref(d), x, 4, None, z, dy, _lib.F32, dx, dw, None, far[6], 1 << 40, None)
 
     for off in (-496, 0, 496):
         assert fwd(y=far[0] + off) == fwd(z=far[0] + off) == fwd(z=far[1] + off) == _lib.EINVAL
         assert fwd(res=far[2] + off) == _lib.EINVAL  # z over the residual
-        assert bwd(dx=far[0] + off) == bwd(dx=far[1] + off) == bwd(dx=far[2] + off) == _lib.EINVAL
-        assert bwd(dw=far[0] + off) == bwd(dw=far[1] + off) == bwd(dw=far[2] + off) == bwd(dw=far[3] + off) == _lib.EINVAL
+        for act in (_lib.ACT_NONE, _lib.ACT_SWIGLU):
+            assert bwd(dx=far[0] + off, act=act) == bwd(dw=far[0] + off, act=act) == _lib.EINVAL
+            assert bwd(dx=far[4] + off, act=act) == _lib.EINVAL
+        assert bwd(dx=far[2] + off) == bwd(dw=far[2] + off) == _lib.EINVAL
     for off in (-496, 496):
         assert fwd(res=far[1] + off) == _lib.EINVAL  # y may be residual, but not part of it
 
