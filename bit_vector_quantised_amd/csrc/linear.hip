@@ -580,6 +580,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 // Few rows: the weights' bytes are what counts
 // ---------------------------------------------------------------------------------------
 
+// The part of a dword to keep whose first `drop` bytes go (a multiple of 2; all of it if 0 or less).
+__device__ __forceinline__ uint32_t few_keep(int drop) { return drop <= 0 ? 0xFFFFFFFFu : (drop >= 4 ? 0u : 0xFFFF0000u); }
+
 // Forward product of at most 16 rows.  Bound by streaming W from HBM once; a 64 x 64 tile spends as much on
 // the parts of its split contraction and their sum (one row, 7168 -> 2048 gated, weights not in
 // any cache: 19 us) as on the weights (11 to 12 us here, of which the 59 MB take 10).  A workgroup
@@ -590,7 +593,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
 // (13.4, 14.2, 15.3, 15.7, 18.3 us), eight waves best of 4, 8 and 16 (17.9, 13.4, 16.6).
 constexpr int FEW_ROWS = 16, FEW_WAVES = 8, FEW_STREAM = 4;
 
-template <typename E, bool GATED>
+//
+// ODD: rows of any width of at least 16 bytes, where they lie (repacked to 16-byte rows, W would move three
+// times: one row, 7071 -> 4096 bf16, 23 us instead of 38; eight in fp32 37 instead of 74).  A row's last chunk is then its last 16 bytes; what the chunk before has counted is
+// replaced by zeros, in both operands: an infinity times zero would be NaN.
+template <typename E, bool GATED, bool ODD>
 __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(GemmArgs g) {
   constexpr int STEP = 64;   // bytes of a row per load of its 16 rows
   constexpr int PITCH = 20;  // floats between the staged rows
@@ -616,14 +623,27 @@ __global__ __launch_bounds__(64 * FEW_WAVES) void few_rows_kernel(GemmArgs g) {
       // (a load behind this wave's share repeats its last one, a chunk behind the row's end its first one;
       // both are replaced by zeros below)
       const int at = (s + j < s1 ? s + j : s1 - 1) * STEP;
-      const int off = at + q * 16 < bytes ? at : -q * 16;
-      wv[j] = *reinterpret_cast<const u32x4_t*>(w + off);
-      xv[j] = *reinterpret_cast<const u32x4_t*>(x + off);
+      int off = at + q * 16 < bytes ? at : -q * 16;
+      if (ODD) {
+        off = off + q * 16 + 16 > bytes ? bytes - 16 - q * 16 : off;
+        const u32x4_any a = *reinterpret_cast<const u32x4_any*>(w + off), b = *reinterpret_cast<const u32x4_any*>(x + off);
+        wv[j] = u32x4_t{a.x, a.y, a.z, a.w};
+        xv[j] = u32x4_t{b.x, b.y, b.z, b.w};
+      } else {
+        wv[j] = *reinterpret_cast<const u32x4_t*>(w + off);
+        xv[j] = *reinterpret_cast<const u32x4_t*>(x + off);
+      }
     }
 #pragma unroll
     for (int j = 0; j < FEW_STREAM; ++j) {
       const bool ok = s + j < s1 && (s + j) * STEP + q * 16 < bytes;
       const u32x4_t none = {0, 0, 0, 0};
+      if (ODD) {
+        const int drop = (s + j) * STEP + q * 16 + 16 - bytes;  // bytes of the chunk that the one before holds
+        const u32x4_t keep = {few_keep(drop), few_keep(drop - 4), few_keep(drop - 8), few_keep(drop - 12)};
+        wv[j] &= keep;
+        xv[j] &= keep;
+      }
       E::mma(ok ? wv[j] : none, ok ? xv[j] : none, acc);
     }
   }
@@ -933,8 +953,11 @@ hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t s
 template <typename E>
 void few_go(const GemmArgs& g, bool gated, hipStream_t st) {
   const unsigned grid = (unsigned)div_up(g.out_n, gated ? 8 : 16);
-  if (gated) few_rows_kernel<E, true><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
-  else few_rows_kernel<E, false><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  const bool odd = g.b_pitch % 16 != 0;
+  if (gated && odd) few_rows_kernel<E, true, true><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  else if (gated) few_rows_kernel<E, true, false><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  else if (odd) few_rows_kernel<E, false, true><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
+  else few_rows_kernel<E, false, false><<<grid, 64 * FEW_WAVES, 0, st>>>(g);
 }
 
 template <int DTYPE, int DY_DTYPE>
@@ -1028,13 +1051,14 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   GemmArgs g{};
   g.a = static_cast<const char*>(c.x);
   g.b = static_cast<const char*>(c.L->w);
-  if (p.pack_k) {
+  const bool few = p.few && !c.group_start, as_is = few && p.K * p.size >= 16;
+  if (p.pack_k && !as_is) {
     pack_rows(p, c.x, at<char>(c.ws, p.xp), p.M, st);
     pack_rows(p, c.L->w, at<char>(c.ws, p.wp), (size_t)p.G * p.R, st);
     g.a = at<char>(c.ws, p.xp);
     g.b = at<char>(c.ws, p.wp);
   }
-  g.a_pitch = g.b_pitch = (uint32_t)p.Kp * p.size;
+  g.a_pitch = g.b_pitch = (uint32_t)(as_is ? p.K : p.Kp) * p.size;
   g.w_group = (uint64_t)p.R * g.b_pitch;
   g.group_start = c.group_start;
   g.G = p.G; g.M = p.M;
@@ -1051,7 +1075,7 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.z_dtype = p.dtype;
   g.act = c.L->act;
   g.lim = c.L->swiglu_limit;
-  if (p.few && !c.group_start) {
+  if (few) {
     if (p.dtype == MOE_VQ_BF16) few_go<Bf16>(g, c.L->act == MOE_VQ_ACT_SWIGLU, st);
     else few_go<F32>(g, c.L->act == MOE_VQ_ACT_SWIGLU, st);
     return hipGetLastError();

@@ -254,6 +254,27 @@ def test_linear_forward(M, K, N, start, act, dtype, y_dtype, bias, residual):
         assert torch.equal(same.cpu()[keep], out.cpu()[keep])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("K", [3, 5, 9, 15, 17, 31, 33, 63, 65, 255, 1001, 2047, 4102])
+def test_few_rows_of_odd_widths(K, dtype):
+    """Rows whose last 16 bytes overlap the 16 before them: every value counts once, and an infinity in one of the
+    last values stays one (the values left out there are not multiplied by zero)."""
+    say(f"few rows K={K} {dtype}")
+    for M, N, act in ((1, 33, "swiglu"), (16, 21, "none")):
+        g, R, x, w, b, r = linear_inputs(M, K, N, None, act, dtype, F32, True, True)
+        lin = Linear(w.cuda(), b.cuda(), act=act, max_rows=M)
+        out, z = torch.empty((M, N), device="cuda"), torch.empty((M, R), dtype=dtype, device="cuda")
+        lin.forward(x.cuda(), None, r.cuda(), out, z)
+        y, by, zz, bz = ref.linear_forward64(x, w, b, None, act, 0.0, r, F32, dtype)
+        ref.check(out, y, by, "y")
+        ref.check(z, zz, bz, "z")
+    w[:, max(0, K - 8):] = 0.5
+    for m in range(8):
+        x[m, max(0, K - 1 - m)] = float("inf")
+    y = Linear(w.cuda(), max_rows=M).forward(x.cuda(), out=torch.empty((M, N), device="cuda")).cpu()
+    assert (y[:8] == float("inf")).all() and torch.isfinite(y[8:]).all()
+
+
 @pytest.mark.parametrize("M,K,N,start,act,dtype,y_dtype,bias,residual", LINEAR_CASES)
 def test_linear_backward(M, K, N, start, act, dtype, y_dtype, bias, residual):
     say(f"linear backward M={M} K={K} N={N} {act} {dtype}")
