@@ -1,5 +1,7 @@
 // C ABI of the row operators and the dense product: argument checks, workspace layout and
 // the launches.  Every check runs on the host before any HIP call.
+#include <initializer_list>
+
 #include "dense.h"
 
 using namespace mvq;
@@ -13,10 +15,24 @@ bool dtype_ok(int d) { return d == MOE_VQ_F32 || d == MOE_VQ_BF16; }
 bool off16(const void* p) { return ((uintptr_t)p & 15) != 0; }
 bool off4(const void* p) { return ((uintptr_t)p & 3) != 0; }
 
-// Buffers [p, p + n) and [q, q + m) share a byte.  An output that overlaps an input would be written by
-// one workgroup while another still reads it.
-bool overlap(const void* p, size_t n, const void* q, size_t m) {
-  return p && q && (uintptr_t)p < (uintptr_t)q + m && (uintptr_t)q < (uintptr_t)p + n;
+// A buffer of n bytes (p null: not there).
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& a, const Span& b) {
+  return a.p && b.p && a.n && b.n && (uintptr_t)a.p < (uintptr_t)b.p + b.n && (uintptr_t)b.p < (uintptr_t)a.p + a.n;
+}
+// A buffer that is written shares a byte with another one, or with one that is read: a workgroup would write
+// it while another still reads, or writes, the same byte.
+bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (overlap(*o, i)) return true;
+    for (const Span* q = o + 1; q != outs.end(); ++q)
+      if (overlap(*o, *q)) return true;
+  }
+  return false;
 }
 size_t size_of(int d) { return d == MOE_VQ_BF16 ? 2 : 4; }
 
@@ -48,6 +64,13 @@ int check_linear_ws(const LinearPlan& p, const void* ws, size_t ws_bytes) {
   return ws_bytes < p.total ? MOE_VQ_ENOSPACE : MOE_VQ_OK;
 }
 
+// What a product reads beside its rows (bias: also the size of dbias).
+struct LinearSpans {
+  Span w, bias, table;
+  LinearSpans(const moe_vq_linear* L, const LinearPlan& p, const int32_t* group_start)
+      : w{L->w, (size_t)p.G * p.R * p.K * p.size}, bias{L->bias, (size_t)p.G * p.R * 4}, table{group_start, ((size_t)p.G + 1) * 4} {}
+};
+
 }  // namespace
 
 extern "C" {
@@ -75,7 +98,10 @@ int moe_vq_sort_pairs(const int32_t* topk_ids, int n_tokens, int top_k, int n_ex
   a.pair_row = pair_row;
   a.row_pair = row_pair;
   a.hist = static_cast<int32_t*>(ws);
-  if (ws_bytes < (size_t)sort_blocks(a.P) * n_experts * sizeof(int32_t)) return MOE_VQ_ENOSPACE;
+  const size_t hist = (size_t)sort_blocks(a.P) * n_experts * sizeof(int32_t), pairs = (size_t)a.P * 4;
+  if (ws_bytes < hist) return MOE_VQ_ENOSPACE;
+  if (clash({{expert_start, ((size_t)n_experts + 1) * 4}, {pair_row, pairs}, {row_pair, pairs}, {ws, hist}}, {{topk_ids, pairs}}))
+    return MOE_VQ_EINVAL;
   return hip_status(launch_sort(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -85,7 +111,7 @@ int moe_vq_gather_rows(const void* x, int dtype, int n_tokens, int top_k, int n_
   if (n_tokens == 0) return MOE_VQ_OK;
   if (!x || !pair_row || !xs || off16(x) || off16(xs) || off4(pair_row)) return MOE_VQ_EINVAL;
   const size_t bytes = (size_t)n_tokens * n_cols * size_of(dtype);
-  if (overlap(xs, bytes * top_k, x, bytes)) return MOE_VQ_EINVAL;
+  if (clash({{xs, bytes * top_k}}, {{x, bytes}, {pair_row, (size_t)n_tokens * top_k * 4}})) return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.x = x;
@@ -100,9 +126,10 @@ int moe_vq_combine_rows(const void* rows, int dtype, int n_tokens, int top_k, in
   if (n_tokens == 0) return MOE_VQ_OK;
   if (!rows || !pair_row || !y || off16(rows) || off16(y) || off16(residual)) return MOE_VQ_EINVAL;
   if (off4(pair_row) || off4(w)) return MOE_VQ_EINVAL;
-  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * size_of(y_dtype);
-  if (overlap(y, bytes, rows, cells * top_k * size_of(dtype))) return MOE_VQ_EINVAL;
-  if (y != residual && overlap(y, bytes, residual, bytes)) return MOE_VQ_EINVAL;
+  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * size_of(y_dtype), pairs = (size_t)n_tokens * top_k * 4;
+  if (clash({{y, bytes}}, {{rows, cells * top_k * size_of(dtype)}, {residual == y ? nullptr : residual, bytes},
+                           {pair_row, pairs}, {w, pairs}}))
+    return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.pair_w = w;
@@ -120,8 +147,11 @@ int moe_vq_combine_rows_backward(const void* dy, int dy_dtype, int n_tokens, int
   if (n_tokens == 0 || (!drows && !dw)) return MOE_VQ_OK;
   if (!dy || !pair_row || (dw && !rows) || off16(dy) || off16(rows) || off16(drows)) return MOE_VQ_EINVAL;
   if (off4(pair_row) || off4(w) || off4(dw)) return MOE_VQ_EINVAL;
-  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * top_k * size_of(dtype);
-  if (overlap(drows, bytes, rows, bytes) || overlap(drows, bytes, dy, cells * size_of(dy_dtype))) return MOE_VQ_EINVAL;
+  const size_t cells = (size_t)n_tokens * n_cols, bytes = cells * top_k * size_of(dtype), pairs = (size_t)n_tokens * top_k * 4;
+  // (a workgroup reads the weights of its own pairs before it writes their gradients: dw may be w itself)
+  if (clash({{drows, bytes}, {dw, pairs}}, {{rows, bytes}, {dy, cells * size_of(dy_dtype)}, {pair_row, pairs}}) ||
+      overlap({drows, bytes}, {w, pairs}) || (dw != w && overlap({dw, pairs}, {w, pairs})))
+    return MOE_VQ_EINVAL;
   RowsArgs a{};
   a.pair_row = pair_row;
   a.pair_w = w;
@@ -149,8 +179,10 @@ int moe_vq_linear_forward(const moe_vq_linear* L, const void* x, int n_rows, con
   const LinearPlan p = linear_plan(L, n_rows, false);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
   const size_t xb = (size_t)p.M * p.K * p.size, zb = (size_t)p.M * p.R * p.size, yb = (size_t)p.M * p.N * size_of(y_dtype);
-  if (overlap(y, yb, x, xb) || (y != residual && overlap(y, yb, residual, yb))) return MOE_VQ_EINVAL;
-  if (overlap(z, zb, x, xb) || overlap(z, zb, y, yb) || overlap(z, zb, residual, yb)) return MOE_VQ_EINVAL;
+  const LinearSpans in(L, p, group_start);
+  if (clash({{y, yb}, {z, zb}, {ws, p.total}}, {{x, xb}, in.w, in.bias, in.table}) ||
+      clash({{z, zb}, {ws, p.total}}, {{residual, yb}}) || (y != residual && overlap({y, yb}, {residual, yb})))
+    return MOE_VQ_EINVAL;
   LinearCall c{};
   c.L = L;
   c.x = x;
@@ -174,12 +206,16 @@ int moe_vq_linear_backward(const moe_vq_linear* L, const void* x, int n_rows, co
   if (n_rows > 0 && (!dy || (dw && !x) || (L->act != MOE_VQ_ACT_NONE && !z))) return MOE_VQ_EINVAL;
   const LinearPlan p = linear_plan(L, n_rows, true);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
-  const size_t xb = (size_t)p.M * p.K * p.size, wb = (size_t)p.G * p.R * p.K * p.size;
-  const size_t yb = (size_t)p.M * p.N * size_of(dy_dtype);
-  // (z, and dy where there is an activation, are read by dz's kernel, before dx and dw are written; x is
-  // read for dw only)
-  if (overlap(dx, xb, dw, wb) || (dw && (overlap(dx, xb, x, xb) || overlap(dw, wb, x, xb)))) return MOE_VQ_EINVAL;
-  if (L->act == MOE_VQ_ACT_NONE && (overlap(dx, xb, dy, yb) || overlap(dw, wb, dy, yb))) return MOE_VQ_EINVAL;
+  const LinearSpans in(L, p, group_start);
+  const bool act = L->act != MOE_VQ_ACT_NONE;
+  const Span dx_s{dx, (size_t)p.M * p.K * p.size}, dw_s{dw, in.w.n}, db_s{dbias, in.bias.n}, ws_s{ws, p.total};
+  const Span dy_s{dy, (size_t)p.M * p.N * size_of(dy_dtype)}, z_s{act ? z : nullptr, (size_t)p.M * p.R * p.size};
+  const Span x_s{dw ? x : nullptr, dx_s.n}, w_s{dx ? L->w : nullptr, in.w.n};  // (each read for one product only)
+  // In order: dz and its column sums from dy and z, then dx from w, then dw from x.  So dx and dw may lie over
+  // z, and over dy where dz is another tensor, and dw over w; without an activation both products read dy.
+  if (clash({dx_s, dw_s, db_s, ws_s}, {x_s, in.table}) || clash({db_s, ws_s}, {dy_s, z_s, w_s}) || overlap(dx_s, w_s) ||
+      (!act && (overlap(dx_s, dy_s) || overlap(dw_s, dy_s))))
+    return MOE_VQ_EINVAL;
   LinearCall c{};
   c.L = L;
   c.x = x;

@@ -378,7 +378,9 @@ int moe_vq_cpu_experts(const moe_vq_layer *layer, const uint8_t *host_pool, uint
  * fp32 products on the matrix cores) in a fixed order, without atomics.  None of them
  * leaves anything in the workspace for a later call, so one workspace may serve several
  * calls that are stream-ordered; two calls (or two replayed graphs) that may overlap need
- * two.  Every call may be captured into a graph. */
+ * two.  Every call may be captured into a graph.  A buffer that a call writes (its workspace
+ * among them) must not overlap another of the call's buffers, unless its text allows it: such
+ * calls return MOE_VQ_EINVAL. */
 
 /* [host] Workspace bytes of moe_vq_sort_pairs, 0 if an argument is invalid. */
 size_t moe_vq_sort_bytes(int n_tokens, int top_k, int n_experts);
@@ -397,7 +399,7 @@ int moe_vq_sort_pairs(const int32_t *topk_ids, int n_tokens, int top_k, int n_ex
 /* xs[pair_row[t*k + i]] = x[t]: the token's row copied to each of its pairs' rows.  x
  * [n_tokens][n_cols], xs [n_tokens*k][n_cols], both in dtype and 16-byte aligned, n_cols
  * 1..65536.  A pair_row outside 0..n_tokens*k-1 is a dropped pair; rows of xs that no pair
- * names are left as they were.  xs must not overlap x (MOE_VQ_EINVAL).  The gradient is moe_vq_combine_rows without weights:
+ * names are left as they were.  The gradient is moe_vq_combine_rows without weights:
  * dx[t] = sum_i dxs[pair_row[t*k + i]]. */
 int moe_vq_gather_rows(const void *x, int dtype, int n_tokens, int top_k, int n_cols,
                        const int32_t *pair_row, void *xs, void *stream);
@@ -407,7 +409,7 @@ int moe_vq_gather_rows(const void *x, int dtype, int n_tokens, int top_k, int n_
  * 1); residual and y [n_tokens][n_cols] in y_dtype (residual may be NULL, and may be y
  * itself).  rows, residual, y 16-byte aligned.  A dropped pair adds nothing, and its weight and
  * whatever lies in unnamed rows are not looked at; a token without pairs gets its residual,
- * or zeros.  y must not overlap rows, nor residual in part (MOE_VQ_EINVAL). */
+ * or zeros. */
 int moe_vq_combine_rows(const void *rows, int dtype, int n_tokens, int top_k, int n_cols,
                         const int32_t *pair_row, const float *w, const void *residual, void *y, int y_dtype,
                         void *stream);
@@ -415,8 +417,7 @@ int moe_vq_combine_rows(const void *rows, int dtype, int n_tokens, int top_k, in
 /* Gradients of moe_vq_combine_rows: drows[pair_row[p]] = w[p] * dy[t] (dtype; rows that no
  * pair names are left as they were) and dw[p] = <dy[t], rows[pair_row[p]]> (fp32, 0 for a
  * dropped pair).  drows or dw may be NULL (rows is needed for dw only; w NULL: all 1).  The
- * residual's gradient is dy.  dy [n_tokens][n_cols] in dy_dtype.  drows must overlap
- * neither rows nor dy (MOE_VQ_EINVAL). */
+ * residual's gradient is dy.  dy [n_tokens][n_cols] in dy_dtype.  dw may be w itself. */
 int moe_vq_combine_rows_backward(const void *dy, int dy_dtype, int n_tokens, int top_k, int n_cols,
                                  const int32_t *pair_row, const float *w, const void *rows, int dtype,
                                  void *drows, float *dw, void *stream);
@@ -453,8 +454,7 @@ size_t moe_vq_linear_bytes(const moe_vq_linear *lin, int n_rows, int backward);
  * rows in no group are neither read nor written.  It may be NULL with n_groups = 1: every row.
  * z [n_rows][R] in dtype, or NULL: the values before the activation, kept for the backward
  * call.  Products of bf16 values are exact and summed in fp32; y and z are each rounded once.
- * x, w, residual, y, z 16-byte aligned; 0 <= n_rows <= 2097152 (65536 tokens, top-32); no
- * buffer may overlap y or z except residual as said (MOE_VQ_EINVAL where x, residual, y or z do).
+ * x, w, residual, y, z 16-byte aligned; 0 <= n_rows <= 2097152 (65536 tokens, top-32).
  * Errors: MOE_VQ_EINVAL, MOE_VQ_ENOSPACE, MOE_VQ_EHIP. */
 int moe_vq_linear_forward(const moe_vq_linear *lin, const void *x, int n_rows, const int32_t *group_start,
                           const void *residual, void *y, int y_dtype, void *z, void *ws, size_t ws_bytes,
@@ -467,8 +467,8 @@ int moe_vq_linear_forward(const moe_vq_linear *lin, const void *x, int n_rows, c
  * no gradient.  dz is rounded to dtype once for the products (dbias adds it unrounded); every
  * output is summed in fp32 and rounded once.  Groups without rows get zeros in dw and dbias (with
  * n_rows = 0 all of them); rows in no group are neither read nor written.  The residual's
- * gradient is dy.  dx and dw must not overlap each other, nor x if dw is asked for, nor dy
- * for MOE_VQ_ACT_NONE (MOE_VQ_EINVAL).
+ * gradient is dy.  Overlaps allowed here, whole or in part: dx and dw with z, and with dy unless
+ * act is MOE_VQ_ACT_NONE; dx with x if dw is NULL; dw with w.
  * Alignment and errors as moe_vq_linear_forward. */
 int moe_vq_linear_backward(const moe_vq_linear *lin, const void *x, int n_rows, const int32_t *group_start,
                            const void *z, const void *dy, int dy_dtype, void *dx, void *dw, float *dbias,

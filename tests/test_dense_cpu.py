@@ -191,3 +191,95 @@ def test_python_refuses_what_the_library_cannot_see():
     for bad in (t.t(), t[:, :3], t.bfloat16(), t[:3]):
         with pytest.raises(ValueError):
             _need(bad, "t", (4, 6), torch.float32, cpu)
+
+
+class Buffers:
+    """Named buffers far apart: their sizes, the alignment each needs, and calls with one of them moved onto another."""
+
+    def __init__(self, **sizes):
+        self.size = {n: v[0] for n, v in sizes.items()}
+        self.align = {n: v[1] for n, v in sizes.items()}
+        self.at = {n: A + ((i + 1) << 32) for i, n in enumerate(sizes)}
+
+    def refused(self, call, a, b, same=True):
+        """a's last bytes on b's first, both at one address (unless `same` allows that), a's first on b's last."""
+        step = self.align[a]
+        spots = {-self.size[a] + step, 0, (self.size[b] - 1) // step * step}
+        for off in spots if same else spots - {0}:
+            assert call({**self.at, a: self.at[b] + off}) == _lib.EINVAL, (a, "at", b, off)
+
+
+def test_every_written_buffer_is_kept_apart():
+    """Each buffer that a call writes against each other one that it reads or writes (only refusals, which return
+    before any launch)."""
+    big = 1 << 40
+    b = Buffers(ids=(16, 4), start=(16, 4), pair=(16, 4), row=(16, 4), ws=(256, 256))
+
+    def sort(p):
+        return RAW.moe_vq_sort_pairs(p["ids"], 4, 1, 3, p["start"], p["pair"], p["row"], p["ws"], big, None)
+
+    for a, c in (("start", "ids"), ("pair", "ids"), ("row", "ids"), ("start", "pair"), ("start", "row"), ("pair", "row"),
+                 ("ws", "ids"), ("ws", "start"), ("ws", "pair"), ("ws", "row")):
+        b.refused(sort, a, c)
+
+    # 4 tokens, top-2, 64 columns
+    b = Buffers(x=(512, 16), rows=(1024, 16), res=(1024, 16), y=(1024, 16), pair=(32, 4), w=(32, 4), dy=(1024, 16),
+                drows=(1024, 16), dw=(32, 4))
+
+    def gather(p):
+        return RAW.moe_vq_gather_rows(p["x"], _lib.BF16, 4, 2, 64, p["pair"], p["rows"], None)
+
+    def combine(p):
+        return RAW.moe_vq_combine_rows(p["rows"], _lib.BF16, 4, 2, 64, p["pair"], p["w"], p["res"], p["y"], _lib.F32, None)
+
+    def back(p):
+        return RAW.moe_vq_combine_rows_backward(p["dy"], _lib.F32, 4, 2, 64, p["pair"], p["w"], p["rows"], _lib.BF16,
+                                                p["drows"], p["dw"], None)
+
+    for a, c in (("rows", "x"), ("rows", "pair")):
+        b.refused(gather, a, c)
+    for a in ("rows", "pair", "w"):
+        b.refused(combine, a, "y")
+    b.refused(combine, "res", "y", same=False)
+    for a in ("dy", "rows", "pair", "w", "dw"):
+        b.refused(back, a, "drows")
+    for a in ("dy", "rows", "pair"):
+        b.refused(back, "dw", a)
+    b.refused(back, "dw", "w", same=False)
+
+    # 4 rows, 64 -> 32, bf16 with fp32 outputs; dx and dw of x's and w's sizes
+    for act, R in ((_lib.ACT_NONE, 32), (_lib.ACT_SILU, 32), (_lib.ACT_SWIGLU, 64)):
+        sizes = dict(x=(512, 16), w=(R * 128, 16), bias=(R * 4, 4), table=(8, 4), res=(512, 16), y=(512, 16), z=(R * 8, 16),
+                     dy=(512, 16), dx=(512, 16), dw=(R * 128, 16), db=(R * 4, 4))
+
+        def fwd(p):
+            d = lin(n_in=64, n_out=32, act=act, w=p["w"], bias=p["bias"])
+            return RAW.moe_vq_linear_forward(ctypes.byref(d), p["x"], 4, p["table"], p["res"], p["y"], _lib.F32, p["z"], p["ws"],
+                                             big, None)
+
+        def bwd(p):
+            d = lin(n_in=64, n_out=32, act=act, w=p["w"], bias=p["bias"])
+            return RAW.moe_vq_linear_backward(ctypes.byref(d), p["x"], 4, p["table"], p["z"], p["dy"], _lib.F32, p["dx"], p["dw"],
+                                              p["db"], p["ws"], big, None)
+
+        b = Buffers(**sizes, ws=(256, 256))
+        for a in ("x", "w", "bias", "table"):
+            b.refused(fwd, a, "y")
+            b.refused(fwd, a, "z")
+            b.refused(fwd, "ws", a)
+        b.refused(fwd, "y", "z")
+        b.refused(fwd, "res", "z")
+        b.refused(fwd, "res", "y", same=False)
+        for a in ("res", "y", "z"):
+            b.refused(fwd, "ws", a)
+        read = ["x", "table", "dy"] + (["z"] if act != _lib.ACT_NONE else [])
+        for a in ["w", "dx", "dw"] + read:
+            b.refused(bwd, "db", a)
+            b.refused(bwd, "ws", a)
+        for a in ("w", "x", "table", "dw"):
+            b.refused(bwd, "dx", a)
+        for a in ("x", "table"):
+            b.refused(bwd, "dw", a)
+        if act == _lib.ACT_NONE:
+            b.refused(bwd, "dx", "dy")
+            b.refused(bwd, "dw", "dy")

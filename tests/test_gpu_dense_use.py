@@ -1,0 +1,57 @@
+"""The row operators and the dense product as programs use them: buffers that lie over each
+other where that is allowed, weights and routings that change between calls, streams."""
+import pytest
+import torch
+
+import dense_ref as ref
+from bit_vector_quantised_amd.dense import DenseExperts, ExpertRows, Linear  # noqa: F401
+
+from gpu_util import say
+from test_gpu_dense import BF16, F32, gen, linear_inputs, randn, routing
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("act", ["none", "silu", "swiglu"])
+def test_gradients_over_their_inputs(act):
+    """The overlaps that are allowed give the gradients of separate buffers, to the bit: dw over w, dx over z, and
+    over dy where an activation makes dz another tensor.  Sizes at which every product has many workgroups."""
+    say(f"gradients over inputs {act}")
+    M, N = 600, 512
+    K = 2 * N if act == "swiglu" else N  # (z and dx of one size)
+    g, R, x, w, b, _ = linear_inputs(M, K, N, None, act, BF16, BF16, True, False)
+    z, dy = randn(g, M, R, dtype=BF16).cuda(), randn(g, M, N, dtype=BF16).cuda()
+    x, w = x.cuda(), w.cuda()
+
+    def grads(**over):
+        xx, ww, zz, dd = x.clone(), w.clone(), z.clone(), dy.clone()
+        at = {"w": ww, "z": zz, "dy": dd}
+        dx = at[over["dx"]] if "dx" in over else torch.empty_like(x)
+        dw = at[over["dw"]] if "dw" in over else torch.empty_like(w)
+        db = torch.empty(R, device="cuda")
+        lin = Linear(ww, b.cuda(), act=act, max_rows=M, backward=True)
+        lin.backward(xx, dd, None if act == "none" else zz, dx=dx, dw=dw, dbias=db)
+        return dx.clone(), dw.clone(), db
+
+    want = grads()
+    cases = [dict(dw="w")]
+    if act != "none":
+        cases += [dict(dx="z"), dict(dx="z", dw="w")]
+        if act != "swiglu":
+            cases += [dict(dx="dy"), dict(dx="dy", dw="w")]
+    for over in cases:
+        for a, c in zip(grads(**over), want):
+            assert torch.equal(a, c), over
+
+
+def test_weight_gradients_over_the_weights():
+    say("dw of combine over w")
+    T, k, C = 700, 8, 264
+    rows = ExpertRows(16, k, T)
+    g = gen(4)
+    rows.sort(routing(g, T, k, 16, dropped=0.1).cuda())
+    o, dy, w = randn(g, T * k, C, dtype=BF16).cuda(), randn(g, T, C).cuda(), torch.rand(T, k, generator=g).cuda()
+    want = rows.combine_backward(dy, w, o, torch.zeros_like(o))
+    same = w.clone()
+    got = rows.combine_backward(dy, same, o, torch.zeros_like(o), same)
+    assert torch.equal(got[0], want[0]) and torch.equal(same, want[1])
