@@ -130,7 +130,8 @@ class Linear(_OnDevice):
     """y = act(x W^T + b) + residual for up to max_rows rows.  w: [R, n_in], or [G, R, n_in] for one
     matrix per group of rows; bf16 or fp32.  R is n_out, or 2 n_out for act "swiglu" (gate rows, then
     up rows; swiglu_limit: its clamp, 0 none).  bias: fp32 [R] or [G, R].  backward: make the
-    workspace of the gradients too."""
+    workspace of the gradients too.  Each call reads w and bias where they are at that time (a
+    captured graph where they were when it was captured)."""
 
     def __init__(self, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
                  swiglu_limit: float = 0.0, max_rows: int = 1, backward: bool = False):
@@ -144,15 +145,20 @@ class Linear(_OnDevice):
         self.n_groups = w.shape[0] if self.grouped else 1
         self.n_rows_w, self.n_in = w.shape[-2], w.shape[-1]
         self.n_out = self.n_rows_w // 2 if act == "swiglu" else self.n_rows_w
-        wp = _need(w, "w", w.shape, w.dtype, self.device)
-        bp = _need(bias, "bias", w.shape[:-1], torch.float32, self.device) if bias is not None else None
-        self.c = _lib.LinearDesc(self.n_in, self.n_out, self.n_groups, ACTS[act], x_dtype_code(w), float(swiglu_limit),
-                                 wp, bp)
+        self.w_shape, self.dtype = w.shape, w.dtype
+        self.c = _lib.LinearDesc(self.n_in, self.n_out, self.n_groups, ACTS[act], x_dtype_code(w), float(swiglu_limit))
+        self._weights()
         need = [_lib.linear_bytes(self.c, max_rows, b) for b in (False, True)[:2 if backward else 1]]
         if 0 in need:
             raise ValueError("invalid sizes")
         self.ws_bytes = max(need)
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+
+    def _weights(self) -> _lib.LinearDesc:
+        """The description of the product, with the present addresses of w and bias."""
+        self.c.w = _need(self.w, "w", self.w_shape, self.dtype, self.device)
+        self.c.bias = _need(self.bias, "bias", self.w_shape[:-1], torch.float32, self.device) if self.bias is not None else None
+        return self.c
 
     def _rows(self, x: torch.Tensor, group_start: Optional[torch.Tensor]) -> Tuple[int, int]:
         if x.shape[0] > self.max_rows:
@@ -170,13 +176,13 @@ class Linear(_OnDevice):
         in no group are neither read nor written.  out: bf16 or fp32 (by default as residual, or as x); it
         may be residual.  z [M, R]: receives the values before the activation, for backward."""
         M, gs = self._rows(x, group_start)
-        xp = _need(x, "x", (M, self.n_in), self.w.dtype, self.device)
+        xp = _need(x, "x", (M, self.n_in), self.dtype, self.device)
         if out is None:
             out = torch.empty((M, self.n_out), dtype=x.dtype if residual is None else residual.dtype, device=self.device)
         y = _need(out, "out", (M, self.n_out), out.dtype, self.device)
         r = _need(residual, "residual", (M, self.n_out), out.dtype, self.device) if residual is not None else 0
-        zp = _need(z, "z", (M, self.n_rows_w), self.w.dtype, self.device) if z is not None else 0
-        self._call(_lib.linear_forward, self.c, xp, M, gs, r, y, x_dtype_code(out), zp, self.ws.data_ptr(),
+        zp = _need(z, "z", (M, self.n_rows_w), self.dtype, self.device) if z is not None else 0
+        self._call(_lib.linear_forward, self._weights(), xp, M, gs, r, y, x_dtype_code(out), zp, self.ws.data_ptr(),
                    self.ws_bytes)
         return out
 
@@ -186,13 +192,13 @@ class Linear(_OnDevice):
         """Gradients from dy [M, n_out] and the z that forward kept (not needed for act "none"): those of dx
         [M, n_in], dw (as w) and dbias (as bias) that are given are written."""
         M, gs = self._rows(x, group_start)
-        xp = _need(x, "x", (M, self.n_in), self.w.dtype, self.device)
+        xp = _need(x, "x", (M, self.n_in), self.dtype, self.device)
         g = _need(dy, "dy", (M, self.n_out), dy.dtype, self.device)
-        zp = _need(z, "z", (M, self.n_rows_w), self.w.dtype, self.device) if z is not None else 0
-        xd = _need(dx, "dx", (M, self.n_in), self.w.dtype, self.device) if dx is not None else 0
-        wd = _need(dw, "dw", self.w.shape, self.w.dtype, self.device) if dw is not None else 0
-        bd = _need(dbias, "dbias", self.w.shape[:-1], torch.float32, self.device) if dbias is not None else 0
-        self._call(_lib.linear_backward, self.c, xp, M, gs, zp, g, x_dtype_code(dy), xd, wd, bd, self.ws.data_ptr(),
+        zp = _need(z, "z", (M, self.n_rows_w), self.dtype, self.device) if z is not None else 0
+        xd = _need(dx, "dx", (M, self.n_in), self.dtype, self.device) if dx is not None else 0
+        wd = _need(dw, "dw", self.w_shape, self.dtype, self.device) if dw is not None else 0
+        bd = _need(dbias, "dbias", self.w_shape[:-1], torch.float32, self.device) if dbias is not None else 0
+        self._call(_lib.linear_backward, self._weights(), xp, M, gs, zp, g, x_dtype_code(dy), xd, wd, bd, self.ws.data_ptr(),
                    self.ws_bytes)
 
 

@@ -55,3 +55,27 @@ def test_weight_gradients_over_the_weights():
     same = w.clone()
     got = rows.combine_backward(dy, same, o, torch.zeros_like(o), same)
     assert torch.equal(got[0], want[0]) and torch.equal(same, want[1])
+
+
+def test_weights_that_move():
+    """Weights and a bias whose storage is replaced after the object was made: the next call reads the new one."""
+    say("weights moved")
+    M, K, N = 5, 64, 24
+    g, R, x, w, b, _ = linear_inputs(M, K, N, None, "silu", F32, F32, True, False)
+    x, w, b = x.cuda(), w.cuda(), b.cuda()
+    lin = Linear(w, b, act="silu", max_rows=M, backward=True)
+    first = lin.forward(x).clone()
+    old = (w.data, b.data)  # (kept alive: nothing else can be given their memory)
+    w.data, b.data = w.data * 2, b.data + 1
+    assert w.data_ptr() != old[0].data_ptr() and b.data_ptr() != old[1].data_ptr()
+    z = torch.empty(M, R, device="cuda")
+    y = lin.forward(x, z=z)
+    want = Linear(w.clone(), b.clone(), act="silu", max_rows=M, backward=True)
+    assert torch.equal(y, want.forward(x)) and not torch.equal(y, first)
+    dx, dwant = torch.empty_like(x), torch.empty_like(x)
+    lin.backward(x, y, z, dx=dx)
+    want.backward(x, y, z, dx=dwant)
+    assert torch.equal(dx, dwant)
+    w.data = old[0].double()
+    with pytest.raises(ValueError, match="w: need"):
+        lin.forward(x)
