@@ -206,7 +206,8 @@ class DenseExperts:
     """The routed-expert step of a layer with unquantised experts: w1 [E, 2I, H] (gate rows, then up
     rows) and w2 [E, H, I], bf16 or fp32.  forward(x, ids, w) computes y = sum_i w_i E_i(x) (+ y
     itself with add=True) from a routing such as Step.route's; after a forward with keep=True,
-    backward(dy) gives the gradients of x, the routing weights and the experts."""
+    backward(dy) gives the gradients of x, the routing weights and the experts.  What backward needs
+    of the pass is kept here: x, ids and w may change in between (w1 and w2 may not)."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, top_k: int, max_tokens: int, swiglu_limit: float = 0.0,
                  backward: bool = False):
@@ -220,6 +221,7 @@ class DenseExperts:
         new = lambda *shape: torch.empty(shape, dtype=w1.dtype, device=w1.device)  # noqa: E731
         self.xs, self.h, self.o = new(P, H), new(P, R // 2), new(P, H)
         self.z, self.dh, self.do = (new(P, R), new(P, R // 2), new(P, H)) if backward else (None, None, None)
+        self.w_kept = torch.empty((max_tokens, top_k), dtype=torch.float32, device=w1.device) if backward else None
         self._kept = None
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = None,
@@ -236,7 +238,8 @@ class DenseExperts:
         self.fc1.forward(self.xs[:P], start, out=self.h[:P], z=self.z[:P] if keep else None)
         self.fc2.forward(self.h[:P], start, out=self.o[:P])
         out = self.rows.combine(self.o[:P], w, y if add else None, y)
-        self._kept = (x, w) if keep else None
+        if keep:
+            self._kept = (x, self.w_kept[:x.shape[0]].copy_(w))  # (of x only the number of tokens is used)
         return out
 
     def backward(self, dy: torch.Tensor, dx: torch.Tensor, dw: torch.Tensor, dw1: torch.Tensor,

@@ -79,3 +79,26 @@ def test_weights_that_move():
     w.data = old[0].double()
     with pytest.raises(ValueError, match="w: need"):
         lin.forward(x)
+
+
+def test_the_next_routing_before_backward():
+    """The routing's buffers are the caller's: the next step may overwrite them before this one's backward."""
+    say("routing overwritten before backward")
+    T, H, I, E, k = 19, 64, 32, 5, 2
+    g = gen(17)
+    w1, w2 = randn(g, E, 2 * I, H, scale=0.1).cuda(), randn(g, E, H, I, scale=0.1).cuda()
+    step = DenseExperts(w1, w2, k, T + 3, backward=True)
+    x, dy = randn(g, T, H).cuda(), randn(g, T, H).cuda()
+    ids, w = routing(g, T, k, E).cuda(), torch.rand(T, k, generator=g).cuda()
+
+    def grads(change):
+        i, v, xx = ids.clone(), w.clone(), x.clone()
+        step.forward(xx, i, v, keep=True)
+        if change:
+            i.fill_(-1); v.fill_(7.0); xx.fill_(3.0)
+        out = torch.empty_like(x), torch.empty_like(w), torch.empty_like(w1), torch.empty_like(w2)
+        step.backward(dy, *out)
+        return out
+
+    for a, b in zip(grads(False), grads(True)):
+        assert torch.equal(a, b)
