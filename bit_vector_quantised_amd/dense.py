@@ -5,11 +5,13 @@ sorted rows), and their gradients.
 As in layer.py, PyTorch provides device memory and the stream; every step of the
 computation runs in the HIP library.  An object's workspace serves its calls one after the
 other on a stream: calls of one object that may overlap (on two streams, or in two graphs
-replayed at once) need two objects.
+replayed at once) need two objects.  An object may be dropped while its calls are still under way on
+any stream; one whose calls are in a captured graph has to be kept as long as the graph.  As with a
+tensor, another stream than the one it was made on waits for that one before its first call.
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import List, Optional, Tuple
 
 import torch
 
@@ -39,14 +41,27 @@ class _OnDevice:
         if device.type != "cuda":
             raise ValueError(f"need a GPU tensor or device, got {device}")
         self.device = device
+        self._buffers: List[torch.Tensor] = []
+        self._streams = {torch.cuda.current_stream(device).cuda_stream}  # the buffers' allocator knows of these
+
+    def _new(self, shape, dtype) -> torch.Tensor:
+        """A buffer of the object, in use by the streams of its calls."""
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        self._buffers.append(t)
+        return t
 
     def _call(self, fn, *args) -> None:
         index = self.device.index
+        stream = torch.cuda.current_stream(index)
+        if stream.cuda_stream not in self._streams:
+            for t in self._buffers:
+                t.record_stream(stream)
+            self._streams.add(stream.cuda_stream)
         if torch.cuda.current_device() == index:
-            fn(*args, torch.cuda.current_stream(index).cuda_stream)
+            fn(*args, stream.cuda_stream)
         else:
             with torch.cuda.device(index):
-                fn(*args, torch.cuda.current_stream(index).cuda_stream)
+                fn(*args, stream.cuda_stream)
 
 
 class ExpertRows(_OnDevice):
@@ -60,10 +75,10 @@ class ExpertRows(_OnDevice):
         self.ws_bytes = _lib.sort_bytes(max_tokens, top_k, n_experts)
         if self.ws_bytes == 0:
             raise ValueError("invalid number of experts, tokens or top_k")
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
-        self.expert_start = torch.zeros(n_experts + 1, dtype=torch.int32, device=self.device)
-        self.pair_row = torch.empty(max_tokens * top_k, dtype=torch.int32, device=self.device)
-        self.row_pair = torch.empty(max_tokens * top_k, dtype=torch.int32, device=self.device)
+        self.ws = self._new(self.ws_bytes, torch.uint8)
+        self.expert_start = self._new(n_experts + 1, torch.int32).zero_()
+        self.pair_row = self._new(max_tokens * top_k, torch.int32)
+        self.row_pair = self._new(max_tokens * top_k, torch.int32)
 
     def sort(self, ids: torch.Tensor) -> torch.Tensor:
         """Sort the pairs of ids [T, k] (int32; outside 0..E-1: dropped); returns expert_start."""
@@ -152,7 +167,7 @@ class Linear(_OnDevice):
         if 0 in need:
             raise ValueError("invalid sizes")
         self.ws_bytes = max(need)
-        self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        self.ws = self._new(self.ws_bytes, torch.uint8)
 
     def _weights(self) -> _lib.LinearDesc:
         """The description of the product, with the present addresses of w and bias."""
@@ -218,10 +233,11 @@ class DenseExperts:
         self.fc1 = Linear(w1, act="swiglu", swiglu_limit=swiglu_limit, max_rows=P, backward=backward)
         self.fc2 = Linear(w2, max_rows=P, backward=backward)
         self.rows = ExpertRows(E, top_k, max_tokens, device=w1.device)
-        new = lambda *shape: torch.empty(shape, dtype=w1.dtype, device=w1.device)  # noqa: E731
+        # (buffers of rows: each pass of the step calls it, on the pass's stream)
+        new = lambda *shape: self.rows._new(shape, w1.dtype)  # noqa: E731
         self.xs, self.h, self.o = new(P, H), new(P, R // 2), new(P, H)
         self.z, self.dh, self.do = (new(P, R), new(P, R // 2), new(P, H)) if backward else (None, None, None)
-        self.w_kept = torch.empty((max_tokens, top_k), dtype=torch.float32, device=w1.device) if backward else None
+        self.w_kept = self.rows._new((max_tokens, top_k), torch.float32) if backward else None
         self._kept = None
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = None,

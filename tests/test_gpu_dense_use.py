@@ -102,3 +102,49 @@ def test_the_next_routing_before_backward():
 
     for a, b in zip(grads(False), grads(True)):
         assert torch.equal(a, b)
+
+
+def test_buffers_outlive_the_calls_of_a_dropped_object():
+    """An object used on a side stream and dropped at once: its buffers are not given out again while the side
+    stream's work is under way (here a wait of the stream, then nothing: the buffers are only looked at by address)."""
+    say("buffers of dropped objects")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    g = gen(31)
+    T, H, I, E, k = 64, 64, 32, 4, 2
+    w1, w2 = randn(g, E, 2 * I, H, dtype=BF16).cuda(), randn(g, E, H, I, dtype=BF16).cuda()
+    x, ids, w = randn(g, T, H, dtype=BF16).cuda(), routing(g, T, k, E).cuda(), torch.rand(T, k, generator=g).cuda()
+    wl, y = randn(g, 40, 64, dtype=BF16).cuda(), torch.empty(T, H, device="cuda")
+
+    def buffers(o, seen):
+        for v in vars(o).values():
+            if isinstance(v, torch.Tensor):
+                seen.append(v)
+            elif isinstance(v, (Linear, ExpertRows)):
+                buffers(v, seen)
+        return seen
+
+    def linear():
+        return Linear(wl, max_rows=T, backward=True), lambda o: o.forward(x)
+
+    def experts():
+        return DenseExperts(w1, w2, k, T, backward=True), lambda o: o.forward(x, ids, w, y)
+
+    def rows():
+        return ExpertRows(E, k, T), lambda o: o.sort(ids)
+
+    mine = {t.data_ptr() for t in (w1, w2, wl, x, ids, w, y)}
+    for make in (linear, experts, rows):
+        o, call = make()
+        own = {t.data_ptr(): t.numel() * t.element_size() for t in buffers(o, []) if t.data_ptr() not in mine}
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+            call(o)
+        del o
+        again = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in own.values() for _ in range(3)]
+        assert not side.query()  # (the wait is still under way, so the answer means something)
+        for t in again:
+            assert not any(p <= t.data_ptr() < p + max(size, 1) for p, size in own.items()), make.__name__
+        side.synchronize()
