@@ -126,18 +126,23 @@ class ExpertRows(_OnDevice):
     def combine_backward(self, dy: torch.Tensor, w: Optional[torch.Tensor], rows: torch.Tensor,
                          drows: Optional[torch.Tensor] = None,
                          dw: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
-        """(drows, dw) of combine from dy [T, C]; rows are the ones combined."""
+        """(drows, dw) of combine from dy [T, C]; rows are the ones combined.  drows: bf16 or fp32 (by default as
+        rows; in another type by a launch of its own)."""
         T, k = self.n_tokens, self.top_k
         C = rows.shape[-1]
         g = _need(dy, "dy", (T, C), dy.dtype, self.device)
         r = _need(rows, "rows", (T * k, C), rows.dtype, self.device)
         drows = torch.empty_like(rows) if drows is None else drows
         dw = torch.empty((T, k), dtype=torch.float32, device=self.device) if dw is None else dw
-        d = _need(drows, "drows", (T * k, C), rows.dtype, self.device)
+        d = _need(drows, "drows", (T * k, C), drows.dtype, self.device)
         p = _need(dw, "dw", (T, k), torch.float32, self.device)
         wp = _need(w, "w", (T, k), torch.float32, self.device) if w is not None else 0
+        both = drows.dtype == rows.dtype
+        if not both:  # (first: dw may be w, and is written by the second)
+            self._call(_lib.combine_rows_backward, g, x_dtype_code(dy), T, k, C, self.pair_row.data_ptr(), wp, 0,
+                       x_dtype_code(drows), d, 0)
         self._call(_lib.combine_rows_backward, g, x_dtype_code(dy), T, k, C, self.pair_row.data_ptr(), wp, r,
-                   x_dtype_code(rows), d, p)
+                   x_dtype_code(rows), d if both else 0, p)
         return drows, dw
 
 
@@ -222,7 +227,10 @@ class DenseExperts:
     rows) and w2 [E, H, I], bf16 or fp32.  forward(x, ids, w) computes y = sum_i w_i E_i(x) (+ y
     itself with add=True) from a routing such as Step.route's; after a forward with keep=True,
     backward(dy) gives the gradients of x, the routing weights and the experts.  What backward needs
-    of the pass is kept here: x, ids and w may change in between (w1 and w2 may not)."""
+    of the pass is kept here: x, ids and w may change in between (w1 and w2 may not).
+
+    With bf16 experts h, z and the gradients between the products are held in bf16, which the matrix
+    instructions take; an expert's output o is held in fp32 until the weighted sum."""
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, top_k: int, max_tokens: int, swiglu_limit: float = 0.0,
                  backward: bool = False):
@@ -235,7 +243,7 @@ class DenseExperts:
         self.rows = ExpertRows(E, top_k, max_tokens, device=w1.device)
         # (buffers of rows: each pass of the step calls it, on the pass's stream)
         new = lambda *shape: self.rows._new(shape, w1.dtype)  # noqa: E731
-        self.xs, self.h, self.o = new(P, H), new(P, R // 2), new(P, H)
+        self.xs, self.h, self.o = new(P, H), new(P, R // 2), self.rows._new((P, H), torch.float32)
         self.z, self.dh, self.do = (new(P, R), new(P, R // 2), new(P, H)) if backward else (None, None, None)
         self.w_kept = self.rows._new((max_tokens, top_k), torch.float32) if backward else None
         self._kept = None
@@ -269,6 +277,6 @@ class DenseExperts:
         start = self.rows.expert_start
         self.rows.combine_backward(dy, w, self.o[:P], self.do[:P], dw)
         self.fc2.backward(self.h[:P], self.do[:P], group_start=start, dx=self.dh[:P], dw=dw2)
-        # (do and o have been read: o takes the gradient of the gathered rows)
-        self.fc1.backward(self.xs[:P], self.dh[:P], self.z[:P], start, dx=self.o[:P], dw=dw1)
-        self.rows.gather_backward(self.o[:P], dx)
+        # (do has been read: it takes the gradient of the gathered rows)
+        self.fc1.backward(self.xs[:P], self.dh[:P], self.z[:P], start, dx=self.do[:P], dw=dw1)
+        self.rows.gather_backward(self.do[:P], dx)

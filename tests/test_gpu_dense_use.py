@@ -148,3 +148,47 @@ def test_buffers_outlive_the_calls_of_a_dropped_object():
         for t in again:
             assert not any(p <= t.data_ptr() < p + max(size, 1) for p, size in own.items()), make.__name__
         side.synchronize()
+
+
+def test_experts_outputs_are_not_rounded_before_their_sum():
+    """Whole numbers of more than eight bits as the experts' outputs, exact in fp32: y and the weights' gradients,
+    sums of multiples of 32 below 2^29, are exact too.  (silu(64) is 64 in fp32; x picks columns of w1, so h = 64 u is exact in bf16.)"""
+    say("experts' outputs in fp32")
+    T, H, I, E, k = 11, 32, 16, 4, 3
+    g = gen(23)
+    whole = lambda n, *s: torch.randint(-n, n + 1, s, generator=g).float()  # noqa: E731
+    w1, w2 = torch.cat((torch.full((E, I, H), 64.0), whole(100, E, I, H)), 1), whole(3, E, H, I)
+    x = torch.zeros(T, H)
+    x[torch.arange(T), torch.randint(0, H, (T,), generator=g)] = 1.0
+    ids, w, dy = routing(g, T, k, E, dropped=0.1), 2.0 ** torch.randint(-1, 2, (T, k), generator=g), whole(3, T, H)
+    h = 64 * torch.einsum("th,eih->tei", x.double(), w1[:, I:].double())
+    o = torch.einsum("tei,ehi->teh", h, w2.double())
+    assert (o.bfloat16().double() != o).any() and o.abs().max() * 3 * H < 2 ** 29
+    at = torch.where(ids < 0, 0, ids).long()
+    mine = torch.where((ids < 0)[:, :, None], 0.0, o[torch.arange(T)[:, None], at])
+    step = DenseExperts(w1.to(BF16).cuda(), w2.to(BF16).cuda(), k, T, backward=True)
+    y = step.forward(x.to(BF16).cuda(), ids.cuda(), w.cuda(), keep=True)
+    assert torch.equal(y.cpu().double(), (mine * w[:, :, None].double()).sum(1))
+    dx, dw = torch.empty(T, H, dtype=BF16, device="cuda"), torch.empty(T, k, device="cuda")
+    step.backward(dy.cuda(), dx, dw, torch.empty(w1.shape, dtype=BF16, device="cuda"), torch.empty(w2.shape, dtype=BF16, device="cuda"))
+    assert torch.equal(dw.cpu().double(), (mine * dy[:, None].double()).sum(2))
+
+
+@pytest.mark.parametrize("dtype,other", [(F32, BF16), (BF16, F32)])
+def test_combine_backward_into_rows_of_another_type(dtype, other):
+    say(f"combine backward {dtype} into {other}")
+    T, k, C = 23, 4, 101
+    g = gen(6)
+    ids = routing(g, T, k, 6, dropped=0.2)
+    rows = ExpertRows(6, k, T)
+    rows.sort(ids.cuda())
+    o, dy, w = randn(g, T * k, C, dtype=dtype), randn(g, T, C), torch.rand(T, k, generator=g)
+    drows, wc = torch.full((T * k, C), -3.0, dtype=other, device="cuda"), w.cuda()
+    _, dw = rows.combine_backward(dy.cuda(), wc, o.cuda(), drows, wc)
+    d, _, named, v, bv = ref.combine_backward64(dy, rows.pair_row.cpu(), w, o, T, k)
+    bd = (ref.U + ref.HALF[other]) * d.abs()
+    left = torch.ones(T * k, dtype=torch.bool)
+    left[named] = False
+    d[left] = -3.0
+    ref.check(drows, d, bd, "drows")
+    ref.check(dw, v, bv, "dw")
