@@ -69,7 +69,25 @@ struct GemmArgs {
 // Activations
 // ---------------------------------------------------------------------------------------
 
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * (1.0f + erff(z * 0.70710678f)); }
+// Phi(-a) for a >= 0 from e = exp(-a^2 / 2): e q(a), with q(a) = erfc(a / sqrt(2)) exp(a^2 / 2) / 2, a smooth function
+// between 1/2 and 0.4 / a, as a polynomial in s = 1 / (1 + 0.23 a) fitted to its relative error over 0..14 (5e-8;
+// evaluated in fp32 4.2e-7).  The usual 1 + erf(z / sqrt(2)) loses what is left of Phi below z = -4, and is 0 from
+// -5.5 on; the library's erfcf keeps it (column sums of dz, 8192 x 8192 values in bf16: 52 us this way, 76 by
+// erff, 104 by erfcf).
+__device__ __forceinline__ float normal_tail(float a, float e) {
+  const float s = __builtin_amdgcn_rcpf(fmaf(0.23f, a, 1.0f));
+  constexpr float C[] = {-2.7751521e-05f, 0.09237833f, 0.08576334f, 0.119514026f, -0.032923725f,
+                         0.3014828f, -0.27813974f, 0.29042214f, -0.078469455f};
+  float q = C[8];
+#pragma unroll
+  for (int i = 7; i >= 0; --i) q = fmaf(q, s, C[i]);
+  return e * q;
+}
+__device__ __forceinline__ float normal_cdf(float z, float e) {
+  const float p = normal_tail(fabsf(z), e);
+  return z < 0.f ? p : 1.0f - p;
+}
+__device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z, __expf(-0.5f * z * z)); }
 // (v_rcp_f32: within one unit in the last place)
 __device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
@@ -77,7 +95,8 @@ __device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn
 __device__ __forceinline__ float silu_grad(float z, float s) { return s * (1.0f + z * (1.0f - s)); }
 // d gelu(z) / dz = Phi(z) + z phi(z)
 __device__ __forceinline__ float gelu_grad(float z) {
-  return 0.5f * (1.0f + erff(z * 0.70710678f)) + z * 0.39894228f * __expf(-0.5f * z * z);
+  const float e = __expf(-0.5f * z * z);
+  return normal_cdf(z, e) + z * 0.39894228f * e;
 }
 
 // ---------------------------------------------------------------------------------------

@@ -192,3 +192,31 @@ def test_combine_backward_into_rows_of_another_type(dtype, other):
     d[left] = -3.0
     ref.check(drows, d, bd, "drows")
     ref.check(dw, v, bv, "dw")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_gelu_keeps_its_relative_precision(dtype):
+    """z Phi(z) and its derivative where Phi(z) is tiny.  Errors, with t = -z / sqrt(2): Phi(z) = erfc(t) / 2 falls as
+    exp(-t^2), whose exponent is off by up to 1.5 * 2^-24 of itself twice over (z^2 and the product with the
+    base's logarithm, each rounded once, and the constant), that is 3 t^2 * 2^-24 of the value; what multiplies
+    it, and the products: 16 * 2^-24, and 2.3 t * 2^-24 of a reciprocal of 1 + a multiple of t.  phi(z): the same
+    exponent, and 8 * 2^-23 of the rest."""
+    say(f"gelu tail {dtype}")
+    z = torch.cat((torch.linspace(-12, 12, 4001), torch.tensor([0.0, -0.0, -1e-20, 1e-20, -5.5, -6.0, -10.5]))).to(dtype).reshape(-1, 1)
+    n = z.shape[0]
+    lin = Linear(torch.ones(1, 1, dtype=dtype, device="cuda"), act="gelu", max_rows=n, backward=True)
+    y = lin.forward(z.cuda(), out=torch.empty(n, 1, device="cuda"))
+    v = z.double()
+    t = -v / 2.0 ** 0.5
+    half = 0.5 * torch.special.erfc(t)
+    e = (1.5 * (2 * t * t + 1.5 * t.abs() + 1) + 16) * 2.0 ** -24
+    ref.check(y, v * half, e * (v * half).abs(), "gelu")
+    dz = torch.empty(1, device="cuda")
+    phi = torch.exp(-v * v / 2) / (2 * torch.pi) ** 0.5
+    slope = half + v * phi
+    be = e * half + (3 * v * v / 2 + 16) * 2.0 ** -24 * (v * phi).abs() + 2 * ref.U * slope.abs()
+    # one row at a time (its column sum is its own dz, not rounded to the type)
+    one = torch.ones(1, 1, device="cuda")
+    for i in list(range(0, n, 97)) + list(range(n - 7, n)):
+        lin.backward(z[i:i + 1].cuda(), one, z[i:i + 1].cuda(), dbias=dz)
+        ref.check(dz, slope[i], be[i], f"derivative at {v[i].item()}")
