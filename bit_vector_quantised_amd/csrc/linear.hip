@@ -733,12 +733,27 @@ __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
 // Repacking rows whose width is no multiple of 16 bytes (dst pitch: the next one, zero-filled)
 // ---------------------------------------------------------------------------------------
 
-// 16 bytes of dst per thread and turn; the turns cover any number of rows with a bounded grid.
+// 16 bytes of dst per thread and turn; the turns cover any number of rows with a bounded grid.  With a row table of
+// G groups, only what the groups use: of x (wrows 0) the rows of groups, of the weights those of groups
+// that have rows, `wrows` of each group blockIdx.y.
 template <typename T>
-__global__ __launch_bounds__(256) void pack_rows_kernel(const T* src, T* dst, size_t rows, int cols, int pitch) {
+__global__ __launch_bounds__(256) void pack_rows_kernel(const T* src, T* dst, size_t rows, int cols, int pitch,
+                                                        const int32_t* group_start, int G, int wrows) {
   constexpr int N = 16 / sizeof(T);
-  const size_t per = pitch / N, all = rows * per;
-  for (size_t at = (size_t)blockIdx.x * 256 + threadIdx.x; at < all; at += (size_t)gridDim.x * 256) {
+  const size_t per = pitch / N;
+  size_t begin = 0, end = rows;
+  if (group_start && wrows) {
+    const int g = blockIdx.y;
+    if (group_start[g] >= group_start[g + 1]) return;
+    begin = (size_t)g * wrows;
+    end = begin + wrows;
+  } else if (group_start) {
+    const int lo = group_start[0], hi = group_start[G];
+    begin = lo < 0 ? 0 : lo;
+    end = hi < 0 ? 0 : ((size_t)hi < rows ? hi : rows);
+  }
+  end *= per;
+  for (size_t at = begin * per + (size_t)blockIdx.x * 256 + threadIdx.x; at < end; at += (size_t)gridDim.x * 256) {
     const size_t r = at / per;
     const int c = (int)(at - r * per) * N;
     const T* from = src + r * cols + c;
@@ -998,14 +1013,28 @@ void launch_dz(const LinearPlan& p, const DzArgs& d, int dy_dtype, int act, hipS
   }
 }
 
-void pack_rows(const LinearPlan& p, const void* src, void* dst, size_t rows, hipStream_t st) {
-  const size_t blocks = (rows * p.Kp * p.size / 16 + 255) / 256;
+void pack_rows(const LinearPlan& p, const void* src, void* dst, size_t rows, const int32_t* group_start, int wrows,
+               hipStream_t st) {
+  // (groups side by side; enough workgroups for each that a few of them that have rows fill the device)
+  const unsigned groups = group_start && wrows ? p.G : 1, most = 64 * CUS / groups > 64 ? 64 * CUS / groups : 64;
+  const size_t blocks = (rows / groups * p.Kp * p.size / 16 + 255) / 256;
   if (blocks == 0) return;
-  const unsigned grid = (unsigned)(blocks < 64 * CUS ? blocks : 64 * CUS);
-  if (p.size == 2)
-    pack_rows_kernel<uint16_t><<<grid, 256, 0, st>>>(static_cast<const uint16_t*>(src), static_cast<uint16_t*>(dst), rows, p.K, p.Kp);
-  else
-    pack_rows_kernel<uint32_t><<<grid, 256, 0, st>>>(static_cast<const uint32_t*>(src), static_cast<uint32_t*>(dst), rows, p.K, p.Kp);
+  const dim3 grid((unsigned)(blocks < most ? blocks : most), groups);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    pack_rows_kernel<T><<<grid, 256, 0, st>>>(static_cast<const T*>(src), static_cast<T*>(dst), rows, p.K, p.Kp, group_start, p.G, wrows);
+  };
+  if (p.size == 2) go(uint16_t{});
+  else go(uint32_t{});
+}
+// x's rows and the weights, to where the plan has them in the workspace.
+const char* pack_x(const LinearPlan& p, const LinearCall& c, hipStream_t st) {
+  pack_rows(p, c.x, static_cast<char*>(c.ws) + p.xp, p.M, c.group_start, 0, st);
+  return static_cast<char*>(c.ws) + p.xp;
+}
+const char* pack_w(const LinearPlan& p, const LinearCall& c, hipStream_t st) {
+  pack_rows(p, c.L->w, static_cast<char*>(c.ws) + p.wp, (size_t)p.G * p.R, c.group_start, p.R, st);
+  return static_cast<char*>(c.ws) + p.wp;
 }
 
 template <typename T>
@@ -1072,10 +1101,8 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
   g.b = static_cast<const char*>(c.L->w);
   const bool few = p.few && !c.group_start, as_is = few && p.K * p.size >= 16;
   if (p.pack_k && !as_is) {
-    pack_rows(p, c.x, at<char>(c.ws, p.xp), p.M, st);
-    pack_rows(p, c.L->w, at<char>(c.ws, p.wp), (size_t)p.G * p.R, st);
-    g.a = at<char>(c.ws, p.xp);
-    g.b = at<char>(c.ws, p.wp);
+    g.a = pack_x(p, c, st);
+    g.b = pack_w(p, c, st);
   }
   g.a_pitch = g.b_pitch = (uint32_t)(as_is ? p.K : p.Kp) * p.size;
   g.w_group = (uint64_t)p.R * g.b_pitch;
@@ -1124,8 +1151,8 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
   const void* x = c.x;
   const void* w = c.L->w;
   if (p.pack_k) {
-    if (c.dw) { pack_rows(p, c.x, at<char>(c.ws, p.xp), p.M, st); x = at<char>(c.ws, p.xp); }
-    if (c.dx) { pack_rows(p, c.L->w, at<char>(c.ws, p.wp), (size_t)p.G * p.R, st); w = at<char>(c.ws, p.wp); }
+    if (c.dw) x = pack_x(p, c, st);
+    if (c.dx) w = pack_w(p, c, st);
   }
   GemmArgs g{};
   g.a = static_cast<const char*>(dz);

@@ -445,7 +445,9 @@ typedef struct moe_vq_linear {
 
 /* [host] Workspace bytes of moe_vq_linear_forward (backward = 0) or moe_vq_linear_backward
  * (backward = 1) for up to n_rows rows, 0 if an argument is invalid.  Pointers are not
- * inspected.  A call with fewer rows may use it too. */
+ * inspected.  A call with fewer rows may use it too.  If n_in is no multiple of 16 bytes the
+ * workspace holds x and all groups' weights once more: each call copies the rows and the weights
+ * that its groups use there, except a forward call of at most 16 rows without group_start. */
 size_t moe_vq_linear_bytes(const moe_vq_linear *lin, int n_rows, int backward);
 
 /* y = act(x W^T + b) + residual.  x [n_rows][n_in]; y and residual [n_rows][n_out] in y_dtype

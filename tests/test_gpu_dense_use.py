@@ -7,7 +7,7 @@ import dense_ref as ref
 from bit_vector_quantised_amd.dense import DenseExperts, ExpertRows, Linear  # noqa: F401
 
 from gpu_util import say
-from test_gpu_dense import BF16, F32, gen, linear_inputs, randn, routing
+from test_gpu_dense import BF16, F32, gen, linear_inputs, outside, randn, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -220,3 +220,37 @@ def test_gelu_keeps_its_relative_precision(dtype):
     for i in list(range(0, n, 97)) + list(range(n - 7, n)):
         lin.backward(z[i:i + 1].cuda(), one, z[i:i + 1].cuda(), dbias=dz)
         ref.check(dz, slope[i], be[i], f"derivative at {v[i].item()}")
+
+
+@pytest.mark.parametrize("K,dtype", [(201, BF16), (33, F32)])
+def test_repacking_leaves_out_what_no_group_uses(K, dtype):
+    """Widths that are repacked: neither rows in no group nor the weights of groups without rows are copied, so no
+    more of the workspace changes than the others take; and the outputs are those of the groups."""
+    say(f"repacking K={K} {dtype}")
+    start, M, N = [9, 9, 9, 20, 20, 31, 31, 31, 31], 50, 40
+    g, R, x, w, b, _ = linear_inputs(M, K, N, start, "silu", dtype, F32, True, False)
+    size = x.element_size()
+    row = (K * size + 15) // 16 * 16
+    none = outside(M, start)
+    lin = Linear(w.cuda(), b.cuda(), act="silu", max_rows=M, backward=True)
+    gs = torch.tensor(start, dtype=torch.int32, device="cuda")
+    y = torch.full((M, N), -3.0, device="cuda")
+
+    def changed(call):
+        lin.ws.fill_(0xA5)
+        call()
+        return int((lin.ws != 0xA5).sum())
+
+    assert changed(lambda: lin.forward(x.cuda(), gs, out=y)) <= (22 + 2 * R) * row
+    want, by, _, _ = ref.linear_forward64(x, w, b, start, "silu", 0.0, None, F32, dtype)
+    want[none] = -3.0
+    ref.check(y, want, by, "y")
+    lin = Linear(w.cuda(), max_rows=M, backward=True)
+    dy = randn(g, M, N, dtype=dtype)
+    dx, dw = torch.full((M, K), -3.0, dtype=dtype, device="cuda"), torch.full(w.shape, -3.0, dtype=dtype, device="cuda")
+    assert changed(lambda: lin.backward(x.cuda(), dy.cuda(), group_start=gs, dx=dx)) <= 2 * R * row
+    assert changed(lambda: lin.backward(x.cuda(), dy.cuda(), group_start=gs, dw=dw)) <= 22 * row
+    want = ref.linear_backward64(x, w, start, "none", 0.0, None, dy, dtype)
+    want["dx"][0][none] = -3.0
+    ref.check(dx, *want["dx"], "dx")
+    ref.check(dw, *want["dw"], "dw")
