@@ -180,14 +180,14 @@ class Linear(_OnDevice):
         self.c.bias = _need(self.bias, "bias", self.w_shape[:-1], torch.float32, self.device) if self.bias is not None else None
         return self.c
 
-    def _rows(self, x: torch.Tensor, group_start: Optional[torch.Tensor]) -> Tuple[int, int]:
-        if x.shape[0] > self.max_rows:
-            raise ValueError(f"{x.shape[0]} rows, made for {self.max_rows}")
+    def _rows(self, rows: torch.Tensor, group_start: Optional[torch.Tensor]) -> Tuple[int, int]:
+        if rows.shape[0] > self.max_rows:
+            raise ValueError(f"{rows.shape[0]} rows, made for {self.max_rows}")
         if group_start is None:
             if self.grouped:
                 raise ValueError("weights of groups need group_start")
-            return x.shape[0], 0
-        return x.shape[0], _need(group_start, "group_start", (self.n_groups + 1,), torch.int32, self.device)
+            return rows.shape[0], 0
+        return rows.shape[0], _need(group_start, "group_start", (self.n_groups + 1,), torch.int32, self.device)
 
     def forward(self, x: torch.Tensor, group_start: Optional[torch.Tensor] = None,
                 residual: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
@@ -206,13 +206,15 @@ class Linear(_OnDevice):
                    self.ws_bytes)
         return out
 
-    def backward(self, x: torch.Tensor, dy: torch.Tensor, z: Optional[torch.Tensor] = None,
+    def backward(self, x: Optional[torch.Tensor], dy: torch.Tensor, z: Optional[torch.Tensor] = None,
                  group_start: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                  dw: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None) -> None:
         """Gradients from dy [M, n_out] and the z that forward kept (not needed for act "none"): those of dx
-        [M, n_in], dw (as w) and dbias (as bias) that are given are written."""
-        M, gs = self._rows(x, group_start)
-        xp = _need(x, "x", (M, self.n_in), self.dtype, self.device)
+        [M, n_in], dw (as w) and dbias (as bias) that are given are written.  x may be None without dw."""
+        M, gs = self._rows(dy, group_start)
+        if x is None and dw is not None:
+            raise ValueError("dw needs x")
+        xp = _need(x, "x", (M, self.n_in), self.dtype, self.device) if x is not None else 0
         g = _need(dy, "dy", (M, self.n_out), dy.dtype, self.device)
         zp = _need(z, "z", (M, self.n_rows_w), self.dtype, self.device) if z is not None else 0
         xd = _need(dx, "dx", (M, self.n_in), self.dtype, self.device) if dx is not None else 0

@@ -254,3 +254,23 @@ def test_repacking_leaves_out_what_no_group_uses(K, dtype):
     want["dx"][0][none] = -3.0
     ref.check(dx, *want["dx"], "dx")
     ref.check(dw, *want["dw"], "dw")
+
+
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_gradients_that_need_no_x(act):
+    """dx and dbias are made without x; dw is not."""
+    say(f"gradients without x {act}")
+    M, K, N = 21, 48, 24
+    g, R, x, w, b, _ = linear_inputs(M, K, N, None, act, BF16, F32, True, False)
+    lin = Linear(w.cuda(), b.cuda(), act=act, max_rows=M, backward=True)
+    x, dy, z = x.cuda(), randn(g, M, N).cuda(), None if act == "none" else randn(g, M, R, dtype=BF16).cuda()
+    new = lambda: (torch.empty_like(x), torch.empty(R, device="cuda"))  # noqa: E731
+    with_x, without = new(), new()
+    lin.backward(x, dy, z, dx=with_x[0], dbias=with_x[1])
+    lin.backward(None, dy, z, dx=without[0], dbias=without[1])
+    for a, c in zip(with_x, without):
+        assert torch.equal(a, c)
+    with pytest.raises(ValueError, match="x"):
+        lin.backward(None, dy, z, dw=torch.empty_like(w).cuda())
+    with pytest.raises(ValueError, match="rows"):
+        lin.backward(None, torch.empty(M + 1, N, device="cuda"), z, dx=torch.empty(M + 1, K, dtype=BF16, device="cuda"))
