@@ -283,3 +283,22 @@ def test_every_written_buffer_is_kept_apart():
         if act == _lib.ACT_NONE:
             b.refused(bwd, "dx", "dy")
             b.refused(bwd, "dw", "dy")
+
+
+def test_a_workspace_serves_every_smaller_call():
+    """What a call needs itself, not only its bound: with the bytes for the largest number of rows no smaller call is
+    told that its workspace is too small.  (The calls' buffers overlap, which is looked at last: nothing is launched.)"""
+    shapes = [dict(n_in=k, n_out=n, groups=g, act=a, dtype=t)
+              for k, n in ((256, 128), (8192, 64), (64, 8192), (333, 4097), (7168, 2048), (16384, 40), (24, 24))
+              for g in (1, 3, 64, 1024) for a in (_lib.ACT_NONE, _lib.ACT_SWIGLU) for t in (_lib.BF16, _lib.F32)]
+    rows = (1, 2, 15, 16, 17, 63, 64, 65, 100, 128, 129, 300, 511, 512, 513, 1000, 2048, 5000, 20000, 100000)
+    for kw in shapes:
+        d = lin(**kw)
+        for i, most in enumerate(rows):
+            need = [_lib.linear_bytes(d, most, b) for b in (False, True)]
+            for m in rows[:i + 1]:
+                p = ctypes.byref(d)
+                start = A if kw["groups"] > 1 else None
+                assert RAW.moe_vq_linear_forward(p, A, m, start, None, A, _lib.F32, A, A, need[0], None) == _lib.EINVAL, (kw, most, m)
+                assert RAW.moe_vq_linear_backward(p, A, m, start, A, A, _lib.F32, A, A, A, A, need[1], None) == _lib.EINVAL, (kw, most, m)
+        assert RAW.moe_vq_linear_forward(p, A, m, start, None, A, _lib.F32, A, A, 255, None) == _lib.ENOSPACE

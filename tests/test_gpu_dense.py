@@ -176,8 +176,8 @@ LINEAR_CASES = [  # M, K, N, start (None: one matrix), act, dtype, y_dtype, bias
     (64, 1000, 130, None, "none", BF16, BF16, False, True),
     (65, 333, 100, None, "silu", BF16, F32, True, True),
     (129, 200, 257, None, "swiglu", BF16, F32, True, False),
-    (200, 1024, 64, None, "gelu", BF16, BF16, True, True),   # few tiles: the contraction is split
-    (300, 2056, 31, None, "swiglu", BF16, BF16, True, True),
+    (200, 1024, 64, None, "gelu", BF16, BF16, True, True),   # few tiles
+    (300, 2056, 31, None, "swiglu", BF16, BF16, True, True),  # few tiles: the contraction is split forward
     (300, 136, 520, None, "none", BF16, BF16, True, True),
     (1, 100, 40, None, "swiglu", F32, F32, True, True),
     (77, 130, 67, None, "gelu", F32, F32, True, True),
