@@ -604,12 +604,12 @@ __device__ __forceinline__ uint32_t few_keep(int drop) { return drop <= 0 ? 0xFF
 
 // Forward product of at most 16 rows.  Bound by streaming W from HBM once; a 64 x 64 tile spends as much on
 // the parts of its split contraction and their sum (one row, 7168 -> 2048 gated, weights not in
-// any cache: 19 us) as on the weights (11 to 12 us here, of which the 59 MB take 10).  A workgroup
+// any cache: 19 us) as on the weights (12 us here, of which the 59 MB take 10).  A workgroup
 // takes 16 weight rows (gated: eight gate rows and their up rows), its eight waves split the
 // contraction among them, and their sums meet in LDS in a fixed order: one launch.  W goes from
 // memory to the registers of the matrix operand, 16 rows of 64 bytes per load; the rows of x, which
-// every workgroup reads, come from L2.  Four loads ahead measured best of 4, 7, 8, 14 and 16
-// (13.4, 14.2, 15.3, 15.7, 18.3 us), eight waves best of 4, 8 and 16 (17.9, 13.4, 16.6).
+// every workgroup reads, come from L2.  Of 2, 4, 8 and 14 loads ahead two
+// and four measured best (12.3, 12.3, 13.7, 13.5 us), of 4, 8 and 16 waves eight (14.8, 12.3, 14.7).
 constexpr int FEW_ROWS = 16, FEW_WAVES = 8, FEW_STREAM = 4;
 
 //
@@ -924,8 +924,8 @@ constexpr TileKind F32_TILES[] = {{128, 2, 3.9f, 2.1f, 6.f}, {64, 2, 1.0f, 0.75f
 // How a product is cut.  rows: output rows in all, of `groups` groups; cols: output columns (weight rows forward);
 // steps: contraction steps.  The cut with the smallest estimate is taken: rounds of workgroups over the
 // device, times a workgroup's time, and for a split contraction the write and read of its parts (from
-// the caches: 10 TB/s) and one more launch.  Large products so take 256 x 256 tiles (1400 TFLOP/s at 8192^3, 128 x 128 tiles, which read LDS twice as
-// often for their products, 1150) unless the last round would be nearly empty; small outputs with
+// the caches: 10 TB/s) and one more launch.  Large products so take 256 x 256 tiles (at 8192^3, on a card where they reach 1400 TFLOP/s, 128 x 128
+// tiles, which read LDS twice as often for their products, reach 1150) unless the last round would be nearly empty; small outputs with
 // long contractions are split, and outputs too small for that take small tiles.
 Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool forward) {
   const long per = (rows + groups - 1) / groups;

@@ -138,7 +138,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_kernel(SortArgs a) {
 
 // At most 64 pairs: every lane holds one and counts the pairs before it (smaller expert, or the same and an
 // earlier pair); the rest of the work, the experts' first rows, is counted the same way.
-// Measured 2.7 us for one token's eight pairs, where the counting sort takes 5.0.
+// Measured 3.8 us for one token's eight pairs, where the counting sort takes 5.0.
 constexpr int SORT_FEW = 64;
 
 __global__ __launch_bounds__(256) void sort_few_kernel(SortArgs a) {
@@ -251,10 +251,11 @@ __device__ __forceinline__ void store_n(float* p, const float* v) {
   }
 }
 
-// Rows of more bytes than the memory-side cache holds are streamed: gather 94 us instead of 105,
-// combine 97 instead of 109 (470 MB of rows); smaller ones stay where the next kernel finds them.
-// Streamed rows are fastest with workgroups of 128 threads (gather 94 us, 256 threads 99; combine 97, 106),
-// rows that a cache holds with 256 (combine of 1021 tokens of 2047 fp32 columns, top-6: 15 us, 22 with 128).
+// Rows of more bytes than the memory-side cache holds are streamed: gather 90 us instead of 114,
+// combine 123 instead of 141 with an fp32 residual, 96 instead of 130 in bf16 alone (470 MB of rows); smaller ones
+// stay where the next kernel finds them.  Streamed rows are fastest with workgroups of 128 threads (gather
+// 90 us, 256 threads 98; combine 123, 131), rows that a cache holds a little faster with 256 (combine of 32 tokens
+// of 7168 fp32 columns, top-8: 4.0 us, 4.3 with 128; of 1021 tokens of 2047 columns, top-6: 17 either way).
 constexpr int row_threads_log(bool stream) { return stream ? 7 : 8; }
 static bool streamed(const RowsArgs& a, size_t size) { return (size_t)a.T * a.k * a.C * size > ((size_t)256 << 20); }
 
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(1 << row_threads_log(STREAM)) void gather_kernel(Ro
   const int32_t* row = a.pair_row + (size_t)t * a.k;
   const int P = a.T * a.k;
   if (at + 16 <= bytes) {
-    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from);  // (streaming the loads too takes 105 us)
+    const u32x4_any v = *reinterpret_cast<const u32x4_any*>(from);  // (streaming the loads too: 101 us)
     for (int i = 0; i < a.k; ++i) {
       const int r = row[i];
       if ((uint32_t)r < (uint32_t)P) store_vec<STREAM>(reinterpret_cast<u32x4_any*>(to + (size_t)r * bytes), v);

@@ -1,6 +1,7 @@
 """Unquantised experts on top of the C ABI: the routed pairs sorted by expert and back, the
 dense product with bias, activation and residual (one matrix, or one per expert over the
-sorted rows), and their gradients.
+sorted rows), and their gradients.  The gradients are calls of their own: nothing here records a graph
+for autograd, and outputs carry none even if an input requires a gradient.
 
 As in layer.py, PyTorch provides device memory and the stream; every step of the
 computation runs in the HIP library.  An object's workspace serves its calls one after the

@@ -368,8 +368,9 @@ int moe_vq_cpu_experts(const moe_vq_layer *layer, const uint8_t *host_pool, uint
 
 /* ---- The step with unquantised experts, and its gradients.  The coded experts above are
  * made from, and judged against, experts in bf16 or fp32; the shared expert and the dense
- * layers of such models are kept that way, and a router or the experts are tuned through
- * them.  These calls run that layer from the same routing (topk_ids, topk_w):
+ * layers of such models are kept that way, and a model is tuned through them: the
+ * gradients reach the rows, the experts' matrices and the routing weights (what the router's
+ * softmax makes of these is the caller's).  These calls run that layer from the same routing (topk_ids, topk_w):
  *   sort_pairs      the routed pairs p = t*k + i sorted by expert
  *   gather_rows     the tokens' rows in that order
  *   linear_forward  the experts' products, with bias, activation and residual
