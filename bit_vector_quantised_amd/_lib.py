@@ -18,13 +18,17 @@ F32, BF16 = 0, 1
 FMT_ABSENT, FMT_VQ2, FMT_MXFP4 = 0, 1, 2
 MAT_GATE, MAT_UP, MAT_DOWN = 0, 1, 2
 ACT_NONE, ACT_SILU, ACT_GELU, ACT_SWIGLU = range(4)
+SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
 
 EXPORTS = ("moe_vq_expert_bytes", "moe_vq_slot_layout", "moe_vq_workspace_bytes", "moe_vq_route_topk",
            "moe_vq_fc1_silu", "moe_vq_fc2_combine", "moe_vq_forward", "moe_vq_forward_static", "moe_vq_shared_expert", "moe_vq_prefill_gemm", "moe_vq_decode_expert",
            "moe_vq_check", "moe_vq_step_info", "moe_vq_tier_init", "moe_vq_tier_plan", "moe_vq_tier_resolve", "moe_vq_cpu_experts",
            "moe_vq_time_next_kernel", "moe_vq_read_probe",
            "moe_vq_sort_bytes", "moe_vq_sort_pairs", "moe_vq_gather_rows", "moe_vq_combine_rows", "moe_vq_combine_rows_backward",
-           "moe_vq_linear_bytes", "moe_vq_linear_forward", "moe_vq_linear_backward", "moe_vq_last_hip_error", "moe_vq_strerror")
+           "moe_vq_linear_bytes", "moe_vq_linear_forward", "moe_vq_linear_backward",
+           "moe_vq_rows8_pitch", "moe_vq_rows8_pack", "moe_vq_rows8_unpack", "moe_vq_gather_rows8", "moe_vq_act_backward8",
+           "moe_vq_linear_bytes8", "moe_vq_linear_backward8", "moe_vq_norm_forward", "moe_vq_norm_bytes", "moe_vq_norm_backward",
+           "moe_vq_choose", "moe_vq_choose_backward", "moe_vq_last_hip_error", "moe_vq_strerror")
 
 
 class MoeVqError(RuntimeError):
@@ -60,6 +64,18 @@ class LinearDesc(ctypes.Structure):
                 ("w", ctypes.c_void_p), ("bias", ctypes.c_void_p)]
 
 
+class Rows8Desc(ctypes.Structure):
+    """struct moe_vq_rows8"""
+    _fields_ = [("q", ctypes.c_void_p), ("e", ctypes.c_void_p)]
+
+
+class Choice(ctypes.Structure):
+    """struct moe_vq_choice"""
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float), ("bias", ctypes.c_void_p)]
+
+
 def _load():
     # The library must run on the same HIP runtime as PyTorch, whose streams and
     # device memory it is handed.  The torch wheel bundles libamdhip64.so.7 under the
@@ -75,6 +91,9 @@ def _load():
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
     LP = ctypes.POINTER(Layer)
     DP = ctypes.POINTER(LinearDesc)
+    QP = ctypes.POINTER(Rows8Desc)
+    CP = ctypes.POINTER(Choice)
+    f32 = ctypes.c_float
     sig = {
         "moe_vq_expert_bytes": (sz, [i32, i32, i32]),
         "moe_vq_slot_layout": (i32, [i32, i32, i32, ctypes.POINTER(ctypes.c_uint64)]),
@@ -106,6 +125,18 @@ def _load():
         "moe_vq_linear_bytes": (sz, [DP, i32, i32]),
         "moe_vq_linear_forward": (i32, [DP, vp, i32, vp, vp, vp, i32, vp, vp, sz, vp]),
         "moe_vq_linear_backward": (i32, [DP, vp, i32, vp, vp, vp, i32, vp, vp, vp, vp, sz, vp]),
+        "moe_vq_rows8_pitch": (sz, [i32]),
+        "moe_vq_rows8_pack": (i32, [vp, i32, i32, i32, vp, i32, QP, vp]),
+        "moe_vq_rows8_unpack": (i32, [QP, i32, i32, vp, i32, vp, i32, vp]),
+        "moe_vq_gather_rows8": (i32, [QP, i32, i32, i32, vp, vp, i32, vp]),
+        "moe_vq_act_backward8": (i32, [QP, i32, f32, i32, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, vp]),
+        "moe_vq_linear_bytes8": (sz, [DP, i32]),
+        "moe_vq_linear_backward8": (i32, [DP, vp, QP, i32, vp, vp, QP, vp, i32, vp, vp, vp, vp, sz, vp]),
+        "moe_vq_norm_forward": (i32, [vp, i32, vp, vp, i32, i32, i32, vp, f32, vp, i32, QP, vp]),
+        "moe_vq_norm_bytes": (sz, [i32, i32]),
+        "moe_vq_norm_backward": (i32, [vp, i32, i32, i32, vp, f32, vp, vp, i32, vp, vp, i32, vp, vp, sz, vp]),
+        "moe_vq_choose": (i32, [CP, vp, i32, vp, vp, vp]),
+        "moe_vq_choose_backward": (i32, [CP, vp, i32, vp, vp, vp, vp]),
         "moe_vq_last_hip_error": (ctypes.c_char_p, []),
         "moe_vq_strerror": (ctypes.c_char_p, [i32]),
     }
@@ -330,6 +361,75 @@ def linear_backward(lin: LinearDesc, x: int, n_rows: int, group_start: int, z: i
     """group_start, z, dx, dw and dbias may be 0 (NULL)."""
     _ok(_lib.moe_vq_linear_backward(ctypes.byref(lin), x, n_rows, group_start, z, dy, dy_dtype, dx, dw, dbias, ws,
                                     ws_bytes, stream), "linear_backward")
+
+
+def _r8(r):
+    return None if r is None else ctypes.byref(r)
+
+
+def rows8_pitch(n_cols: int) -> int:
+    return int(_lib.moe_vq_rows8_pitch(n_cols))
+
+
+def rows8_pack(x: int, dtype: int, n_rows: int, n_cols: int, group_start: int, n_groups: int, r: Rows8Desc,
+               stream: int = 0) -> None:
+    """group_start may be 0 (NULL)."""
+    _ok(_lib.moe_vq_rows8_pack(x, dtype, n_rows, n_cols, group_start, n_groups, _r8(r), stream), "rows8_pack")
+
+
+def rows8_unpack(r: Rows8Desc, n_rows: int, n_cols: int, group_start: int, n_groups: int, x: int, dtype: int,
+                 stream: int = 0) -> None:
+    """group_start may be 0 (NULL)."""
+    _ok(_lib.moe_vq_rows8_unpack(_r8(r), n_rows, n_cols, group_start, n_groups, x, dtype, stream), "rows8_unpack")
+
+
+def gather_rows8(r: Rows8Desc, n_tokens: int, top_k: int, n_cols: int, pair_row: int, xs: int, dtype: int,
+                 stream: int = 0) -> None:
+    _ok(_lib.moe_vq_gather_rows8(_r8(r), n_tokens, top_k, n_cols, pair_row, xs, dtype, stream), "gather_rows8")
+
+
+def act_backward8(z8: Rows8Desc, act: int, swiglu_limit: float, n_tokens: int, top_k: int, n_out: int, pair_row: int,
+                  w: int, dy: int, dy_dtype: int, dz: int, y: int, dtype: int, dw: int, stream: int = 0) -> None:
+    """w, dz, y and dw may be 0 (NULL)."""
+    _ok(_lib.moe_vq_act_backward8(_r8(z8), act, swiglu_limit, n_tokens, top_k, n_out, pair_row, w, dy, dy_dtype, dz, y,
+                                  dtype, dw, stream), "act_backward8")
+
+
+def linear_bytes8(lin: LinearDesc, n_rows: int) -> int:
+    return int(_lib.moe_vq_linear_bytes8(ctypes.byref(lin), n_rows))
+
+
+def linear_backward8(lin: LinearDesc, x: int, x8, n_rows: int, group_start: int, z: int, z8, dy: int, dy_dtype: int,
+                     dx: int, dw: int, dbias: int, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    """x8 and z8: Rows8Desc or None; the other pointers but dy and ws may be 0 (NULL)."""
+    _ok(_lib.moe_vq_linear_backward8(ctypes.byref(lin), x, _r8(x8), n_rows, group_start, z, _r8(z8), dy, dy_dtype, dx, dw,
+                                     dbias, ws, ws_bytes, stream), "linear_backward8")
+
+
+def norm_forward(x: int, dtype: int, residual: int, s: int, s_dtype: int, n_rows: int, n_cols: int, gain: int, eps: float,
+                 y: int, y_dtype: int, y8, stream: int = 0) -> None:
+    """residual, s and y may be 0 (NULL), y8 None."""
+    _ok(_lib.moe_vq_norm_forward(x, dtype, residual, s, s_dtype, n_rows, n_cols, gain, eps, y, y_dtype, _r8(y8), stream),
+        "norm_forward")
+
+
+def norm_bytes(n_rows: int, n_cols: int) -> int:
+    return int(_lib.moe_vq_norm_bytes(n_rows, n_cols))
+
+
+def norm_backward(s: int, s_dtype: int, n_rows: int, n_cols: int, gain: int, eps: float, dy: int, dy2: int, dy_dtype: int,
+                  ds: int, dx: int, dx_dtype: int, dgain: int, ws: int, ws_bytes: int, stream: int = 0) -> None:
+    """dy2, ds, dx and dgain may be 0 (NULL)."""
+    _ok(_lib.moe_vq_norm_backward(s, s_dtype, n_rows, n_cols, gain, eps, dy, dy2, dy_dtype, ds, dx, dx_dtype, dgain, ws,
+                                  ws_bytes, stream), "norm_backward")
+
+
+def choose(c: Choice, logits: int, n_tokens: int, ids: int, w: int, stream: int = 0) -> None:
+    _ok(_lib.moe_vq_choose(ctypes.byref(c), logits, n_tokens, ids, w, stream), "choose")
+
+
+def choose_backward(c: Choice, logits: int, n_tokens: int, ids: int, dw: int, dlogits: int, stream: int = 0) -> None:
+    _ok(_lib.moe_vq_choose_backward(ctypes.byref(c), logits, n_tokens, ids, dw, dlogits, stream), "choose_backward")
 
 
 def raw():

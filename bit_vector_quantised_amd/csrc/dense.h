@@ -2,7 +2,7 @@
 // (linear.hip); the entry points that check and call them are in dense_api.hip.
 #pragma once
 
-#include "moe_vq_internal.h"
+#include "block.h"
 
 namespace mvq {
 
@@ -56,8 +56,9 @@ struct LinearPlan {
   int split_bias;            // parts of a group's rows in the sums of dbias
   size_t xp, wp, dz, bias_part, part, total;
 };
-LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward);
-size_t linear_max_bytes(const moe_vq_linear* L, int n_rows, bool backward);  // of every call with up to n_rows rows
+// kept8: with room for x from 8 bits
+LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward, bool kept8 = false);
+size_t linear_max_bytes(const moe_vq_linear* L, int n_rows, bool backward, bool kept8 = false);  // of every call with up to n_rows rows
 
 struct LinearCall {
   const moe_vq_linear* L;
@@ -70,6 +71,7 @@ struct LinearCall {
   const void* dy;
   void *dx, *dw;
   float* dbias;
+  moe_vq_rows8 x8, z8;  // backward: x and z in 8 bits (q not null), instead of x and z
   void* ws;
 };
 hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipStream_t st);

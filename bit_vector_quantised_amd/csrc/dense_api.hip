@@ -1,40 +1,11 @@
 // C ABI of the row operators and the dense product: argument checks, workspace layout and
 // the launches.  Every check runs on the host before any HIP call.
-#include <initializer_list>
-
+#include "api_checks.h"
 #include "dense.h"
 
 using namespace mvq;
 
 namespace {
-
-constexpr int MAX_COLS = 65536;
-constexpr int MAX_ROWS = MAX_T * MAX_K;
-
-bool dtype_ok(int d) { return d == MOE_VQ_F32 || d == MOE_VQ_BF16; }
-bool off16(const void* p) { return ((uintptr_t)p & 15) != 0; }
-bool off4(const void* p) { return ((uintptr_t)p & 3) != 0; }
-
-// A buffer of n bytes (p null: not there).
-struct Span {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Span& a, const Span& b) {
-  return a.p && b.p && a.n && b.n && (uintptr_t)a.p < (uintptr_t)b.p + b.n && (uintptr_t)b.p < (uintptr_t)a.p + a.n;
-}
-// A buffer that is written shares a byte with another one, or with one that is read: a workgroup would write
-// it while another still reads, or writes, the same byte.
-bool clash(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
-  for (const Span* o = outs.begin(); o != outs.end(); ++o) {
-    for (const Span& i : ins)
-      if (overlap(*o, i)) return true;
-    for (const Span* q = o + 1; q != outs.end(); ++q)
-      if (overlap(*o, *q)) return true;
-  }
-  return false;
-}
-size_t size_of(int d) { return d == MOE_VQ_BF16 ? 2 : 4; }
 
 bool rows_dims_ok(int n_tokens, int top_k, int n_cols) {
   return n_tokens >= 0 && n_tokens <= MAX_T && top_k >= 1 && top_k <= MAX_K && n_cols >= 1 && n_cols <= MAX_COLS;
@@ -70,6 +41,49 @@ struct LinearSpans {
   LinearSpans(const moe_vq_linear* L, const LinearPlan& p, const int32_t* group_start)
       : w{L->w, (size_t)p.G * p.R * p.K * p.size}, bias{L->bias, (size_t)p.G * p.R * 4}, table{group_start, ((size_t)p.G + 1) * 4} {}
 };
+
+// Either gradient call: x and z as they are, or (kept8) in 8 bits.
+int backward(const moe_vq_linear* L, const void* x, const moe_vq_rows8* x8, int n_rows, const int32_t* group_start,
+             const void* z, const moe_vq_rows8* z8, const void* dy, int dy_dtype, void* dx, void* dw, float* dbias, void* ws,
+             size_t ws_bytes, void* stream, bool kept8) {
+  int st = check_linear(L, n_rows, group_start);
+  if (st) return st;
+  if (!dtype_ok(dy_dtype)) return MOE_VQ_EINVAL;
+  if (!dx && !dw && !dbias) return MOE_VQ_OK;
+  if (off16(x) || off16(z) || off16(dy) || off16(dx) || off16(dw) || off4(dbias)) return MOE_VQ_EINVAL;
+  if (x8 && (!x8->q || !x8->e || off16(x8->q))) return MOE_VQ_EINVAL;
+  if (z8 && (!z8->q || !z8->e || off16(z8->q))) return MOE_VQ_EINVAL;
+  if (n_rows > 0 && (!dy || (dw && !x && !x8) || (L->act != MOE_VQ_ACT_NONE && !z && !z8))) return MOE_VQ_EINVAL;
+  const LinearPlan p = linear_plan(L, n_rows, true, kept8);
+  if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
+  const LinearSpans in(L, p, group_start);
+  const bool act = L->act != MOE_VQ_ACT_NONE;
+  const Span dx_s{dx, (size_t)p.M * p.K * p.size}, dw_s{dw, in.w.n}, db_s{dbias, in.bias.n}, ws_s{ws, p.total};
+  const Span dy_s{dy, (size_t)p.M * p.N * size_of(dy_dtype)}, z_s{act ? z : nullptr, (size_t)p.M * p.R * p.size};
+  const Span x_s{dw ? x : nullptr, dx_s.n}, w_s{dx ? L->w : nullptr, in.w.n};  // (each read for one product only)
+  // In order: dz and its column sums from dy and z, then dx from w, then dw from x.  So dx and dw may lie over
+  // z, and over dy where dz is another tensor, and dw over w; without an activation both products read dy.
+  if (clash({dx_s, dw_s, db_s, ws_s}, {x_s, in.table}) || clash({db_s, ws_s}, {dy_s, z_s, w_s}) || overlap(dx_s, w_s) ||
+      (!act && (overlap(dx_s, dy_s) || overlap(dw_s, dy_s))))
+    return MOE_VQ_EINVAL;
+  const moe_vq_rows8 *xr = dw ? x8 : nullptr, *zr = act ? z8 : nullptr;
+  if (clash({dx_s, dw_s, db_s, ws_s}, {bytes8(xr, p.M, p.K), scales8(xr, p.M, p.K), bytes8(zr, p.M, p.R), scales8(zr, p.M, p.R)}))
+    return MOE_VQ_EINVAL;
+  LinearCall c{};
+  c.L = L;
+  c.x = x;
+  c.group_start = group_start;
+  c.y_dtype = dy_dtype;
+  c.z = const_cast<void*>(z);
+  if (x8) c.x8 = *x8;
+  if (z8) c.z8 = *z8;
+  c.dy = dy;
+  c.dx = dx;
+  c.dw = dw;
+  c.dbias = dbias;
+  c.ws = ws;
+  return hip_status(launch_linear_backward(p, c, static_cast<hipStream_t>(stream)));
+}
 
 }  // namespace
 
@@ -198,36 +212,19 @@ int moe_vq_linear_forward(const moe_vq_linear* L, const void* x, int n_rows, con
 int moe_vq_linear_backward(const moe_vq_linear* L, const void* x, int n_rows, const int32_t* group_start,
                            const void* z, const void* dy, int dy_dtype, void* dx, void* dw, float* dbias, void* ws,
                            size_t ws_bytes, void* stream) {
-  int st = check_linear(L, n_rows, group_start);
-  if (st) return st;
-  if (!dtype_ok(dy_dtype)) return MOE_VQ_EINVAL;
-  if (!dx && !dw && !dbias) return MOE_VQ_OK;
-  if (off16(x) || off16(z) || off16(dy) || off16(dx) || off16(dw) || off4(dbias)) return MOE_VQ_EINVAL;
-  if (n_rows > 0 && (!dy || (dw && !x) || (L->act != MOE_VQ_ACT_NONE && !z))) return MOE_VQ_EINVAL;
-  const LinearPlan p = linear_plan(L, n_rows, true);
-  if ((st = check_linear_ws(p, ws, ws_bytes))) return st;
-  const LinearSpans in(L, p, group_start);
-  const bool act = L->act != MOE_VQ_ACT_NONE;
-  const Span dx_s{dx, (size_t)p.M * p.K * p.size}, dw_s{dw, in.w.n}, db_s{dbias, in.bias.n}, ws_s{ws, p.total};
-  const Span dy_s{dy, (size_t)p.M * p.N * size_of(dy_dtype)}, z_s{act ? z : nullptr, (size_t)p.M * p.R * p.size};
-  const Span x_s{dw ? x : nullptr, dx_s.n}, w_s{dx ? L->w : nullptr, in.w.n};  // (each read for one product only)
-  // In order: dz and its column sums from dy and z, then dx from w, then dw from x.  So dx and dw may lie over
-  // z, and over dy where dz is another tensor, and dw over w; without an activation both products read dy.
-  if (clash({dx_s, dw_s, db_s, ws_s}, {x_s, in.table}) || clash({db_s, ws_s}, {dy_s, z_s, w_s}) || overlap(dx_s, w_s) ||
-      (!act && (overlap(dx_s, dy_s) || overlap(dw_s, dy_s))))
-    return MOE_VQ_EINVAL;
-  LinearCall c{};
-  c.L = L;
-  c.x = x;
-  c.group_start = group_start;
-  c.y_dtype = dy_dtype;
-  c.z = const_cast<void*>(z);
-  c.dy = dy;
-  c.dx = dx;
-  c.dw = dw;
-  c.dbias = dbias;
-  c.ws = ws;
-  return hip_status(launch_linear_backward(p, c, static_cast<hipStream_t>(stream)));
+  return backward(L, x, nullptr, n_rows, group_start, z, nullptr, dy, dy_dtype, dx, dw, dbias, ws, ws_bytes, stream, false);
+}
+
+size_t moe_vq_linear_bytes8(const moe_vq_linear* L, int n_rows) {
+  if (!linear_dims_ok(L) || n_rows < 0 || n_rows > MAX_ROWS) return 0;
+  return linear_max_bytes(L, n_rows, true, true);
+}
+
+int moe_vq_linear_backward8(const moe_vq_linear* L, const void* x, const moe_vq_rows8* x8, int n_rows,
+                            const int32_t* group_start, const void* z, const moe_vq_rows8* z8, const void* dy,
+                            int dy_dtype, void* dx, void* dw, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  if ((x && x8) || (z && z8)) return MOE_VQ_EINVAL;
+  return backward(L, x, x8, n_rows, group_start, z, z8, dy, dy_dtype, dx, dw, dbias, ws, ws_bytes, stream, true);
 }
 
 }  // extern "C"

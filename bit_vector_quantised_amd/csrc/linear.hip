@@ -25,7 +25,7 @@
 #include <type_traits>
 
 #include "dense.h"
-#include "moe_vq_device.h"
+#include "rows8_device.h"
 
 namespace mvq {
 
@@ -33,8 +33,6 @@ namespace {
 
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) char lds_char;
 typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
@@ -66,40 +64,6 @@ struct GemmArgs {
 };
 
 // ---------------------------------------------------------------------------------------
-// Activations
-// ---------------------------------------------------------------------------------------
-
-// Phi(-a) for a >= 0 from e = exp(-a^2 / 2): e q(a), with q(a) = erfc(a / sqrt(2)) exp(a^2 / 2) / 2, a smooth function
-// between 1/2 and 0.4 / a, as a polynomial in s = 1 / (1 + 0.23 a) fitted to its relative error over 0..14 (5e-8;
-// evaluated in fp32 4.2e-7).  The usual 1 + erf(z / sqrt(2)) loses what is left of Phi below z = -4, and is 0 from
-// -5.5 on; the library's erfcf keeps it (column sums of dz, 8192 x 8192 values in bf16: 52 us this way, 76 by
-// erff, 104 by erfcf).
-__device__ __forceinline__ float normal_tail(float a, float e) {
-  const float s = __builtin_amdgcn_rcpf(fmaf(0.23f, a, 1.0f));
-  constexpr float C[] = {-2.7751521e-05f, 0.09237833f, 0.08576334f, 0.119514026f, -0.032923725f,
-                         0.3014828f, -0.27813974f, 0.29042214f, -0.078469455f};
-  float q = C[8];
-#pragma unroll
-  for (int i = 7; i >= 0; --i) q = fmaf(q, s, C[i]);
-  return e * q;
-}
-__device__ __forceinline__ float normal_cdf(float z, float e) {
-  const float p = normal_tail(fabsf(z), e);
-  return z < 0.f ? p : 1.0f - p;
-}
-__device__ __forceinline__ float gelu(float z) { return z * normal_cdf(z, __expf(-0.5f * z * z)); }
-// (v_rcp_f32: within one unit in the last place)
-__device__ __forceinline__ float sigmoid_fast(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
-
-// d silu(z) / dz = s + z s (1 - s), s = sigmoid(z)
-__device__ __forceinline__ float silu_grad(float z, float s) { return s * (1.0f + z * (1.0f - s)); }
-// d gelu(z) / dz = Phi(z) + z phi(z)
-__device__ __forceinline__ float gelu_grad(float z) {
-  const float e = __expf(-0.5f * z * z);
-  return normal_cdf(z, e) + z * 0.39894228f * e;
-}
-
-// ---------------------------------------------------------------------------------------
 // Element types
 // ---------------------------------------------------------------------------------------
 
@@ -119,51 +83,6 @@ struct F32 {
       c = __builtin_amdgcn_mfma_f32_16x16x4f32(__builtin_bit_cast(float, av[j]), __builtin_bit_cast(float, bv[j]), c, 0, 0, 0);
   }
 };
-
-__device__ __forceinline__ float load_as_f32(const void* p, size_t i, int dtype) {
-  return dtype == MOE_VQ_BF16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-__device__ __forceinline__ void store_as(void* p, size_t i, int dtype, float v) {
-  if (dtype == MOE_VQ_BF16) static_cast<uint16_t*>(p)[i] = f32_to_bf16_rne(v);
-  else static_cast<float*>(p)[i] = v;
-}
-// Eight consecutive values from index i, the first `n` of them valid: as one or two accesses where all are.
-__device__ __forceinline__ void load8(const void* p, size_t i, int dtype, int n, float* v) {
-  if (n >= 8 && dtype == MOE_VQ_BF16) {
-    const u32x4_any u = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      v[2 * q] = bf16_bits_to_f32(w[q] & 0xFFFFu);
-      v[2 * q + 1] = __builtin_bit_cast(float, w[q] & 0xFFFF0000u);
-    }
-  } else if (n >= 8) {
-#pragma unroll
-    for (int q = 0; q < 8; q += 4) {
-      const f32x4_any u = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(p) + i + q);
-      v[q] = u.x; v[q + 1] = u.y; v[q + 2] = u.z; v[q + 3] = u.w;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
-  }
-}
-// STREAM: nontemporal stores, which leave the L2 to the operands that other tiles share.
-template <bool STREAM = false>
-__device__ __forceinline__ void store8(void* p, size_t i, int dtype, int n, const float* v) {
-  if (n >= 8 && dtype == MOE_VQ_BF16) {
-    store_vec<STREAM>(reinterpret_cast<u32x4_any*>(static_cast<uint16_t*>(p) + i),
-                      u32x4_any{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])});
-  } else if (n >= 8) {
-#pragma unroll
-    for (int q = 0; q < 8; q += 4)
-      store_vec<STREAM>(reinterpret_cast<f32x4_any*>(static_cast<float*>(p) + i + q), f32x4_any{v[q], v[q + 1], v[q + 2], v[q + 3]});
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < n) store_as(p, i + j, dtype, v[j]);
-  }
-}
 
 // Epilogue of eight consecutive output columns n.. of output row m: bias, z, activation, residual, one
 // rounding to the output's type.  v: the sums (SWIGLU: the gate's), u: the up sums.  z keeps the
@@ -774,6 +693,7 @@ __global__ __launch_bounds__(256) void pack_rows_kernel(const T* src, T* dst, si
 struct DzArgs {
   const void* dy;
   const void* z;
+  moe_vq_rows8 z8; // z in 8 bits
   void* dz;        // [M][pitch], or null (column sums only)
   float* bias;     // [splits][G][R] column sums, or null
   const int32_t* group_start;
@@ -818,7 +738,7 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
 // overlapping; rows of 1024 bytes, streamed loads or stores and half or twice the workgroups change
 // nothing or cost 2 to 3 us).  dz is rounded to the element type for the matrix products; the column
 // sums add the unrounded values in fp32, rows in a fixed order.
-template <int DTYPE, int DY_DTYPE, int ACT>
+template <int DTYPE, int DY_DTYPE, int ACT, bool Z8>
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
@@ -851,6 +771,16 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
     if (n == 0)
       for (int c = a.R; c < a.pitch; ++c) store_as(a.dz, row + c, DTYPE, 0.f);
   };
+  const size_t pitch8 = rows8_pitch(a.R);
+  auto load_z = [&](size_t r, int c, float* v) {  // eight columns of z from column c
+    if constexpr (Z8) {
+      const uint8_t *q = a.z8.q + r * pitch8, *e = a.z8.e + r * (pitch8 / 32);
+      if (a.N % 8 == 0) load8_q<true>(q, e, c, left, v);
+      else load8_q<false>(q, e, c, left, v);
+    } else {
+      load8(a.z, r * a.R + c, DTYPE, left, v);
+    }
+  };
   if (n < a.N) {
     for (int m = m0 + ty; m < m1; m += 2 * DZ_TY) {
       float dy[2][V], zg[2][V], zu[2][V], d[2][2][V];
@@ -859,8 +789,8 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
       for (int i = 0; i < 2; ++i) {
         const size_t r = i ? next : m;
         load8(a.dy, r * a.N + n, DY_DTYPE, left, dy[i]);
-        if (any) load8(a.z, r * a.R + n, DTYPE, left, zg[i]);
-        if (two) load8(a.z, r * a.R + a.N + n, DTYPE, left, zu[i]);
+        if (any) load_z(r, n, zg[i]);
+        if (two) load_z(r, a.N + n, zu[i]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) dz_values<ACT>(a, dy[i], zg[i], zu[i], d[i]);
@@ -997,10 +927,15 @@ void few_go(const GemmArgs& g, bool gated, hipStream_t st) {
 template <int DTYPE, int DY_DTYPE>
 void dz_go(const LinearPlan& p, const DzArgs& d, int act, hipStream_t st) {
   const dim3 grid(div_up(p.N, DZ_TX * 8), p.G, d.splits);
-  if (act == MOE_VQ_ACT_NONE) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_NONE><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
-  else if (act == MOE_VQ_ACT_SILU) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_SILU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
-  else if (act == MOE_VQ_ACT_GELU) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_GELU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
-  else dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_SWIGLU><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  auto go = [&](auto a) {
+    constexpr int ACT = decltype(a)::value;
+    if (d.z8.q) dz_kernel<DTYPE, DY_DTYPE, ACT, true><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+    else dz_kernel<DTYPE, DY_DTYPE, ACT, false><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  };
+  if (act == MOE_VQ_ACT_NONE) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_NONE, false><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  else if (act == MOE_VQ_ACT_SILU) go(std::integral_constant<int, MOE_VQ_ACT_SILU>{});
+  else if (act == MOE_VQ_ACT_GELU) go(std::integral_constant<int, MOE_VQ_ACT_GELU>{});
+  else go(std::integral_constant<int, MOE_VQ_ACT_SWIGLU>{});
 }
 
 void launch_dz(const LinearPlan& p, const DzArgs& d, int dy_dtype, int act, hipStream_t st) {
@@ -1043,7 +978,7 @@ T* at(void* base, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(b
 }  // namespace
 
 // bound: the workspace of every call with at most n_rows rows (fewer rows may take more splits).
-static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, bool bound) {
+static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, bool kept8, bool bound) {
   LinearPlan p{};
   p.M = n_rows; p.K = L->n_in; p.N = L->n_out; p.G = L->n_groups;
   p.R = L->act == MOE_VQ_ACT_SWIGLU ? 2 * p.N : p.N;
@@ -1055,7 +990,7 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   p.pack_k = p.Kp != p.K;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
-  p.xp = take(p.pack_k ? (size_t)p.M * p.Kp * p.size : 0);
+  p.xp = take(p.pack_k || kept8 ? (size_t)p.M * p.Kp * p.size : 0);
   p.wp = take(p.pack_k ? (size_t)p.G * p.R * p.Kp * p.size : 0);
   p.fwd = pick_cut(p.dtype, p.M, p.G, p.R, div_up(p.K, kt), true);
   p.few = p.G == 1 && p.M <= FEW_ROWS;
@@ -1091,8 +1026,12 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
   return p;
 }
 
-LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward) { return plan_of(L, n_rows, backward, false); }
-size_t linear_max_bytes(const moe_vq_linear* L, int n_rows, bool backward) { return plan_of(L, n_rows, backward, true).total; }
+LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward, bool kept8) {
+  return plan_of(L, n_rows, backward, kept8, false);
+}
+size_t linear_max_bytes(const moe_vq_linear* L, int n_rows, bool backward, bool kept8) {
+  return plan_of(L, n_rows, backward, kept8, true).total;
+}
 
 hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipStream_t st) {
   if (p.M == 0) return hipSuccess;
@@ -1137,7 +1076,7 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
   const void* dz = same ? c.dy : at<void>(c.ws, p.dz);
   if (need_dz || c.dbias) {
     DzArgs d{};
-    d.dy = c.dy; d.z = c.z;
+    d.dy = c.dy; d.z = c.z; d.z8 = c.z8;
     d.dz = need_dz ? at<void>(c.ws, p.dz) : nullptr;
     d.splits = p.split_bias;
     d.bias = !c.dbias ? nullptr : (d.splits > 1 ? at<float>(c.ws, p.bias_part) : c.dbias);
@@ -1150,8 +1089,17 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
   }
   const void* x = c.x;
   const void* w = c.L->w;
+  if (c.dw && c.x8.q) {  // (exact in either type)
+    Rows8Args r{};
+    r.q = c.x8.q; r.e = c.x8.e;
+    r.y = at<void>(c.ws, p.xp);
+    r.start = c.group_start; r.G = p.G;
+    r.M = p.M; r.C = p.K; r.pitch = p.Kp;
+    if (p.M > 0) launch_rows8_unpack(r, p.dtype, st);
+    x = r.y;
+  }
   if (p.pack_k) {
-    if (c.dw) x = pack_x(p, c, st);
+    if (c.dw && !c.x8.q) x = pack_x(p, c, st);
     if (c.dx) w = pack_w(p, c, st);
   }
   GemmArgs g{};

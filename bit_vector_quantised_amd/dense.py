@@ -12,7 +12,7 @@ tensor, another stream than the one it was made on waits for that one before its
 """
 from __future__ import annotations
 
-from typing import List, Optional, Tuple
+from typing import List, Optional, Tuple, Union
 
 import torch
 
@@ -65,6 +65,56 @@ class _OnDevice:
                 fn(*args, stream.cuda_stream)
 
 
+class Rows8(_OnDevice):
+    """Rows in 8 bits, for up to n_rows rows of n_cols columns: q [n_rows, pitch] holds e4m3 values (pitch: n_cols
+    rounded up to 32), e [n_rows, pitch / 32] a power of two (+ 127, as an exponent) for each 32 columns.  A value is
+    off by at most 1/16 of itself (by 2^-10 scales if it is below 2^-6 of them), and what the bytes stand for is
+    exact in bf16 and fp32.  Like a tensor it is the caller's: a call that reads it uses its first rows."""
+
+    def __init__(self, n_rows: int, n_cols: int, device="cuda"):
+        super().__init__(_device(device))
+        pitch = _lib.rows8_pitch(n_cols)
+        if pitch == 0 or not 0 <= n_rows <= (1 << 34) // pitch:
+            raise ValueError("invalid number of rows or columns")
+        self.n_rows, self.n_cols = n_rows, n_cols
+        self.q = self._new((n_rows, pitch), torch.uint8)
+        self.e = self._new((n_rows, pitch // 32), torch.uint8)
+        self._shapes = self.q.shape, self.e.shape
+
+    def desc(self, what: str, n_rows: int, n_cols: int, device) -> _lib.Rows8Desc:
+        """The addresses, for a call that takes n_rows rows of n_cols columns."""
+        if n_rows > self.n_rows or n_cols != self.n_cols or device != self.device:
+            raise ValueError(f"{what}: need up to {n_rows} rows of {n_cols} columns on {device}, "
+                             f"got {self.n_rows} of {self.n_cols} on {self.device}")
+        return _lib.Rows8Desc(_need(self.q, "q", self._shapes[0], torch.uint8, self.device),
+                              _need(self.e, "e", self._shapes[1], torch.uint8, self.device))
+
+    def _groups(self, group_start: Optional[torch.Tensor]) -> Tuple[int, int]:
+        if group_start is None:
+            return 0, 0
+        n = group_start.shape[0] - 1
+        return _need(group_start, "group_start", (n + 1,), torch.int32, self.device), n
+
+    def pack(self, x: torch.Tensor, group_start: Optional[torch.Tensor] = None) -> "Rows8":
+        """The first rows from x [M, n_cols], bf16 or fp32.  group_start [G + 1] (int32): rows in no group stay."""
+        M = x.shape[0]
+        p = _need(x, "x", (M, self.n_cols), x.dtype, self.device)
+        gs, n = self._groups(group_start)
+        self._call(_lib.rows8_pack, p, x_dtype_code(x), M, self.n_cols, gs, n, self.desc("self", M, self.n_cols, self.device))
+        return self
+
+    def unpack(self, n_rows: Optional[int] = None, out: Optional[torch.Tensor] = None,
+               group_start: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """The first n_rows rows (all; out's) as bf16 (as out).  Rows in no group of group_start stay as they were."""
+        if out is None:
+            out = torch.empty((self.n_rows if n_rows is None else n_rows, self.n_cols), dtype=torch.bfloat16, device=self.device)
+        M = out.shape[0] if n_rows is None else n_rows
+        o = _need(out, "out", (M, self.n_cols), out.dtype, self.device)
+        gs, n = self._groups(group_start)
+        self._call(_lib.rows8_unpack, self.desc("self", M, self.n_cols, self.device), M, self.n_cols, gs, n, o, x_dtype_code(out))
+        return out
+
+
 class ExpertRows(_OnDevice):
     """The pairs of up to max_tokens tokens in the order of their experts.  sort(ids) fills
     expert_start [E + 1], pair_row and row_pair [T*k] (int32, valid until the next sort);
@@ -92,9 +142,16 @@ class ExpertRows(_OnDevice):
         self.n_tokens = T
         return self.expert_start
 
-    def gather(self, x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """x [T, C] -> rows [T*k, C] in the order of the experts (rows of dropped pairs as they were)."""
+    def gather(self, x: Union[torch.Tensor, Rows8], out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """x [T, C] -> rows [T*k, C] in the order of the experts (rows of dropped pairs as they were).  From x in
+        8 bits the rows are the values that it stands for, in bf16 or fp32 (as out)."""
         T, k = self.n_tokens, self.top_k
+        if isinstance(x, Rows8):
+            C = x.n_cols
+            out = torch.empty((T * k, C), dtype=torch.bfloat16, device=self.device) if out is None else out
+            o = _need(out, "out", (T * k, C), out.dtype, self.device)
+            self._call(_lib.gather_rows8, x.desc("x", T, C, self.device), T, k, C, self.pair_row.data_ptr(), o, x_dtype_code(out))
+            return out
         C = x.shape[-1]
         p = _need(x, "x", (T, C), x.dtype, self.device)
         out = torch.empty((T * k, C), dtype=x.dtype, device=self.device) if out is None else out
@@ -146,16 +203,39 @@ class ExpertRows(_OnDevice):
                    x_dtype_code(rows), d if both else 0, p)
         return drows, dw
 
+    def act_backward(self, z: Rows8, dy: torch.Tensor, w: Optional[torch.Tensor] = None, act: str = "swiglu",
+                     swiglu_limit: float = 0.0, dz: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     dw: Optional[torch.Tensor] = None) -> None:
+        """The way back through an activation whose input z was kept in 8 bits [T*k, R], from the gradient dy
+        [T*k, n_out] of its output before the routing weights: those of dz [T*k, R] = w dy act'(z), y [T*k, n_out] =
+        w act(z) and dw [T, k] = <dy, act(z)> that are given are written (dz and y: bf16 or fp32; rows of dropped
+        pairs stay as they were).  w None: all 1."""
+        if act not in ACTS:
+            raise ValueError(f"act must be one of {', '.join(ACTS)}")
+        T, k = self.n_tokens, self.top_k
+        N = dy.shape[-1]
+        R = 2 * N if act == "swiglu" else N
+        g = _need(dy, "dy", (T * k, N), dy.dtype, self.device)
+        zp = z.desc("z", T * k, R, self.device)
+        wp = _need(w, "w", (T, k), torch.float32, self.device) if w is not None else 0
+        like = dz if dz is not None else y
+        kind = dy.dtype if like is None else like.dtype
+        dzp = _need(dz, "dz", (T * k, R), kind, self.device) if dz is not None else 0
+        yp = _need(y, "y", (T * k, N), kind, self.device) if y is not None else 0
+        dp = _need(dw, "dw", (T, k), torch.float32, self.device) if dw is not None else 0
+        self._call(_lib.act_backward8, zp, ACTS[act], float(swiglu_limit), T, k, N, self.pair_row.data_ptr(), wp, g,
+                   x_dtype_code(dy), dzp, yp, _lib.BF16 if kind == torch.bfloat16 else _lib.F32, dp)
+
 
 class Linear(_OnDevice):
     """y = act(x W^T + b) + residual for up to max_rows rows.  w: [R, n_in], or [G, R, n_in] for one
     matrix per group of rows; bf16 or fp32.  R is n_out, or 2 n_out for act "swiglu" (gate rows, then
     up rows; swiglu_limit: its clamp, 0 none).  bias: fp32 [R] or [G, R].  backward: make the
-    workspace of the gradients too.  Each call reads w and bias where they are at that time (a
+    workspace of the gradients too; kept8: and that of gradients from Rows8.  Each call reads w and bias where they are at that time (a
     captured graph where they were when it was captured)."""
 
     def __init__(self, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
-                 swiglu_limit: float = 0.0, max_rows: int = 1, backward: bool = False):
+                 swiglu_limit: float = 0.0, max_rows: int = 1, backward: bool = False, kept8: bool = False):
         super().__init__(_device(w.device))
         if act not in ACTS:
             raise ValueError(f"act must be one of {', '.join(ACTS)}")
@@ -170,6 +250,9 @@ class Linear(_OnDevice):
         self.c = _lib.LinearDesc(self.n_in, self.n_out, self.n_groups, ACTS[act], x_dtype_code(w), float(swiglu_limit))
         self._weights()
         need = [_lib.linear_bytes(self.c, max_rows, b) for b in (False, True)[:2 if backward else 1]]
+        self.kept8 = kept8
+        if kept8:
+            need.append(_lib.linear_bytes8(self.c, max_rows))
         if 0 in need:
             raise ValueError("invalid sizes")
         self.ws_bytes = max(need)
@@ -207,22 +290,32 @@ class Linear(_OnDevice):
                    self.ws_bytes)
         return out
 
-    def backward(self, x: Optional[torch.Tensor], dy: torch.Tensor, z: Optional[torch.Tensor] = None,
+    def backward(self, x: Union[torch.Tensor, Rows8, None], dy: torch.Tensor, z: Union[torch.Tensor, Rows8, None] = None,
                  group_start: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
                  dw: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None) -> None:
         """Gradients from dy [M, n_out] and the z that forward kept (not needed for act "none"): those of dx
-        [M, n_in], dw (as w) and dbias (as bias) that are given are written.  x may be None without dw."""
+        [M, n_in], dw (as w) and dbias (as bias) that are given are written.  x may be None without dw.  x
+        and z may be in 8 bits (kept8): dw and dz are then those of the values that they stand for."""
         M, gs = self._rows(dy, group_start)
         if x is None and dw is not None:
             raise ValueError("dw needs x")
-        xp = _need(x, "x", (M, self.n_in), self.dtype, self.device) if x is not None else 0
+        x8, z8 = isinstance(x, Rows8), isinstance(z, Rows8)
+        if (x8 or z8) and not self.kept8:
+            raise ValueError("made without kept8")
+        xp = x.desc("x", M, self.n_in, self.device) if x8 else \
+            _need(x, "x", (M, self.n_in), self.dtype, self.device) if x is not None else 0
         g = _need(dy, "dy", (M, self.n_out), dy.dtype, self.device)
-        zp = _need(z, "z", (M, self.n_rows_w), self.dtype, self.device) if z is not None else 0
+        zp = z.desc("z", M, self.n_rows_w, self.device) if z8 else \
+            _need(z, "z", (M, self.n_rows_w), self.dtype, self.device) if z is not None else 0
         xd = _need(dx, "dx", (M, self.n_in), self.dtype, self.device) if dx is not None else 0
         wd = _need(dw, "dw", self.w_shape, self.dtype, self.device) if dw is not None else 0
         bd = _need(dbias, "dbias", self.w_shape[:-1], torch.float32, self.device) if dbias is not None else 0
-        self._call(_lib.linear_backward, self._weights(), xp, M, gs, zp, g, x_dtype_code(dy), xd, wd, bd, self.ws.data_ptr(),
-                   self.ws_bytes)
+        if x8 or z8:
+            self._call(_lib.linear_backward8, self._weights(), 0 if x8 else xp, xp if x8 else None, M, gs, 0 if z8 else zp,
+                       zp if z8 else None, g, x_dtype_code(dy), xd, wd, bd, self.ws.data_ptr(), self.ws_bytes)
+        else:
+            self._call(_lib.linear_backward, self._weights(), xp, M, gs, zp, g, x_dtype_code(dy), xd, wd, bd,
+                       self.ws.data_ptr(), self.ws_bytes)
 
 
 class DenseExperts:

@@ -477,6 +477,109 @@ int moe_vq_linear_backward(const moe_vq_linear *lin, const void *x, int n_rows, 
                            const void *z, const void *dy, int dy_dtype, void *dx, void *dw, float *dbias,
                            void *ws, size_t ws_bytes, void *stream);
 
+/* ---- Around the experts: the norm before the router and the experts, the choice of experts from
+ * the router's logits in the forms beyond route_topk's, and rows kept in 8 bits between the
+ * forward and the backward pass.  Conventions of the calls above: sums in fp32 in a fixed
+ * order, nothing left in a workspace, every call may be captured, overlaps refused unless the
+ * text allows them. */
+
+/* Rows in 8 bits.  q [n_rows][pitch]: e4m3 values, pitch = moe_vq_rows8_pitch(n_cols), n_cols rounded up to
+ * a multiple of 32 (the columns behind the last are zeros); e [n_rows][pitch/32]: E8M0 exponents
+ * of the scales, one for each block of 32 columns.  A value is q * 2^(e-127), NaN where e is 255, and
+ * exact in bf16 and fp32 where e is 17..247.  q 16-byte aligned. */
+typedef struct moe_vq_rows8 {
+  uint8_t *q;
+  uint8_t *e;
+} moe_vq_rows8;
+
+/* [host] Bytes of a row of q, 0 unless 1 <= n_cols <= 32768. */
+size_t moe_vq_rows8_pitch(int n_cols);
+
+/* x [n_rows][n_cols] in dtype to rows in 8 bits: a block's scale is the smallest power of two, 2^-110 or
+ * more, that brings its largest magnitude to 448 or less, and each value is rounded to the nearest
+ * e4m3 value (ties to even); a block that holds an infinity or NaN gets e = 255.  group_start
+ * [n_groups + 1] (device) or NULL: rows outside group_start[0] .. group_start[n_groups]-1 are neither read nor
+ * written.  x 16-byte aligned; n_rows * pitch <= 2^34. */
+int moe_vq_rows8_pack(const void *x, int dtype, int n_rows, int n_cols, const int32_t *group_start, int n_groups,
+                      const moe_vq_rows8 *r, void *stream);
+
+/* The values again: x [n_rows][n_cols] in dtype.  Rows outside the groups are left as they were. */
+int moe_vq_rows8_unpack(const moe_vq_rows8 *r, int n_rows, int n_cols, const int32_t *group_start, int n_groups,
+                        void *x, int dtype, void *stream);
+
+/* moe_vq_gather_rows from tokens' rows in 8 bits: xs[pair_row[t*k + i]] = the values of row t, in dtype. */
+int moe_vq_gather_rows8(const moe_vq_rows8 *r, int n_tokens, int top_k, int n_cols, const int32_t *pair_row,
+                        void *xs, int dtype, void *stream);
+
+/* The way back through an activation from z in 8 bits, for routed pairs p = t*k + i with row r = pair_row[p] of
+ * z8 [n_tokens*k][R], R = n_out or 2 n_out as in moe_vq_linear, dy [n_tokens*k][n_out] in dy_dtype:
+ *   dz[r] = w[p] dy[r] act'(z[r])    y[r] = w[p] act(z[r])    dw[p] = <dy[r], act(z[r])>
+ * dz and y in dtype, dw fp32; each may be NULL, and w (all 1).  With dy the gradient before the weights
+ * (of the experts' plain outputs) this is the gradient of a sum of w[p] W act(z[r]): of z, of w,
+ * and, by y, of W.  A dropped pair's dw is 0; rows that no pair names are neither read nor written.  dw may
+ * be w.  A value that the SwiGLU clamp cut has no gradient. */
+int moe_vq_act_backward8(const moe_vq_rows8 *z8, int act, float swiglu_limit, int n_tokens, int top_k, int n_out,
+                         const int32_t *pair_row, const float *w, const void *dy, int dy_dtype, void *dz, void *y,
+                         int dtype, float *dw, void *stream);
+
+/* moe_vq_linear_backward with x or z, or both, in 8 bits (x8, z8: NULL where the plain one is given): dz is
+ * made from the values of z8, dw from those of x8.  None of q and e may overlap an output or the workspace, of
+ * moe_vq_linear_bytes8 bytes. */
+size_t moe_vq_linear_bytes8(const moe_vq_linear *lin, int n_rows);
+int moe_vq_linear_backward8(const moe_vq_linear *lin, const void *x, const moe_vq_rows8 *x8, int n_rows,
+                            const int32_t *group_start, const void *z, const moe_vq_rows8 *z8, const void *dy,
+                            int dy_dtype, void *dx, void *dw, float *dbias, void *ws, size_t ws_bytes, void *stream);
+
+/* Root-mean-square norm with the residual's addition: s = x + residual, y = s / sqrt(mean(s^2) + eps) * gain over
+ * each row.  x [n_rows][n_cols] in dtype; residual (or NULL) and s in s_dtype; gain fp32 [n_cols]; y in
+ * y_dtype; y8: y in 8 bits.  s, y and y8 may each be NULL.  s is rounded once; y and y8 are made from the unrounded
+ * sum, each rounded once.  Squares are summed in fp32: magnitudes up to 1e17.  s may be residual,
+ * s or y may be x of the same type.  1 <= n_cols <= 16384, eps > 0; x, residual, s, y 16-byte aligned. */
+int moe_vq_norm_forward(const void *x, int dtype, const void *residual, void *s, int s_dtype, int n_rows, int n_cols,
+                        const float *gain, float eps, void *y, int y_dtype, const moe_vq_rows8 *y8, void *stream);
+
+/* [host] Workspace bytes of moe_vq_norm_backward for up to n_rows rows, 0 if an argument is invalid. */
+size_t moe_vq_norm_bytes(int n_rows, int n_cols);
+
+/* Gradients of the norm from its s (x, if nothing was added) and the gradient dy + dy2 of y (dy2 may be NULL):
+ *   dx = ds + the gradient through y (of x and of residual alike; ds, in dx_dtype, the gradient of s, or NULL)
+ *   dgain [n_cols] fp32 = the sum over the rows of (dy + dy2) s / sqrt(mean(s^2) + eps)
+ * dx or dgain may be NULL (ws is used for dgain only); with n_rows = 0 dgain is zeros.  dx may be ds. */
+int moe_vq_norm_backward(const void *s, int s_dtype, int n_rows, int n_cols, const float *gain, float eps,
+                         const void *dy, const void *dy2, int dy_dtype, const void *ds, void *dx, int dx_dtype,
+                         float *dgain, void *ws, size_t ws_bytes, void *stream);
+
+enum moe_vq_score { MOE_VQ_SCORE_SOFTMAX = 0, MOE_VQ_SCORE_SIGMOID = 1 };
+
+/* [host] How experts are chosen from logits l.  Scores s = softmax(l) or sigmoid(l), values v = s + bias.  The experts
+ * lie in n_groups equal groups of neighbours; the top_groups groups with the largest sums of their group_best
+ * largest values stay (equal sums: the lower group), and of their experts the top_k with the largest values
+ * are chosen, in that order (equal ones: the lower number; without a bias by the logits, which have the scores'
+ * order).  The order is that of the values themselves, as 64-bit arithmetic tells them apart.  Weights are
+ * scale * s, or with renorm scale * s over the chosen experts' sum; the bias has no part in them. */
+typedef struct moe_vq_choice {
+  int32_t n_experts;   /* 1..1024                                          */
+  int32_t top_k;       /* 1..32, at most the experts of top_groups groups  */
+  int32_t score;       /* enum moe_vq_score                                */
+  int32_t n_groups;    /* 1..64, divides n_experts                         */
+  int32_t top_groups;  /* 1..n_groups (n_groups: no choice of groups)      */
+  int32_t group_best;  /* 1 or 2                                           */
+  int32_t renorm;      /* 0 or 1                                           */
+  float scale;         /* finite                                           */
+  const float *bias;   /* device, [n_experts], or NULL                     */
+} moe_vq_choice;
+
+/* logits fp32 [n_tokens][E] -> ids and w [n_tokens][k].  An expert whose logit or bias is -inf or NaN is off: it has
+ * no score and is not chosen.  Places that no expert is left for get id -1 (a dropped pair of
+ * moe_vq_sort_pairs) and weight 0; a token whose experts are all off has only such places.  0 <= n_tokens <= 65536. */
+int moe_vq_choose(const moe_vq_choice *c, const float *logits, int n_tokens, int32_t *ids, float *w, void *stream);
+
+/* dlogits [n_tokens][E], the gradient of the logits, from dw [n_tokens][k] of the weights at the ids that were chosen
+ * (the choice itself and the bias have none).  Places with an id outside 0..E-1 and experts that are off have no
+ * part.  dlogits may be logits. */
+int moe_vq_choose_backward(const moe_vq_choice *c, const float *logits, int n_tokens, const int32_t *ids,
+                           const float *dw, float *dlogits, void *stream);
+
 /* [host] Text of the last HIP runtime error seen by a call of this library on the
  * calling thread (the reason behind MOE_VQ_EHIP), or "" if none. */
 const char *moe_vq_last_hip_error(void);
