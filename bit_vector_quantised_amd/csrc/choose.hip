@@ -8,9 +8,9 @@
 // An expert whose logit or bias is -inf or NaN is off: it has no score and is never chosen.  Places that no expert
 // is left for get expert -1 and weight 0.
 //
-// The order has to be that of the values themselves, which fp32 scores do not always tell apart: a wave that finds
-// two values it has to order (or two groups at the border) closer than fp32's errors takes its token again in 64
-// bits.  Weights need no such care.  They are computed relative to the largest chosen score, so that
+// The order has to be that of the values themselves, which fp32 scores do not always tell apart: a token with two values
+// to be ordered (or two groups at the border) closer than fp32's errors is taken again in 64 bits.
+// Weights need no such care.  They are computed relative to the largest chosen score, so that
 // scores too small for fp32 still share their token.
 #include <cmath>
 
@@ -21,202 +21,449 @@ namespace mvq {
 
 namespace {
 
-constexpr int CHOOSE_THREADS = 256;  // a token per wave
+constexpr int CHOOSE_THREADS = 256, CHOOSE_WAVES = CHOOSE_THREADS / 64;
 
-__device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    const double o = __shfl_xor(v, d);
-    v = o > v ? o : v;
+// ---------------------------------------------------------------------------------------
+// A token by L lanes (16, or the wave)
+// ---------------------------------------------------------------------------------------
+
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  v = fmaxf(v, dpp_f32<dpp::QUAD_XOR1>(v));
+  v = fmaxf(v, dpp_f32<dpp::QUAD_XOR2>(v));
+  v = fmaxf(v, dpp_f32<dpp::ROW_HALF_MIRROR>(v));
+  v = fmaxf(v, dpp_f32<dpp::ROW_MIRROR>(v));
+  if (L == 64) v = fmaxf(fmaxf(lane_f32(v, 0), lane_f32(v, 16)), fmaxf(lane_f32(v, 32), lane_f32(v, 48)));
+  return v;
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_with(uint32_t v) {
+  const uint32_t o = (uint32_t)dpp_i32<CTRL>((int)v);
+  return o > v ? o : v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t max_of(uint32_t v) {
+  v = max_with<dpp::QUAD_XOR1>(v);
+  v = max_with<dpp::QUAD_XOR2>(v);
+  v = max_with<dpp::ROW_HALF_MIRROR>(v);
+  v = max_with<dpp::ROW_MIRROR>(v);
+  if (L == 64) {
+    const uint32_t r0 = __builtin_amdgcn_readlane((int)v, 0), r1 = __builtin_amdgcn_readlane((int)v, 16),
+                   r2 = __builtin_amdgcn_readlane((int)v, 32), r3 = __builtin_amdgcn_readlane((int)v, 48);
+    const uint32_t a = r0 > r1 ? r0 : r1, b = r2 > r3 ? r2 : r3;
+    v = a > b ? a : b;
   }
   return v;
 }
-__device__ __forceinline__ double wave_total(double v) {
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d);
-  return v;
-}
-__device__ __forceinline__ float wave_total(float v) { return wave_sum(v); }
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
 
-// A token's scores over a wave: expert e = lane + 64 i in entry i.
-template <typename T, int NPL>
-__device__ __forceinline__ void scores(const ChooseArgs& a, const float* l, T* s, T& total, float top) {
-  T sum = 0;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    if (a.sigmoid) {
-      s[i] = T(1) / (T(1) + exp_of(-T(l[i])));
-    } else {
-      // (an infinite logit takes everything, several share it)
-      s[i] = l[i] == -INFINITY ? T(0) : (l[i] == top ? T(1) : exp_of(T(l[i]) - T(top)));
-      sum += s[i];
-    }
-  }
-  if (!a.sigmoid) {
-    total = wave_total(sum);
-    const T inv = total > 0 ? T(1) / total : T(0);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) s[i] = sizeof(T) == 8 ? (total > 0 ? s[i] / total : T(0)) : s[i] * inv;
-  }
-}
-
-// The expert with the largest of v over the wave (the lowest of equal ones), or -1 if all are -inf; its entry is
-// set to -inf, and its logit goes to *at.
-template <typename T, int NPL>
-__device__ __forceinline__ int take_best(T* v, const float* l, int lane, T& best, float* at = nullptr) {
-  best = v[0];
-#pragma unroll
-  for (int i = 1; i < NPL; ++i) best = v[i] > best ? v[i] : best;
-  best = wave_max(best);
-  if (best == T(-INFINITY)) return -1;
-  int id = -1;
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const uint64_t m = __ballot(v[i] == best);
-    if (id < 0 && m) {
-      const int from = __builtin_ctzll(m);
-      id = 64 * i + from;
-      if (at) *at = lane_f32(l[i], from);
-      if (lane == from) v[i] = T(-INFINITY);
-    }
-  }
-  return id;
-}
-
-// The k experts in order: place j's in lane j (-1: none) with its logit.  Returns whether T tells them apart.
-template <typename T, int NPL>
-__device__ __forceinline__ bool choose(const ChooseArgs& a, const float* l, const float* b, int lane, float top, float b_most,
-                                       int& my_id, float& my_l, T& total) {
-  constexpr bool SINGLE = sizeof(T) == 4;
-  const T NONE = T(-INFINITY);
-  T rank[NPL];
-  T near = 0;  // how close two values may be for T to order them
-  const bool groups = a.top_groups < a.groups;
-  if (a.bias || groups || !(a.renorm || a.sigmoid)) {
-    scores<T, NPL>(a, l, rank, total, top);
-    if (SINGLE) {
-      // fp32: a score is within 2^-21 of the largest, its sum with b within 2^-24 of itself
-      float most = rank[0];
-#pragma unroll
-      for (int i = 1; i < NPL; ++i) most = fmaxf(most, rank[i]);
-      near = ldexpf(wave_max(most) + b_most, -19);
-    }
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-      const T v = a.bias ? rank[i] + T(b[i]) : rank[i];
-      rank[i] = l[i] == -INFINITY ? NONE : v;
-    }
-  }
-  bool sure = true;
-  uint64_t taken = ~0ull;  // groups, 64 of them at most
-  if (groups) {
-    const int size = a.E / a.groups;
-    T mine = NONE;  // lane g: the value of group g
-    for (int g = 0; g < a.groups; ++g) {
-      T v[NPL], sum = 0, best;
-#pragma unroll
-      for (int i = 0; i < NPL; ++i) {
-        const int e = lane + 64 * i;
-        v[i] = e >= g * size && e < (g + 1) * size ? rank[i] : NONE;
-      }
-      bool any = false;
-      for (int j = 0; j < a.best; ++j) {
-        if (take_best<T, NPL>(v, l, lane, best) < 0) break;
-        sum += best;
-        any = true;
-      }
-      if (lane == g) mine = any ? sum : NONE;
-    }
-    taken = 0;
-    T v[1] = {mine}, last = 0, best;
-    for (int j = 0; j <= a.top_groups; ++j) {
-      const int g = take_best<T, 1>(v, l, lane, best);
-      if (g < 0) break;
-      if (j == a.top_groups) sure = sure && !(SINGLE && last - best <= 2 * near);  // (groups' values are sums of two)
-      else taken |= 1ull << g;
-      last = best;
-    }
-  }
-  if (!a.bias) {
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) rank[i] = T(l[i]);
-  }
-  if (groups) {
-    const int size = a.E / a.groups;
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) rank[i] = (taken >> ((lane + 64 * i) / size)) & 1 ? rank[i] : NONE;
-  }
-  my_id = -1;
-  my_l = -INFINITY;
-  T last = 0;
-  for (int j = 0; j < a.k + (SINGLE && a.bias ? 1 : 0); ++j) {
-    T best;
-    float at = 0.f;
-    const int id = take_best<T, NPL>(rank, l, lane, best, &at);
-    if (id < 0) break;
-    if (SINGLE && a.bias && j > 0 && last - best <= near) sure = false;
-    last = best;
-    if (lane == j && j < a.k) { my_id = id; my_l = at; }
-  }
-  return sure;
-}
-
-// log sigmoid(l)
-__device__ __forceinline__ float log_sigmoid(float l) { return fminf(l, 0.f) - log1pf(expf(-fabsf(l))); }
-
-// The weights of the chosen experts, place j's in lane j: score (of the sums' share, or alone).
+// The weights of the chosen experts, place j's in lane j of L: score (of the sums' share, or alone).
+template <int L>
 __device__ __forceinline__ float weight_of(const ChooseArgs& a, bool chosen, float l, float top, float total) {
   if (!a.renorm) {
     if (!chosen) return 0.f;
     if (a.sigmoid) return 1.0f / (1.0f + expf(-l));
     return (l == top ? 1.f : expf(l - top)) / total;
   }
-  const float s = !chosen ? -INFINITY : (a.sigmoid ? log_sigmoid(l) : l);
-  const float most = wave_max(s);
-  const float p = !chosen ? 0.f : (s == most ? 1.f : expf(s - most));
-  const float sum = wave_sum(p);
+  // relative to the largest chosen score: exp(l - most), for sigmoid over 1 + exp(l) if that is at most 2
+  const float first = max_of<L>(chosen ? l : -INFINITY), most = a.sigmoid ? fminf(first, 0.f) : first;
+  float p = l == most ? 1.f : __expf(l - most);
+  if (a.sigmoid) p = (l < 0.f ? p : 1.f) * __builtin_amdgcn_rcpf(1.0f + __expf(-fabsf(l)));
+  if (!chosen) p = 0.f;
+  const float sum = group_sum<L>(p);
   return chosen ? p / sum : 0.f;
 }
 
-// The token's logits (-inf where an expert is off), the biases and the largest of both.
-template <int NPL>
-__device__ __forceinline__ float load_logits(const ChooseArgs& a, int t, int lane, float* l, float* b, float& b_most) {
-  float top = -INFINITY;
-  b_most = 0.f;
+// The expert of entry i of lane j: four neighbours per lane and 16-byte load.
+template <int L>
+__device__ __forceinline__ int expert_of(int i, int j) { return (i >> 2) * (L * 4) + j * 4 + (i & 3); }
+
+// (no branch around a load, so that all of them go out at once: entries without an expert repeat the first)
+template <int L, int N>
+__device__ __forceinline__ void load_row(const float* row, int E, int j, float* v) {
+  if (E % 4 == 0) {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 64 * i;
-    l[i] = e < a.E ? a.logits[(size_t)t * a.E + e] : -INFINITY;
-    b[i] = a.bias && e < a.E ? a.bias[e] : 0.f;
-  }
+    for (int i = 0; i < N; i += 4) {
+      const int e = expert_of<L>(i, j);
+      const f32x4_any u = *reinterpret_cast<const f32x4_any*>(row + (e < E ? e : 0));
+      v[i] = u.x; v[i + 1] = u.y; v[i + 2] = u.z; v[i + 3] = u.w;
+    }
+  } else {
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    if (!(l[i] > -INFINITY) || !(b[i] > -INFINITY)) l[i] = -INFINITY;  // off (NaN too)
-    top = fmaxf(top, l[i]);
-    b_most = fmaxf(b_most, fabsf(b[i]));
+    for (int i = 0; i < N; ++i) {
+      const int e = expert_of<L>(i, j);
+      v[i] = row[e < E ? e : 0];
+    }
   }
-  if (a.bias) b_most = wave_max(b_most);
-  return wave_max(top);
+}
+// A token's logits (-inf where an expert is off: where l + b is -inf or NaN) and the biases.
+template <int L, int N>
+__device__ __forceinline__ void load_token(const ChooseArgs& a, int t, int j, float* l, float* b) {
+  load_row<L, N>(a.logits + (size_t)t * a.E, a.E, j, l);
+#pragma unroll
+  for (int i = 0; i < N; ++i) b[i] = 0.f;
+  if (a.bias) load_row<L, N>(a.bias, a.E, j, b);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    l[i] = expert_of<L>(i, j) < a.E && l[i] + b[i] > -INFINITY ? l[i] : -INFINITY;
+}
+// Scores, for softmax also the sum of exp(l - top).  exp and 1/x by the hardware: an error of |x| 2^-24 of
+// the exponential beside a few roundings.
+template <int L, int N>
+__device__ __forceinline__ void scores(const ChooseArgs& a, const float* l, float top, float* s, float& total) {
+  if (a.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
+    return;
+  }
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // (an infinite logit takes everything, several share it)
+    s[i] = l[i] == -INFINITY ? 0.f : (l[i] == top ? 1.f : __expf(l[i] - top));
+    sum += s[i];
+  }
+  total = group_sum<L>(sum);
+  const float inv = total > 0.f ? 1.0f / total : 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] *= inv;
 }
 
-template <int NPL>
-__global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
-  const int lane = threadIdx.x & 63, t = blockIdx.x * (CHOOSE_THREADS / 64) + (threadIdx.x >> 6);
-  if (t >= a.T) return;
-  float l[NPL], b[NPL], b_most;
-  const float top = load_logits<NPL>(a, t, lane, l, b, b_most);
-  int id;
-  float at, total = 1.f;
-  if (!choose<float, NPL>(a, l, b, lane, top, b_most, id, at, total)) {
-    double wide;
-    choose<double, NPL>(a, l, b, lane, top, b_most, id, at, wide);
+constexpr int log2_of(int n) { return n <= 1 ? 0 : 1 + log2_of(n / 2); }
+
+// LDS as the wave's own: its accesses complete in order, the fences keep the compiler to it.
+__device__ __forceinline__ void lds_turn() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The two largest of this lane's two and another lane's.
+template <int CTRL>
+__device__ __forceinline__ void two_best(float& m1, float& m2) {
+  const float o1 = dpp_f32<CTRL>(m1), o2 = dpp_f32<CTRL>(m2);
+  m2 = fmaxf(fminf(m1, o1), fmaxf(m2, o2));
+  m1 = fmaxf(m1, o1);
+}
+
+template <int I, int J>
+__device__ __forceinline__ void order_two(uint32_t* k) {  // the larger first
+  const uint32_t x = k[I], y = k[J];
+  k[I] = x > y ? x : y;
+  k[J] = x > y ? y : x;
+}
+// N words, the largest first (a merge exchange network over powers of two).
+template <int N>
+__device__ __forceinline__ void order_all(uint32_t* k) {
+  static_for<0, log2_of(N)>([&](auto pp) {
+    constexpr int P = 1 << decltype(pp)::value;
+    static_for<0, decltype(pp)::value + 1>([&](auto qq) {
+      constexpr int K = P >> decltype(qq)::value;
+      static_for<0, N>([&](auto ii) {
+        constexpr int I = decltype(ii)::value, J0 = K % P;
+        if constexpr (I >= J0 && (I - J0) % (2 * K) < K && I + K < N && I / (2 * P) == (I + K) / (2 * P)) order_two<I, I + K>(k);
+      });
+    });
+  });
+}
+
+// ---- A token by the whole wave in 64 bits: expert e = lane + 64 i in entry i.  Hardly any token comes here, but a
+// wave that does is the last of its launch (of 16384 tokens among 256 experts some 40 do).
+
+template <int CTRL>
+__device__ __forceinline__ double max_with(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp_i32<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp_i32<CTRL>((int)(u >> 32));
+  return fmax(v, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ double lane_f64(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, lane), hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ double wave_max64(double v) {
+  v = max_with<dpp::QUAD_XOR1>(v);
+  v = max_with<dpp::QUAD_XOR2>(v);
+  v = max_with<dpp::ROW_HALF_MIRROR>(v);
+  v = max_with<dpp::ROW_MIRROR>(v);
+  return fmax(fmax(lane_f64(v, 0), lane_f64(v, 16)), fmax(lane_f64(v, 32), lane_f64(v, 48)));
+}
+
+// The entry with the largest of v over the wave (of equal ones the lowest expert), which is set to -inf; -1 if all are.
+template <int N>
+__device__ __forceinline__ int take_best(double* v, int lane, double& best) {
+  best = v[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) best = fmax(best, v[i]);
+  best = wave_max64(best);
+  int id = -1;
+#pragma unroll
+  for (int i = N - 1; i >= 0; --i) {
+    const uint64_t m = __ballot(v[i] == best);
+    id = m ? 64 * i + __builtin_ctzll(m) : id;
   }
-  const float w = weight_of(a, id >= 0, at, top, total);
-  if (lane < a.k) {
-    a.ids[(size_t)t * a.k + lane] = id;
-    a.w[(size_t)t * a.k + lane] = id >= 0 ? a.scale * w : 0.f;
+  if (!(best > -INFINITY)) return -1;
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = id == lane + 64 * i ? -INFINITY : v[i];
+  return id;
+}
+
+// Place j's expert in lane j (-1: none).
+template <int N>
+__device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, float top) {
+  const double NONE = -INFINITY;
+  float l[N];
+  double v[N], sum = 0;
+  const bool groups = a.top_groups < a.groups;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = lane + 64 * i, at = e < a.E ? e : 0;
+    const float x = a.logits[(size_t)t * a.E + at], b = a.bias ? a.bias[at] : 0.f;
+    l[i] = e < a.E && x + b > -INFINITY ? x : -INFINITY;
+    v[i] = l[i];
+  }
+  if (a.bias || groups) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (a.sigmoid) v[i] = 1.0 / (1.0 + exp(-(double)l[i]));
+      else v[i] = l[i] == top ? 1.0 : exp((double)l[i] - top);
+      if (l[i] == -INFINITY) v[i] = 0.0;
+      sum += v[i];
+    }
+    if (!a.sigmoid) {
+#pragma unroll
+      for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = lane + 64 * i;
+      if (!a.sigmoid) v[i] /= sum;
+      if (a.bias) v[i] += (double)a.bias[e < a.E ? e : 0];
+      if (l[i] == -INFINITY) v[i] = NONE;
+    }
+  }
+  double best;
+  if (groups) {
+    const int size = a.E / a.groups;
+    double of[1] = {NONE};  // lane g: the value of group g
+#pragma unroll 1
+    for (int g = 0; g < a.groups; ++g) {
+      double part[N], two = 0;
+      int there = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = lane + 64 * i - g * size;
+        part[i] = e >= 0 && e < size ? v[i] : NONE;
+      }
+#pragma unroll 1
+      for (int j = 0; j < a.best; ++j)
+        if (take_best<N>(part, lane, best) >= 0) { two += best; ++there; }
+      if (lane == g && there) of[0] = two;
+    }
+    uint64_t taken = 0;
+#pragma unroll 1
+    for (int j = 0; j < a.top_groups; ++j) {
+      const int g = take_best<1>(of, lane, best);
+      if (g >= 0) taken |= 1ull << g;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool on = l[i] > -INFINITY && ((taken >> ((lane + 64 * i) / size)) & 1);
+      v[i] = !on ? NONE : (a.bias ? v[i] : (double)l[i]);
+    }
+  }
+  int mine = -1;
+#pragma unroll 1
+  for (int r = 0; r < a.k; ++r) {
+    const int id = take_best<N>(v, lane, best);
+    mine = lane == r ? id : mine;
+  }
+  return mine;
+}
+
+// The choice: 64 / L tokens of a wave side by side, N experts in a lane.  Values become whole numbers of
+// BITS bits over their range with the expert's number below them, so that a round of the choice is a maximum of 32-bit
+// words that are all different, and ties fall to the lower expert.
+template <int L, int N>
+__global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
+  constexpr int TOK = 64 / L, ID_BITS = L == 16 ? 8 : 10, BITS = 32 - ID_BITS;
+  constexpr uint32_t ID_MASK = (1u << ID_BITS) - 1;
+  static_assert(L * N <= 1 << ID_BITS, "an expert's number fits");
+  constexpr float UNITS = (float)(1 << BITS);
+  constexpr int ROW = L * N + L * N / 32;  // values of a token in LDS, one more place behind each 32
+  __shared__ float lds[CHOOSE_WAVES][TOK][ROW];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L, slot = lane / L;
+  const int t0 = (blockIdx.x * CHOOSE_WAVES + wave) * TOK;
+  if (t0 >= a.T) return;
+  const bool there = t0 + slot < a.T;
+  const int t = there ? t0 + slot : a.T - 1;
+  float l[N], b[N], v[N], top = -INFINITY, b_most = 0.f, total = 1.f;
+  load_token<L, N>(a, t, j, l, b);
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, l[i]);
+  top = max_of<L>(top);
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) b_most = fmaxf(b_most, l[i] > -INFINITY ? fabsf(b[i]) : 0.f);
+    b_most = max_of<L>(b_most);
+  }
+  const bool groups = a.top_groups < a.groups;
+  bool sure = top < INFINITY;
+  float near = 0.f, most = 0.f;  // how close two values may be for fp32 to order them; the largest score
+  if (a.bias || groups || !(a.renorm || a.sigmoid)) {
+    scores<L, N>(a, l, top, v, total);
+    most = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-top)) : (total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f);
+    // A score is off by at most 2^-21 (1 + |top| / 4 if top < 0) of the largest (for l <= top < 0 |l| exp(l) is at most
+    // (|top| + 1) exp(top)), its sum with b by 2^-24 of itself; two of them, with room.
+    near = ldexpf(most * (1.0f + fmaxf(-top, 0.f) * 0.25f) + b_most, -19);
+    if (!(top > -INFINITY)) near = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = l[i] == -INFINITY ? -INFINITY : v[i] + b[i];
+  }
+  uint64_t taken = ~0ull;
+  const int size = a.E / a.groups;
+  const uint32_t per = (1u << 20) / size + 1;  // e / size = e * per >> 20 (e, size <= 1024)
+  if (groups) {
+    float* part = &lds[wave][slot][0];
+    const int w = size >> 2;  // lanes of a group
+    if (size % 4 == 0 && w <= 16 && (w & (w - 1)) == 0) {
+      // a group's two best by exchanges between the lanes that hold it
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        float m1 = fmaxf(v[i], v[i + 1]), m2 = fminf(v[i], v[i + 1]);
+        const float n1 = fmaxf(v[i + 2], v[i + 3]), n2 = fminf(v[i + 2], v[i + 3]);
+        m2 = fmaxf(fminf(m1, n1), fmaxf(m2, n2));
+        m1 = fmaxf(m1, n1);
+        if (w >= 2) two_best<dpp::QUAD_XOR1>(m1, m2);
+        if (w >= 4) two_best<dpp::QUAD_XOR2>(m1, m2);
+        if (w >= 8) two_best<dpp::ROW_HALF_MIRROR>(m1, m2);
+        if (w >= 16) two_best<dpp::ROW_MIRROR>(m1, m2);
+        const int e = expert_of<L>(i, j);
+        if (e < a.E && (j & (w - 1)) == 0) part[(e * per) >> 20] = a.best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
+      }
+    } else {
+      // Lane p of the wave, then p + 64 ..: group p % groups of token p / groups, by a scan.
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int e = expert_of<L>(i, j);
+        part[e + (e >> 5)] = v[i];
+      }
+      lds_turn();
+      float of[TOK];
+#pragma unroll
+      for (int q = 0; q < TOK; ++q) {
+        const int p = lane + 64 * q, s = p / a.groups, g = p - s * a.groups;
+        float m1 = -INFINITY, m2 = -INFINITY;
+        if (s < TOK) {
+          const float* from = &lds[wave][s][0];
+#pragma unroll 4
+          for (int c = 0; c < size; ++c) {
+            const int e = g * size + c;
+            const float x = from[e + (e >> 5)];
+            m2 = fmaxf(m2, fminf(m1, x));
+            m1 = fmaxf(m1, x);
+          }
+        }
+        of[q] = a.best > 1 && m2 > -INFINITY ? m1 + m2 : m1;
+      }
+      lds_turn();
+#pragma unroll
+      for (int q = 0; q < TOK; ++q) {
+        const int p = lane + 64 * q, s = p / a.groups;
+        if (s < TOK) lds[wave][s][p - s * a.groups] = of[q];
+      }
+    }
+    lds_turn();
+    // Every lane of a token ranks some of its groups.
+    taken = 0;
+    float in = INFINITY, out = -INFINITY;
+#pragma unroll 1
+    for (int g = j; g < a.groups; g += L) {
+      const float mine = part[g];
+      int rank = 0;
+#pragma unroll 8
+      for (int h = 0; h < a.groups; ++h) {
+        const float o = part[h];
+        rank += o > mine || (o == mine && h < g) ? 1 : 0;
+      }
+      if (rank < a.top_groups) {
+        taken |= 1ull << g;
+        in = fminf(in, mine);
+      } else {
+        out = fmaxf(out, mine);
+      }
+    }
+    in = -max_of<L>(-in);
+    out = max_of<L>(out);
+    // (both values are sums of two; nothing hangs on groups without experts)
+    if (out > -INFINITY && !(in - out > 2.f * near)) sure = false;
+    // every lane's bits together
+#pragma unroll
+    for (int d = 1; d < L; d <<= 1) taken |= __shfl_xor((unsigned long long)taken, d);
+  }
+  // ---- whole numbers, 1 and more
+  uint32_t key[N], tol = 0;
+  {
+    float low, unit;
+    if (a.bias) {
+      const float span = most + 2.f * b_most;  // (values lie in -b_most .. most + b_most)
+      low = -b_most;
+      unit = UNITS / span;
+      tol = (uint32_t)fminf(near * unit, 1.0e6f) + 4;  // (and the roundings on the way here)
+      if (!(span < INFINITY)) sure = false;
+    } else {
+      low = top - 16.f;  // (what lies below is told apart in 64 bits)
+      unit = UNITS / 16.f;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int e = expert_of<L>(i, j);
+      const float x = fmaf((a.bias ? v[i] : l[i]) - low, unit, 1.f);
+      const uint32_t n = (uint32_t)__builtin_amdgcn_fmed3f(x, 1.f, UNITS - 1.f);
+      key[i] = l[i] > -INFINITY ? (n << ID_BITS) | (ID_MASK - e) : 0u;
+    }
+  }
+  auto stay = [&](int i) -> uint32_t {  // all bits if entry i's group is taken
+    return 0u - (uint32_t)((taken >> ((expert_of<L>(i, j) * per) >> 20)) & 1);
+  };
+  if (groups && size % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint32_t m = stay(i);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) key[i + c] &= m;
+    }
+  } else if (groups) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] &= stay(i);
+  }
+  // ---- the rounds, one more than k for the border: every lane's words in order, the largest first one is taken
+  order_all<N>(key);
+  uint32_t mine = 0, last = 0;
+#pragma unroll 1
+  for (int r = 0; r <= a.k; ++r) {
+    const uint32_t best = max_of<L>(key[0]);
+    if (r > 0 && best && (last >> ID_BITS) - (best >> ID_BITS) <= tol) sure = false;
+    last = best;
+    if (j == r) mine = best;
+    const uint32_t out = key[0] == best ? ~0u : 0u;  // (by masks: a choice between two places becomes a search for the index)
+#pragma unroll
+    for (int i = 0; i + 1 < N; ++i) key[i] = (out & key[i + 1]) | (~out & key[i]);
+    key[N - 1] &= ~out;
+  }
+  int id = mine ? (int)(ID_MASK - (mine & ID_MASK)) : -1;
+  for (uint64_t again = __ballot(there && !sure && j == 0); __builtin_expect(again != 0, 0); again &= again - 1) {
+    const int first = __builtin_ctzll(again);  // of the token's lanes
+    const int exact = choose64<L * N / 64>(a, t0 + first / L, lane, lane_f32(top, first));
+    // (from lanes 0 .. k - 1 to the token's)
+    const int moved = __shfl(exact, j);
+    id = lane / L == first / L ? moved : id;
+  }
+  if (j >= a.k) id = -1;
+  const float at = id >= 0 ? a.logits[(size_t)t * a.E + id] : -INFINITY;
+  const float w = weight_of<L>(a, id >= 0, at, top, total);
+  if (there && j < a.k) {
+    a.ids[(size_t)t * a.k + j] = id;
+    a.w[(size_t)t * a.k + j] = id >= 0 ? a.scale * w : 0.f;
   }
 }
 
@@ -224,62 +471,117 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
 //   d log p_i = p_i (dw_i - sum_j p_j dw_j) scale, or p_i dw_i scale;   sigmoid: d l_i = d log p_i (1 - s_i);
 //   softmax: d l_e = sum of e's places, without renormalisation less s_e sum_j d log p_j.
 // An expert that occurs twice gets both places' parts.
-template <int NPL>
+template <int L, int N>
 __global__ __launch_bounds__(CHOOSE_THREADS) void choose_back_kernel(ChooseArgs a) {
-  const int lane = threadIdx.x & 63, t = blockIdx.x * (CHOOSE_THREADS / 64) + (threadIdx.x >> 6);
-  if (t >= a.T) return;
+  constexpr int TOK = 64 / L;
+  __shared__ __align__(16) float lds[CHOOSE_WAVES][TOK][L * N];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L, slot = lane / L;
+  const int t0 = (blockIdx.x * CHOOSE_WAVES + wave) * TOK;
+  if (t0 >= a.T) return;
+  const bool there = t0 + slot < a.T;
+  const int t = there ? t0 + slot : a.T - 1;
   const bool spread = !a.sigmoid && !a.renorm;  // every logit has a part
-  const size_t at = (size_t)t * a.k + lane;
-  int id = lane < a.k ? a.ids[at] : -1;
-  float dw = lane < a.k ? a.w[at] * a.scale : 0.f;
+  const size_t at = (size_t)t * a.k + j;
+  int id = j < a.k ? a.ids[at] : -1;
+  float dw = j < a.k ? a.w[at] * a.scale : 0.f;
   float l = (uint32_t)id < (uint32_t)a.E ? a.logits[(size_t)t * a.E + id] : -INFINITY;
   const bool chosen = l > -INFINITY;
   if (!chosen) { id = -1; dw = 0.f; }
-  float s[NPL], top = 0.f, total = 1.f, b_most;
+  float s[N], top = -INFINITY, total = 1.f;
   if (spread) {
-    float row[NPL], b[NPL];
-    top = load_logits<NPL>(a, t, lane, row, b, b_most);
-    scores<float, NPL>(a, row, s, total, top);
+    float row[N], b[N];
+    load_token<L, N>(a, t, j, row, b);
+#pragma unroll
+    for (int i = 0; i < N; ++i) top = fmaxf(top, row[i]);
+    top = max_of<L>(top);
+    scores<L, N>(a, row, top, s, total);
   }
-  const float p = weight_of(a, chosen, l, top, total);
-  float part = a.renorm ? p * (dw - wave_sum(p * dw)) : p * dw;
+  const float p = weight_of<L>(a, chosen, l, top, total);
+  float part = a.renorm ? p * (dw - group_sum<L>(p * dw)) : p * dw;
   if (a.sigmoid) part *= 1.0f / (1.0f + expf(l));
   if (!chosen) part = 0.f;
-  const float pull = spread ? wave_sum(part) : 0.f;
-  float out[NPL];
+  const float pull = spread ? group_sum<L>(part) : 0.f;
+  // The chosen experts' parts in LDS, each in its expert's place: one after the other, should an expert occur twice.
+  float* parts = &lds[wave][slot][0];
+  float out[N];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) out[i] = spread ? -s[i] * pull : 0.f;
-  for (int j = 0; j < a.k; ++j) {
-    const int e = __builtin_amdgcn_readlane(id, j);
-    const float v = lane_f32(part, j);
-#pragma unroll
-    for (int i = 0; i < NPL; ++i) out[i] += e == lane + 64 * i ? v : 0.f;
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(parts + expert_of<L>(i, j)) = make_float4(0.f, 0.f, 0.f, 0.f);
+  lds_turn();
+  if (chosen) parts[id] = __builtin_bit_cast(float, j);
+  lds_turn();
+  const bool twice = chosen && __builtin_bit_cast(int, parts[id]) != j;
+  lds_turn();
+  if (__ballot(twice) == 0) {
+    if (chosen) parts[id] = part;
+  } else {
+    if (chosen) parts[id] = 0.f;
+    lds_turn();
+    for (int r = 0; r < a.k; ++r) {
+      if (chosen && j == r) parts[id] += part;
+      lds_turn();
+    }
   }
+  lds_turn();
 #pragma unroll
-  for (int i = 0; i < NPL; ++i)
-    if (lane + 64 * i < a.E) a.dlogits[(size_t)t * a.E + lane + 64 * i] = out[i];
+  for (int i = 0; i < N; i += 4) {
+    const float4 u = *reinterpret_cast<const float4*>(parts + expert_of<L>(i, j));
+    out[i] = u.x; out[i + 1] = u.y; out[i + 2] = u.z; out[i + 3] = u.w;
+  }
+  if (spread) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = fmaf(-s[i], pull, out[i]);
+  }
+  if (!there) return;
+  float* row = a.dlogits + (size_t)t * a.E;
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const int e = expert_of<L>(i, j);
+    if (e + 4 <= a.E) {
+      *reinterpret_cast<f32x4_any*>(row + e) = f32x4_any{out[i], out[i + 1], out[i + 2], out[i + 3]};
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (e + c < a.E) row[e + c] = out[i + c];
+    }
+  }
 }
 
+// f(lanes of a token, experts of a lane)
 template <typename F>
-void by_width(int E, F&& f) {
-  if (E <= 64) f(std::integral_constant<int, 1>{});
-  else if (E <= 128) f(std::integral_constant<int, 2>{});
-  else if (E <= 256) f(std::integral_constant<int, 4>{});
-  else if (E <= 512) f(std::integral_constant<int, 8>{});
-  else f(std::integral_constant<int, 16>{});
+void by_width(const ChooseArgs& a, F&& f) {
+  using std::integral_constant;
+  auto wave = [&](auto n) { f(integral_constant<int, 64>{}, n); };
+  auto rows = [&](auto n) { f(integral_constant<int, 16>{}, n); };
+  if (a.E <= 256 && a.k <= 16) {
+    if (a.E <= 64) rows(integral_constant<int, 4>{});
+    else if (a.E <= 128) rows(integral_constant<int, 8>{});
+    else rows(integral_constant<int, 16>{});
+  } else if (a.E <= 256) {
+    wave(integral_constant<int, 4>{});
+  } else if (a.E <= 512) {
+    wave(integral_constant<int, 8>{});
+  } else {
+    wave(integral_constant<int, 16>{});
+  }
+}
+unsigned choose_grid(const ChooseArgs& a, int lanes) {
+  const int tokens = CHOOSE_WAVES * (64 / lanes);
+  return (unsigned)((a.T + tokens - 1) / tokens);
 }
 
 }  // namespace
 
 hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)((a.T + CHOOSE_THREADS / 64 - 1) / (CHOOSE_THREADS / 64));
-  by_width(a.E, [&](auto n) { choose_kernel<decltype(n)::value><<<grid, CHOOSE_THREADS, 0, st>>>(a); });
+  by_width(a, [&](auto l, auto n) {
+    choose_kernel<decltype(l)::value, decltype(n)::value><<<choose_grid(a, decltype(l)::value), CHOOSE_THREADS, 0, st>>>(a);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_choose_back(const ChooseArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)((a.T + CHOOSE_THREADS / 64 - 1) / (CHOOSE_THREADS / 64));
-  by_width(a.E, [&](auto n) { choose_back_kernel<decltype(n)::value><<<grid, CHOOSE_THREADS, 0, st>>>(a); });
+  by_width(a, [&](auto l, auto n) {
+    choose_back_kernel<decltype(l)::value, decltype(n)::value><<<choose_grid(a, decltype(l)::value), CHOOSE_THREADS, 0, st>>>(a);
+  });
   return hipGetLastError();
 }
 
