@@ -75,6 +75,43 @@ __device__ __forceinline__ void load8(const void* p, size_t i, int dtype, int n,
     for (int j = 0; j < 8; ++j) v[j] = j < n ? load_as_f32(p, i + j, dtype) : 0.f;
   }
 }
+// The same in two steps, loads now and values later: the bits of eight values as they lie in memory.
+template <int DTYPE>
+struct Bits8 {
+  uint32_t w[DTYPE == MOE_VQ_BF16 ? 4 : 8];
+};
+template <int DTYPE, bool STREAM = false>
+__device__ __forceinline__ void load_bits8(const void* p, size_t i, int n, Bits8<DTYPE>& b) {
+  if constexpr (DTYPE == MOE_VQ_BF16) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + i;
+    if (n >= 8) {
+      const u32x4_any u = load_vec<STREAM>(reinterpret_cast<const u32x4_any*>(q));
+      b.w[0] = u.x; b.w[1] = u.y; b.w[2] = u.z; b.w[3] = u.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        b.w[j] = (2 * j < n ? q[2 * j] : 0u) | (2 * j + 1 < n ? (uint32_t)q[2 * j + 1] << 16 : 0u);
+    }
+  } else {
+    const uint32_t* q = static_cast<const uint32_t*>(p) + i;
+    if (n >= 8) {
+#pragma unroll
+      for (int j = 0; j < 8; j += 4) {
+        const u32x4_any u = load_vec<STREAM>(reinterpret_cast<const u32x4_any*>(q + j));
+        b.w[j] = u.x; b.w[j + 1] = u.y; b.w[j + 2] = u.z; b.w[j + 3] = u.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) b.w[j] = j < n ? q[j] : 0u;
+    }
+  }
+}
+template <int DTYPE>
+__device__ __forceinline__ float value_of(const Bits8<DTYPE>& b, int j) {
+  if constexpr (DTYPE == MOE_VQ_BF16) return j & 1 ? __builtin_bit_cast(float, b.w[j >> 1] & 0xFFFF0000u) : bf16_bits_to_f32(b.w[j >> 1] & 0xFFFFu);
+  else return __builtin_bit_cast(float, b.w[j]);
+}
+
 // STREAM: nontemporal stores, which leave the L2 to the operands that other tiles share.
 template <bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, size_t i, int dtype, int n, const float* v) {

@@ -738,7 +738,10 @@ __device__ __forceinline__ void dz_values(const DzArgs& a, const float* dy, cons
 // overlapping; rows of 1024 bytes, streamed loads or stores and half or twice the workgroups change
 // nothing or cost 2 to 3 us).  dz is rounded to the element type for the matrix products; the column
 // sums add the unrounded values in fp32, rows in a fixed order.
-template <int DTYPE, int DY_DTYPE, int ACT, bool Z8>
+// Z: as it is, or in 8 bits, with the up values' places at multiples of 8 or anywhere.
+enum DzSource { Z_PLAIN, Z_BITS8, Z_BITS8_ANY };
+
+template <int DTYPE, int DY_DTYPE, int ACT, int Z>
 __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   __shared__ float red[DZ_TY][2][DZ_TX * 8];
   const int tx = threadIdx.x % DZ_TX, ty = threadIdx.x / DZ_TX;
@@ -773,13 +776,8 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
   };
   const size_t pitch8 = rows8_pitch(a.R);
   auto load_z = [&](size_t r, int c, float* v) {  // eight columns of z from column c
-    if constexpr (Z8) {
-      const uint8_t *q = a.z8.q + r * pitch8, *e = a.z8.e + r * (pitch8 / 32);
-      if (a.N % 8 == 0) load8_q<true>(q, e, c, left, v);
-      else load8_q<false>(q, e, c, left, v);
-    } else {
-      load8(a.z, r * a.R + c, DTYPE, left, v);
-    }
+    if constexpr (Z != Z_PLAIN) load8_q<Z == Z_BITS8>(a.z8.q + r * pitch8, a.z8.e + r * (pitch8 / 32), c, left, v);
+    else load8(a.z, r * a.R + c, DTYPE, left, v);
   };
   if (n < a.N) {
     for (int m = m0 + ty; m < m1; m += 2 * DZ_TY) {
@@ -929,10 +927,11 @@ void dz_go(const LinearPlan& p, const DzArgs& d, int act, hipStream_t st) {
   const dim3 grid(div_up(p.N, DZ_TX * 8), p.G, d.splits);
   auto go = [&](auto a) {
     constexpr int ACT = decltype(a)::value;
-    if (d.z8.q) dz_kernel<DTYPE, DY_DTYPE, ACT, true><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
-    else dz_kernel<DTYPE, DY_DTYPE, ACT, false><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+    if (d.z8.q && p.N % 8 == 0) dz_kernel<DTYPE, DY_DTYPE, ACT, Z_BITS8><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+    else if (d.z8.q) dz_kernel<DTYPE, DY_DTYPE, ACT, Z_BITS8_ANY><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+    else dz_kernel<DTYPE, DY_DTYPE, ACT, Z_PLAIN><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
   };
-  if (act == MOE_VQ_ACT_NONE) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_NONE, false><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
+  if (act == MOE_VQ_ACT_NONE) dz_kernel<DTYPE, DY_DTYPE, MOE_VQ_ACT_NONE, Z_PLAIN><<<grid, DZ_TX * DZ_TY, 0, st>>>(d);
   else if (act == MOE_VQ_ACT_SILU) go(std::integral_constant<int, MOE_VQ_ACT_SILU>{});
   else if (act == MOE_VQ_ACT_GELU) go(std::integral_constant<int, MOE_VQ_ACT_GELU>{});
   else go(std::integral_constant<int, MOE_VQ_ACT_SWIGLU>{});

@@ -92,74 +92,91 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void norm_kernel(NormArgs a) {
   }
 }
 
-// Both sums of a row at once, then its gradient; a workgroup walks rows and adds up its part of dg in
-// registers.
+// Both sums of a row at once, then its gradient; a workgroup walks rows and adds up its part of dg in registers.  The
+// next row's loads go out before this one's sums.
 template <int DYT, int ST, int DXT, int NCH, int LPR>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void norm_back_kernel(NormBackArgs a) {
   constexpr int RP = LPR ? 256 / LPR : 1;  // rows of a workgroup at a time
   __shared__ float red[2][16][2];
   __shared__ float meet[LPR ? 256 * V : 1];
   const int width = LPR ? LPR : blockDim.x, tx = LPR ? threadIdx.x % LPR : threadIdx.x;
+  struct Row {
+    Bits8<ST> s[NCH];
+    Bits8<DYT> dy[NCH], dy2[NCH];
+    Bits8<DXT> ds[NCH];
+  } row[2];
+  const int mine = LPR ? threadIdx.x / (LPR ? LPR : 1) : 0;
+  auto load = [&](Row& to, int r0) {
+    const int r = r0 + mine < a.M ? r0 + mine : a.M - 1;
+    const size_t at = (size_t)r * a.C;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (i * width + tx) * V, left = c < a.C ? a.C - c : 0;
+      load_bits8<ST>(a.s, at + c, left, to.s[i]);
+      load_bits8<DYT>(a.dy, at + c, left, to.dy[i]);
+      if (a.dy2) load_bits8<DYT>(a.dy2, at + c, left, to.dy2[i]);
+      if (a.ds) load_bits8<DXT>(a.ds, at + c, left, to.ds[i]);
+    }
+  };
+  constexpr bool AHEAD = NCH == 1;  // (two chunks of two rows, or of a row and the gain, would not fit the registers)
   float g[NCH][V], acc[NCH][V];
+  auto load_gain = [&](int i) {
+    const int c = (i * width + tx) * V;
+    load8(a.gain, c, MOE_VQ_F32, c < a.C ? a.C - c : 0, g[i]);
+  };
 #pragma unroll
   for (int i = 0; i < NCH; ++i) {
-    const int c = (i * width + tx) * V;
+    if (AHEAD) load_gain(i);
 #pragma unroll
-    for (int j = 0; j < V; ++j) g[i][j] = acc[i][j] = 0.f;
-    if (c < a.C) load8(a.gain, c, MOE_VQ_F32, a.C - c, g[i]);
+    for (int j = 0; j < V; ++j) acc[i][j] = 0.f;
   }
-  int turn = 0;
-  for (int r0 = blockIdx.x * RP; r0 < a.M; r0 += gridDim.x * RP, turn ^= 1) {
-    int row = r0 + (LPR ? threadIdx.x / (LPR ? LPR : 1) : 0);
-    const bool there = row < a.M;
-    if (!there) row = a.M - 1;
-    const size_t at = (size_t)row * a.C;
-    float s[NCH][V], d[NCH][V], sum[2] = {0.f, 0.f};
+  const int step = gridDim.x * RP;
+  auto turn = [&](Row& now, Row& then, float (*part)[2], int r0) {
+    if (!AHEAD) load(now, r0);
+    else if (r0 + step < a.M) load(then, r0 + step);
+    const bool there = r0 + mine < a.M;
+    const size_t at = (size_t)(there ? r0 + mine : a.M - 1) * a.C;
+    float sum[2] = {0.f, 0.f};
+    auto dy_of = [&](int i, int j) { return a.dy2 ? value_of(now.dy[i], j) + value_of(now.dy2[i], j) : value_of(now.dy[i], j); };
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (i * width + tx) * V, left = a.C - c;
-#pragma unroll
-      for (int j = 0; j < V; ++j) s[i][j] = d[i][j] = 0.f;
-      if (c < a.C) {
-        load8(a.s, at + c, ST, left, s[i]);
-        load8(a.dy, at + c, DYT, left, d[i]);
-        if (a.dy2) {
-          float t[V];
-          load8(a.dy2, at + c, DYT, left, t);
-#pragma unroll
-          for (int j = 0; j < V; ++j) d[i][j] += t[j];
-        }
-      }
+      if (!AHEAD) load_gain(i);
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        sum[0] = fmaf(s[i][j], s[i][j], sum[0]);
-        sum[1] = fmaf(d[i][j] * g[i][j], s[i][j], sum[1]);
+        const float s = value_of(now.s[i], j);
+        sum[0] = fmaf(s, s, sum[0]);
+        sum[1] = fmaf(dy_of(i, j) * g[i][j], s, sum[1]);
       }
     }
-    // (two turns' sums lie apart: a wave may be a row ahead)
-    row_sums<LPR, 2>(sum, red[turn]);
+    row_sums<LPR, 2>(sum, part);
     const float rho = 1.0f / sqrtf(sum[0] / (float)a.C + a.eps);
     const float pull = rho * rho * (sum[1] / (float)a.C);
+    if (!there) return;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (i * width + tx) * V, left = a.C - c;
-      if (there) {
+      if (!AHEAD) load_gain(i);
+      float o[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[i][j] = fmaf(d[i][j], s[i][j] * rho, acc[i][j]);
+      for (int j = 0; j < V; ++j) {
+        const float s = value_of(now.s[i], j), d = dy_of(i, j);
+        acc[i][j] = fmaf(d, s * rho, acc[i][j]);
+        o[j] = rho * (d * g[i][j] - s * pull);
+        if (a.ds) o[j] += value_of(now.ds[i], j);
       }
-      if (a.dx && there && c < a.C) {
-        float o[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) o[j] = rho * (d[i][j] * g[i][j] - s[i][j] * pull);
-        if (a.ds) {
-          float t[V];
-          load8(a.ds, at + c, DXT, left, t);
-#pragma unroll
-          for (int j = 0; j < V; ++j) o[j] += t[j];
-        }
-        store8(a.dx, at + c, DXT, left, o);
-      }
+      if (a.dx && c < a.C) store8(a.dx, at + c, DXT, left, o);
     }
+  };
+  // (two turns' sums lie apart: a wave may be a row ahead)
+  int r0 = blockIdx.x * RP;
+  if constexpr (AHEAD) {
+    if (r0 < a.M) load(row[0], r0);
+    for (; r0 < a.M; r0 += 2 * step) {
+      turn(row[0], row[1], red[0], r0);
+      if (r0 + step < a.M) turn(row[1], row[0], red[1], r0 + step);
+    }
+  } else {
+    for (int k = 0; r0 < a.M; r0 += step, k ^= 1) turn(row[0], row[0], red[k], r0);
   }
   if (!a.dgain) return;
   if constexpr (LPR > 0) {
@@ -249,10 +266,12 @@ hipError_t launch_norm(const NormArgs& a, int dtype, int s_dtype, int y_dtype, h
   return hipGetLastError();
 }
 
-// Enough workgroups to fill the device.
+// As many workgroups as make 16 waves of a CU, whose loads run a row ahead (4096 x 7168 in bf16, all five tensors: 59 us
+// by one workgroup of 14; two that wait for each row's loads 72).
 int norm_back_blocks(int M, int C) {
   const NormShape s = norm_shape(C);
-  const int rows = s.lpr ? 256 / s.lpr : 1, need = (M + rows - 1) / rows, most = s.lpr ? 1024 : 512;
+  const int rows = s.lpr ? 256 / s.lpr : 1, need = (M + rows - 1) / rows, waves = s.threads / 64;
+  const int most = 256 * (waves < 16 ? 16 / waves : 1);
   return need < most ? need : most;
 }
 
