@@ -6,12 +6,12 @@ the gradients are calls of their own, and calls of one object that may overlap n
 """
 from __future__ import annotations
 
-from typing import Optional, Tuple
+from typing import Optional, Tuple, Union
 
 import torch
 
 from . import _lib
-from .dense import Rows8, _device, _need, _OnDevice
+from .dense import DenseExperts, Linear, Rows8, _device, _need, _OnDevice
 from .layer import x_dtype_code
 
 SCORES = {"softmax": _lib.SCORE_SOFTMAX, "sigmoid": _lib.SCORE_SIGMOID}
@@ -70,12 +70,13 @@ class RmsNorm(_OnDevice):
         sp = _need(s, "s", (M, C), s.dtype, self.device)
         g = _need(dy, "dy", (M, C), dy.dtype, self.device)
         g2 = _need(dy2, "dy2", (M, C), dy.dtype, self.device) if dy2 is not None else 0
-        kind = dx.dtype if dx is not None else ds.dtype if ds is not None else s.dtype
+        like = dx if dx is not None else ds if ds is not None else s
+        kind = like.dtype
         d = _need(ds, "ds", (M, C), kind, self.device) if ds is not None else 0
         xd = _need(dx, "dx", (M, C), kind, self.device) if dx is not None else 0
         gd = _need(dgain, "dgain", (C,), torch.float32, self.device) if dgain is not None else 0
         self._call(_lib.norm_backward, sp, x_dtype_code(s), M, C, self._gain(), self.eps, g, g2, x_dtype_code(dy), d, xd,
-                   _lib.BF16 if kind == torch.bfloat16 else _lib.F32, gd, 0 if self.ws is None else self.ws.data_ptr(), self.ws_bytes)
+                   x_dtype_code(like), gd, 0 if self.ws is None else self.ws.data_ptr(), self.ws_bytes)
 
 
 class ExpertChoice(_OnDevice):
@@ -129,3 +130,109 @@ class ExpertChoice(_OnDevice):
         o = _need(dlogits, "dlogits", (T, self.n_experts), torch.float32, self.device)
         self._call(_lib.choose_backward, self._choice(), p, T, i, d, o)
         return dlogits
+
+
+class Router(_OnDevice):
+    """The router's product and the choice of experts: logits = x w^T (w [E, H], bf16 or fp32; the logits are fp32), then
+    ExpertChoice with the further arguments.  backward: make what the gradients need, from x as it is or in 8 bits."""
+
+    def __init__(self, w: torch.Tensor, top_k: int, max_tokens: int, backward: bool = False, **choice):
+        super().__init__(_device(w.device))
+        E = w.shape[0]
+        self.linear = Linear(w, max_rows=max_tokens, backward=backward, kept8=backward)
+        self.choice = ExpertChoice(E, top_k, device=w.device, **choice)
+        self.logits = self._new((max_tokens, E), torch.float32)
+        self.ids = self._new((max_tokens, top_k), torch.int32)
+        self.w = self._new((max_tokens, top_k), torch.float32)
+        self.dlogits = self._new((max_tokens, E), torch.float32) if backward else None
+        self.n_tokens = None  # of the last forward
+
+    def _here(self) -> None:
+        """The buffers are in use by the current stream, through this object's parts."""
+        self._call(lambda stream: None)
+
+    def forward(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+        """x [T, H] -> ids [T, k] (int32) and w [T, k] (fp32), valid until the next forward."""
+        T = x.shape[0]
+        self.n_tokens = None
+        self._here()
+        if T > self.linear.max_rows:
+            raise ValueError(f"{T} tokens, made for {self.linear.max_rows}")
+        self.linear.forward(x, out=self.logits[:T])
+        ids, w = self.choice.forward(self.logits[:T], self.ids[:T], self.w[:T])
+        self.n_tokens = T
+        return ids, w
+
+    def backward(self, x: Union[torch.Tensor, Rows8, None], dw: torch.Tensor, dx: Optional[torch.Tensor] = None,
+                 dweight: Optional[torch.Tensor] = None) -> None:
+        """Gradients of the last forward from dw [T, k]: those of dx [T, H] and dweight (as w) that are given are
+        written.  x as it was, or in 8 bits; None without dweight."""
+        if self.dlogits is None:
+            raise ValueError("made without backward")
+        if self.n_tokens is None:
+            raise ValueError("no forward to go back through")
+        T = self.n_tokens
+        self._here()
+        dlogits = self.choice.backward(self.logits[:T], self.ids[:T], dw, self.dlogits[:T])
+        self.linear.backward(x, dlogits, dx=dx, dw=dweight)
+
+
+class MoeBlock(_OnDevice):
+    """A layer's mixture of experts with the norm before it: s = x + residual, n = norm(s), ids and w = router(n), y =
+    sum_i w_i E_i(n).  The next block adds y to s.  After a forward with keep=True, backward gives the gradients; what it
+    needs beside s is kept here, by experts made with kept8 in 8 bits, which the norm then writes.  work: another block of
+    the same sizes whose buffers this one uses (see DenseExperts; both of experts with kept8)."""
+
+    def __init__(self, norm: RmsNorm, router: Router, experts: DenseExperts, work: Optional["MoeBlock"] = None):
+        super().__init__(norm.device)
+        T, H, k = experts.rows.max_tokens, norm.n_cols, experts.rows.top_k
+        w1 = experts.fc1.w
+        if router.linear.n_in != H or w1.shape[-1] != H or router.linear.dtype != w1.dtype:
+            raise ValueError("norm, router and experts must be of one hidden size, router and experts of one type")
+        if router.choice.top_k != k or router.choice.n_experts != experts.rows.n_experts:
+            raise ValueError("router and experts must be of one number of experts and top_k")
+        if norm.max_rows < T or router.linear.max_rows < T or {norm.device, router.device, experts.rows.device} != {self.device}:
+            raise ValueError("norm and router must be made for as many tokens as the experts, on their device")
+        if work is not None and not (experts.kept8 and work.experts.kept8 and work.experts.sizes == experts.sizes):
+            raise ValueError("work must be a block of the same sizes, both of experts with kept8")
+        self.norm, self.router, self.experts = norm, router, experts
+        back = experts.z is not None
+
+        def new(name, shape, dtype):
+            return self._new(shape, dtype) if work is None else self._share(getattr(work, name))
+
+        self.n = new("n", (T, H), w1.dtype)
+        self.dn, self.dn2 = (new("dn", (T, H), w1.dtype), new("dn2", (T, H), w1.dtype)) if back else (None, None)
+        self.dw = new("dw", (T, k), torch.float32) if back else None
+        self._kept = None
+
+    def forward(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, s: Optional[torch.Tensor] = None,
+                y: Optional[torch.Tensor] = None, keep: bool = False) -> torch.Tensor:
+        """x [T, H] (and residual [T, H], added to it) -> y [T, H], fp32 unless given.  s receives the sum, which
+        backward takes."""
+        T = x.shape[0]
+        self._kept = None
+        if T > self.experts.rows.max_tokens:
+            raise ValueError(f"{T} tokens, made for {self.experts.rows.max_tokens}")
+        if keep and self.dn is None:
+            raise ValueError("made without backward")
+        self._call(lambda stream: None)
+        kept8 = keep and self.experts.kept8
+        self.norm.forward(x, residual, s, self.n[:T], self.experts.x8 if kept8 else None)
+        ids, w = self.router.forward(self.n[:T])
+        y = self.experts.forward(self.n[:T], ids, w, y, keep=keep, x8_there=kept8)
+        if keep:
+            self._kept = T
+        return y
+
+    def backward(self, s: torch.Tensor, dy: torch.Tensor, ds: Optional[torch.Tensor], dx: torch.Tensor, dgain: torch.Tensor,
+                 drouter: torch.Tensor, dw1: torch.Tensor, dw2: torch.Tensor) -> None:
+        """Gradients of the last forward(keep=True) from dy [T, H] and ds [T, H], the gradient of s (None: y is all that
+        is used): dx [T, H] (of x and of residual alike; it may be ds), dgain, drouter, dw1 and dw2."""
+        if self._kept is None:
+            raise ValueError("the last forward kept nothing")
+        T, self._kept = self._kept, None
+        self._call(lambda stream: None)
+        self.experts.backward(dy, self.dn[:T], self.dw[:T], dw1, dw2)
+        self.router.backward(self.experts.x8 if self.experts.kept8 else self.n[:T], self.dw[:T], self.dn2[:T], drouter)
+        self.norm.backward(s, self.dn[:T], self.dn2[:T], ds, dx, dgain)

@@ -1,6 +1,6 @@
 """Unquantised experts on top of the C ABI: the routed pairs sorted by expert and back, the
 dense product with bias, activation and residual (one matrix, or one per expert over the
-sorted rows), and their gradients.  The gradients are calls of their own: nothing here records a graph
+sorted rows), and their gradients, which may read rows that were kept in 8 bits.  The gradients are calls of their own: nothing here records a graph
 for autograd, and outputs carry none even if an input requires a gradient.
 
 As in layer.py, PyTorch provides device memory and the stream; every step of the
@@ -49,6 +49,12 @@ class _OnDevice:
         """A buffer of the object, in use by the streams of its calls."""
         t = torch.empty(shape, dtype=dtype, device=self.device)
         self._buffers.append(t)
+        return t
+
+    def _share(self, t: torch.Tensor) -> torch.Tensor:
+        """A buffer that another object has made."""
+        self._buffers.append(t)
+        self._streams.clear()  # (whatever this object's streams know, they may not know of this one)
         return t
 
     def _call(self, fn, *args) -> None:
@@ -145,8 +151,8 @@ class ExpertRows(_OnDevice):
         return self.expert_start
 
     def gather(self, x: Union[torch.Tensor, Rows8], out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """x [T, C] -> rows [T*k, C] in the order of the experts (rows of dropped pairs as they were).  From x in
-        8 bits the rows are the values that it stands for, in bf16 or fp32 (as out)."""
+        """x [T, C] -> rows [T*k, C] in the order of the experts (rows of dropped pairs as they were), bf16 or fp32 (as
+        out; by default as x).  From x in 8 bits the rows are the values that it stands for (by default in bf16)."""
         T, k = self.n_tokens, self.top_k
         if isinstance(x, Rows8):
             C = x.n_cols
@@ -157,7 +163,11 @@ class ExpertRows(_OnDevice):
         C = x.shape[-1]
         p = _need(x, "x", (T, C), x.dtype, self.device)
         out = torch.empty((T * k, C), dtype=x.dtype, device=self.device) if out is None else out
-        o = _need(out, "out", (T * k, C), x.dtype, self.device)
+        o = _need(out, "out", (T * k, C), out.dtype, self.device)
+        if out.dtype != x.dtype:  # (what combine's gradient does for weights of 1)
+            self._call(_lib.combine_rows_backward, p, x_dtype_code(x), T, k, C, self.pair_row.data_ptr(), 0, 0, x_dtype_code(out),
+                       o, 0)
+            return out
         self._call(_lib.gather_rows, p, x_dtype_code(x), T, k, C, self.pair_row.data_ptr(), o)
         return out
 
@@ -220,24 +230,25 @@ class ExpertRows(_OnDevice):
         g = _need(dy, "dy", (T * k, N), dy.dtype, self.device)
         zp = z.desc("z", T * k, R, self.device)
         wp = _need(w, "w", (T, k), torch.float32, self.device) if w is not None else 0
-        like = dz if dz is not None else y
-        kind = dy.dtype if like is None else like.dtype
-        dzp = _need(dz, "dz", (T * k, R), kind, self.device) if dz is not None else 0
-        yp = _need(y, "y", (T * k, N), kind, self.device) if y is not None else 0
+        like = dz if dz is not None else y if y is not None else dy
+        dzp = _need(dz, "dz", (T * k, R), like.dtype, self.device) if dz is not None else 0
+        yp = _need(y, "y", (T * k, N), like.dtype, self.device) if y is not None else 0
         dp = _need(dw, "dw", (T, k), torch.float32, self.device) if dw is not None else 0
         self._call(_lib.act_backward8, zp, ACTS[act], float(swiglu_limit), T, k, N, self.pair_row.data_ptr(), wp, g,
-                   x_dtype_code(dy), dzp, yp, _lib.BF16 if kind == torch.bfloat16 else _lib.F32, dp)
+                   x_dtype_code(dy), dzp, yp, x_dtype_code(like), dp)
 
 
 class Linear(_OnDevice):
     """y = act(x W^T + b) + residual for up to max_rows rows.  w: [R, n_in], or [G, R, n_in] for one
     matrix per group of rows; bf16 or fp32.  R is n_out, or 2 n_out for act "swiglu" (gate rows, then
     up rows; swiglu_limit: its clamp, 0 none).  bias: fp32 [R] or [G, R].  backward: make the
-    workspace of the gradients too; kept8: and that of gradients from Rows8.  Each call reads w and bias where they are at that time (a
+    workspace of the gradients too; kept8: and that of gradients from Rows8; work: use the workspace of this Linear, of no
+    smaller a need, whose calls must not overlap this one's.  Each call reads w and bias where they are at that time (a
     captured graph where they were when it was captured)."""
 
     def __init__(self, w: torch.Tensor, bias: Optional[torch.Tensor] = None, act: str = "none",
-                 swiglu_limit: float = 0.0, max_rows: int = 1, backward: bool = False, kept8: bool = False):
+                 swiglu_limit: float = 0.0, max_rows: int = 1, backward: bool = False, kept8: bool = False,
+                 work: Optional["Linear"] = None):
         super().__init__(_device(w.device))
         if act not in ACTS:
             raise ValueError(f"act must be one of {', '.join(ACTS)}")
@@ -257,8 +268,13 @@ class Linear(_OnDevice):
             need.append(_lib.linear_bytes8(self.c, max_rows))
         if 0 in need:
             raise ValueError("invalid sizes")
-        self.ws_bytes = max(need)
-        self.ws = self._new(self.ws_bytes, torch.uint8)
+        if work is not None:
+            if work.device != self.device or work.ws_bytes < max(need):
+                raise ValueError("work has another device or a smaller workspace")
+            self.ws_bytes, self.ws = work.ws_bytes, self._share(work.ws)
+        else:
+            self.ws_bytes = max(need)
+            self.ws = self._new(self.ws_bytes, torch.uint8)
 
     def _weights(self) -> _lib.LinearDesc:
         """The description of the product, with the present addresses of w and bias."""
@@ -328,36 +344,70 @@ class DenseExperts:
     of the pass is kept here: x, ids and w may change in between (w1 and w2 may not).
 
     With bf16 experts h, z and the gradients between the products are held in bf16, which the matrix
-    instructions take; an expert's output o is held in fp32 until the weighted sum."""
+    instructions take; an expert's output o is held in fp32 until the weighted sum.
+
+    kept8: what is kept is the tokens x and the values z before the activation, in 8 bits (x8, z8), and the routing; h is
+    made from z again, and the routing weights' gradient from h, so that nothing else of the pass has to stay (at 8
+    experts a token some 5 KB a pair for hidden 7168, inner 2048 in bf16, instead of 55).  All other buffers are free
+    between a pass's calls: a layer made with work, another one of the same sizes, uses that one's, and their calls
+    must not overlap."""
+
+    kept8 = False
 
     def __init__(self, w1: torch.Tensor, w2: torch.Tensor, top_k: int, max_tokens: int, swiglu_limit: float = 0.0,
-                 backward: bool = False):
+                 backward: bool = False, kept8: bool = False, work: Optional["DenseExperts"] = None):
         E, R, H = w1.shape
         if tuple(w2.shape) != (E, H, R // 2) or w2.dtype != w1.dtype or w2.device != w1.device:
             raise ValueError("w1 must be [E, 2I, H] and w2 [E, H, I], of one type and device")
+        if kept8 and not backward:
+            raise ValueError("kept8 without backward")
+        if kept8 and R > 16384:
+            raise ValueError("kept8 takes an inner size of up to 8192")
+        sizes = (E, R, H, top_k, max_tokens, w1.dtype, w1.device)
+        if work is not None and not (kept8 and work.kept8 and work.sizes == sizes):
+            raise ValueError("work must be a step of the same sizes, both made with kept8")
         P = max_tokens * top_k
-        self.fc1 = Linear(w1, act="swiglu", swiglu_limit=swiglu_limit, max_rows=P, backward=backward)
-        self.fc2 = Linear(w2, max_rows=P, backward=backward)
+        self.kept8, self.sizes, self.swiglu_limit = kept8, sizes, float(swiglu_limit)
+        of = (lambda name: getattr(work, name)) if work is not None else (lambda name: None)
+        self.fc1 = Linear(w1, act="swiglu", swiglu_limit=swiglu_limit, max_rows=P, backward=backward and not kept8, work=of("fc1"))
+        self.fc2 = Linear(w2, max_rows=P, backward=backward, work=of("fc2"))
+        # (from dz on, the way back through the first product is that of one without an activation)
+        self.fc1_back = Linear(w1, max_rows=P, backward=True, work=of("fc1_back")) if kept8 else None
         self.rows = ExpertRows(E, top_k, max_tokens, device=w1.device)
+
         # (buffers of rows: each pass of the step calls it, on the pass's stream)
-        new = lambda *shape: self.rows._new(shape, w1.dtype)  # noqa: E731
-        self.xs, self.h, self.o = new(P, H), new(P, R // 2), self.rows._new((P, H), torch.float32)
-        self.z, self.dh, self.do = (new(P, R), new(P, R // 2), new(P, H)) if backward else (None, None, None)
-        self.w_kept = self.rows._new((max_tokens, top_k), torch.float32) if backward else None
+        def new(name, dtype, *shape):
+            return self.rows._new(shape, dtype) if work is None else self.rows._share(getattr(work, name))
+
+        self.xs, self.h = new("xs", w1.dtype, P, H), new("h", w1.dtype, P, R // 2)
+        self.o = new("o", torch.float32, P, H)
+        self.z = self.dh = self.do = self.w_kept = self.x8 = self.z8 = None
+        if backward:
+            self.z, self.dh, self.do = new("z", w1.dtype, P, R), new("dh", w1.dtype, P, R // 2), new("do", w1.dtype, P, H)
+            self.w_kept = self.rows._new((max_tokens, top_k), torch.float32)
+        if kept8:
+            self.x8, self.z8 = Rows8(max_tokens, H, device=w1.device), Rows8(P, R, device=w1.device)
         self._kept = None
 
     def forward(self, x: torch.Tensor, ids: torch.Tensor, w: torch.Tensor, y: Optional[torch.Tensor] = None,
-                add: bool = False, keep: bool = False) -> torch.Tensor:
-        """x [T, H], ids and w [T, k] -> y [T, H] (fp32 unless given)."""
+                add: bool = False, keep: bool = False, x8_there: bool = False) -> torch.Tensor:
+        """x [T, H], ids and w [T, k] -> y [T, H] (fp32 unless given).  x8_there: x8 holds x in 8 bits already
+        (RmsNorm.forward's rows8)."""
         if keep and self.z is None:
             raise ValueError("made without backward")
         if add and y is None:
             raise ValueError("add needs y")
+        if x8_there and not (keep and self.kept8):
+            raise ValueError("x8_there without keep, or made without kept8")
         self._kept = None  # (from here on the buffers are another pass's, even if a call below is refused)
         P = x.shape[0] * self.rows.top_k
         start = self.rows.sort(ids)
         self.rows.gather(x, self.xs[:P])
         self.fc1.forward(self.xs[:P], start, out=self.h[:P], z=self.z[:P] if keep else None)
+        if keep and self.kept8:
+            if not x8_there:
+                self.x8.pack(x)
+            self.z8.pack(self.z[:P], start)
         self.fc2.forward(self.h[:P], start, out=self.o[:P])
         out = self.rows.combine(self.o[:P], w, y if add else None, y)
         if keep:
@@ -373,6 +423,16 @@ class DenseExperts:
         self._kept = None
         P = x.shape[0] * self.rows.top_k
         start = self.rows.expert_start
+        if self.kept8:
+            self.rows.gather(dy, self.do[:P])
+            self.fc2.backward(None, self.do[:P], group_start=start, dx=self.dh[:P])
+            # (dh before the weights: z takes w dh act'(z), h w act(z))
+            self.rows.act_backward(self.z8, self.dh[:P], w, "swiglu", self.swiglu_limit, self.z[:P], self.h[:P], dw)
+            self.fc2.backward(self.h[:P], self.do[:P], group_start=start, dw=dw2)
+            self.rows.gather(self.x8, self.xs[:P])
+            self.fc1_back.backward(self.xs[:P], self.z[:P], group_start=start, dx=self.do[:P], dw=dw1)
+            self.rows.gather_backward(self.do[:P], dx)
+            return
         self.rows.combine_backward(dy, w, self.o[:P], self.do[:P], dw)
         self.fc2.backward(self.h[:P], self.do[:P], group_start=start, dx=self.dh[:P], dw=dw2)
         # (do has been read: it takes the gradient of the gathered rows)

@@ -196,3 +196,57 @@ def act_backward64(z, dy, pair_row, w, act, lim, dtype):
         dw[pairs] = (d * h).sum(1)
         bw[pairs] = (d.abs() * eh).sum(1) + (N // 64 + 24) * U * (d * h).abs().sum(1)
     return {"dz": (dz, bz), "y": (y, by), "dw": (dw, bw)}, rows
+
+
+def experts_backward8_64(x, z, dy, pair_row, start, w, w1, w2, lim, dtype):
+    """{name: (value, bound)} of dx, dw, dw1, dw2 of the step from what it kept, as values: tokens x [T, H] and rows z
+    [P, R].  Rounded to dtype on the way: dy's rows, dh, w h, dz, dx's rows."""
+    T, H = x.shape
+    k = w.shape[1]
+    P, half = T * k, HALF[dtype]
+    pair_row = pair_row.view(T, k)
+    x, z, dy, w = x.double(), z.double(), dy.double(), w.double()
+    dx, bx = torch.zeros(T, H, dtype=torch.float64), torch.zeros(T, H, dtype=torch.float64)
+    dw, bw = torch.zeros(T, k, dtype=torch.float64), torch.zeros(T, k, dtype=torch.float64)
+    dw1, b1, dw2, b2 = (torch.zeros(t.shape, dtype=torch.float64) for t in (w1, w1, w2, w2))
+    of_row = {int(pair_row[t, i]): (t, i) for t in range(T) for i in range(k) if int(pair_row[t, i]) >= 0}
+    for e in range(w1.shape[0]):
+        rows = list(range(start[e], start[e + 1]))
+        if not rows:
+            continue
+        tok, place = [of_row[r][0] for r in rows], [of_row[r][1] for r in rows]
+        v1, v2 = w1[e].double(), w2[e].double()
+        ww = w[tok, place][:, None]
+        do = dy[tok]
+        edo = half * do.abs()
+        dh, size = do @ v2, do.abs() @ v2.abs()
+        edh = edo @ v2.abs() + (H + 4) * U * size
+        edh = edh + half * (dh.abs() + edh)
+        h, eh, _ = act64(z[rows], "swiglu", lim)
+        f, ef = act_grad64(z[rows], "swiglu", lim)
+        dw[tok, place] = (dh * h).sum(1)
+        bw[tok, place] = (edh * (h.abs() + eh) + dh.abs() * eh).sum(1) + (h.shape[1] // 64 + 24) * U * (dh * h).abs().sum(1)
+        wh = ww * h
+        ewh = ww * eh + 2 * U * wh.abs()
+        ewh = ewh + half * (wh.abs() + ewh)
+        dd, edd = torch.cat((dh, dh), 1), torch.cat((edh, edh), 1)
+        dz = ww * dd * f
+        edz = ww * (edd * (f.abs() + ef) + dd.abs() * ef) + 4 * U * dz.abs()
+        edz = edz + half * (dz.abs() + edz)
+        n = len(rows) + 40
+
+        def product(a, ea, b, eb, n):
+            size = a.abs() @ b.abs()
+            err = ea @ (b.abs() + eb) + a.abs() @ eb + n * U * size
+            v = a @ b
+            return v, err + half * (v.abs() + err)
+
+        zero = torch.zeros_like
+        dw2[e], b2[e] = product(do.t(), edo.t(), wh, ewh, n)
+        dw1[e], b1[e] = product(dz.t(), edz.t(), x[tok], zero(x[tok]), n)
+        part, epart = product(dz, edz, v1, zero(v1), v1.shape[0] + 4)
+        for r in range(len(rows)):
+            dx[tok[r]] += part[r]
+            bx[tok[r]] += epart[r] + (k + 1) * U * part[r].abs()
+    bx = bx + half * (dx.abs() + bx)
+    return {"dx": (dx, bx), "dw": (dw, bw), "dw1": (dw1, b1), "dw2": (dw2, b2)}
