@@ -207,9 +207,9 @@ __device__ __forceinline__ int take_best(double* v, int lane, double& best) {
   return id;
 }
 
-// Place j's expert in lane j (-1: none).
+// Place j's expert in lane j (-1: none).  room: the wave's LDS, 64 N values.
 template <int N>
-__device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, float top) {
+__device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, float top, double* room) {
   const double NONE = -INFINITY;
   float l[N];
   double v[N], sum = 0;
@@ -244,27 +244,31 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
   double best;
   if (groups) {
     const int size = a.E / a.groups;
-    double of[1] = {NONE};  // lane g: the value of group g
+    // lane g: the value of group g by a scan (its two best by exchanges, one group after the other: 8 us of a launch
+    // instead of 1), and its rank among the groups
+#pragma unroll
+    for (int i = 0; i < N; ++i) room[lane + 64 * i] = v[i];
+    lds_turn();
+    double m1 = NONE, m2 = NONE;
+    if (lane < a.groups) {
+      const double* from = room + lane * size;
+#pragma unroll 8
+      for (int c = 0; c < size; ++c) {
+        const int at = c + lane < size ? c + lane : c + lane - size;  // (lanes start apart, so that their reads meet other banks)
+        const double x = from[lane < size ? at : c];
+        m2 = fmax(m2, fmin(m1, x));
+        m1 = fmax(m1, x);
+      }
+    }
+    const double of = a.best > 1 && m2 > NONE ? m1 + m2 : m1;
+    int rank = 0;
 #pragma unroll 1
     for (int g = 0; g < a.groups; ++g) {
-      double part[N], two = 0;
-      int there = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int e = lane + 64 * i - g * size;
-        part[i] = e >= 0 && e < size ? v[i] : NONE;
-      }
-#pragma unroll 1
-      for (int j = 0; j < a.best; ++j)
-        if (take_best<N>(part, lane, best) >= 0) { two += best; ++there; }
-      if (lane == g && there) of[0] = two;
+      const double o = lane_f64(of, g);
+      rank += o > of || (o == of && g < lane) ? 1 : 0;
     }
-    uint64_t taken = 0;
-#pragma unroll 1
-    for (int j = 0; j < a.top_groups; ++j) {
-      const int g = take_best<1>(of, lane, best);
-      if (g >= 0) taken |= 1ull << g;
-    }
+    const uint64_t taken = __ballot(lane < a.groups && rank < a.top_groups);
+    lds_turn();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const bool on = l[i] > -INFINITY && ((taken >> ((lane + 64 * i) / size)) & 1);
@@ -290,7 +294,8 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   static_assert(L * N <= 1 << ID_BITS, "an expert's number fits");
   constexpr float UNITS = (float)(1 << BITS);
   constexpr int ROW = L * N + L * N / 32;  // values of a token in LDS, one more place behind each 32
-  __shared__ float lds[CHOOSE_WAVES][TOK][ROW];
+  constexpr int ROOM = TOK * ROW > 2 * L * N ? TOK * ROW : 2 * L * N;  // (fp32 values of all tokens, or 64-bit ones of one)
+  __shared__ __align__(8) float lds[CHOOSE_WAVES][ROOM];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, j = lane % L, slot = lane / L;
   const int t0 = (blockIdx.x * CHOOSE_WAVES + wave) * TOK;
   if (t0 >= a.T) return;
@@ -312,9 +317,12 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   if (a.bias || groups || !(a.renorm || a.sigmoid)) {
     scores<L, N>(a, l, top, v, total);
     most = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-top)) : (total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f);
-    // A score is off by at most 2^-21 (1 + |top| / 4 if top < 0) of the largest (for l <= top < 0 |l| exp(l) is at most
-    // (|top| + 1) exp(top)), its sum with b by 2^-24 of itself; two of them, with room.
-    near = ldexpf(most * (1.0f + fmaxf(-top, 0.f) * 0.25f) + b_most, -19);
+    // In units of 2^-23: exp(-l) is off by 0.75 |l| + 1 of itself (the exponent's rounding, v_exp_f32), 1 + exp(-l) by
+    // 1/2, its reciprocal by 1, and s (1 - s) |l| is at most 0.23, or for l <= top < 0 (|top| + 1) exp(top): a sigmoid is off
+    // by 4 + 0.75 |top| of the largest, |top| if below 0.  A softmax score is off by 2 of the largest, and all of a
+    // token's by one factor, its sum's 20 additions: 10 of the difference.  The sum with b is off by 1/2 of both.
+    // All of it twice, for two values.
+    near = ldexpf(most * (a.sigmoid ? 9.f + fmaxf(-top, 0.f) * 1.5f : 16.f) + b_most, -23);
     if (!(top > -INFINITY)) near = 0.f;
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = l[i] == -INFINITY ? -INFINITY : v[i] + b[i];
@@ -323,7 +331,7 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   const int size = a.E / a.groups;
   const uint32_t per = (1u << 20) / size + 1;  // e / size = e * per >> 20 (e, size <= 1024)
   if (groups) {
-    float* part = &lds[wave][slot][0];
+    float* part = &lds[wave][slot * ROW];
     const int w = size >> 2;  // lanes of a group
     if (size % 4 == 0 && w <= 16 && (w & (w - 1)) == 0) {
       // a group's two best by exchanges between the lanes that hold it
@@ -354,7 +362,7 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
         const int p = lane + 64 * q, s = p / a.groups, g = p - s * a.groups;
         float m1 = -INFINITY, m2 = -INFINITY;
         if (s < TOK) {
-          const float* from = &lds[wave][s][0];
+          const float* from = &lds[wave][s * ROW];
 #pragma unroll 4
           for (int c = 0; c < size; ++c) {
             const int e = g * size + c;
@@ -369,7 +377,7 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
 #pragma unroll
       for (int q = 0; q < TOK; ++q) {
         const int p = lane + 64 * q, s = p / a.groups;
-        if (s < TOK) lds[wave][s][p - s * a.groups] = of[q];
+        if (s < TOK) lds[wave][s * ROW + p - s * a.groups] = of[q];
       }
     }
     lds_turn();
@@ -453,7 +461,7 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   int id = mine ? (int)(ID_MASK - (mine & ID_MASK)) : -1;
   for (uint64_t again = __ballot(there && !sure && j == 0); __builtin_expect(again != 0, 0); again &= again - 1) {
     const int first = __builtin_ctzll(again);  // of the token's lanes
-    const int exact = choose64<L * N / 64>(a, t0 + first / L, lane, lane_f32(top, first));
+    const int exact = choose64<L * N / 64>(a, t0 + first / L, lane, lane_f32(top, first), reinterpret_cast<double*>(&lds[wave][0]));
     // (from lanes 0 .. k - 1 to the token's)
     const int moved = __shfl(exact, j);
     id = lane / L == first / L ? moved : id;
