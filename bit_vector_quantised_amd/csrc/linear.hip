@@ -289,13 +289,15 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   const int nt = (g.out_n + per_n - 1) / per_n;
   int grp = 0, im, in, split, r0, r1, m0;
   if (MODE == GEMM_DW) {
-    const int mt = (g.out_m + BM - 1) / BM;
-    const int tiles = mt * nt * g.G;
-    const int bid = xcd_order(blockIdx.x, tiles * g.splits);
-    split = bid / tiles;
-    const int id = bid - split * tiles;
-    grp = id / (mt * nt);
-    band_order<4>(id - grp * mt * nt, mt, nt, im, in);
+    // Every XCD takes an eighth of each group's tiles (neighbouring ones), as groups differ in their rows, by which a
+    // tile's work goes; which eighth, the longer ones first, turns with the group.
+    const int mt = (g.out_m + BM - 1) / BM, tiles = mt * nt, per = (tiles + 7) / 8;
+    const int x = blockIdx.x & 7, q = blockIdx.x >> 3, all = q / per;
+    split = all / g.G;
+    grp = all - split * g.G;
+    const int eighth = (x + grp) & 7, id = eighth * per + q - all * per;
+    if (id >= tiles) return;  // (the last eighths may be short)
+    band_order<4>(id, mt, nt, im, in);
     group_rows(g, grp, r0, r1);
     m0 = im * BM;
   } else {
@@ -890,7 +892,7 @@ void gemm_go(const GemmArgs& g, hipStream_t st) {
   // (each group of rows adds at most one partial row tile)
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
-  const long grid = nt * mt * g.splits;
+  const long grid = MODE == GEMM_DW ? (nt * div_up(g.out_m, BM) + 7) / 8 * 8 * g.G * g.splits : nt * mt * g.splits;
   if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
 }
 
