@@ -290,7 +290,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   int grp = 0, im, in, split, r0, r1, m0;
   if (MODE == GEMM_DW) {
     // Every XCD takes an eighth of each group's tiles (neighbouring ones), as groups differ in their rows, by which a
-    // tile's work goes; which eighth, the longer ones first, turns with the group.
+    // tile's work goes; which eighth, the longer ones first, turns with the group.  (Whole groups to an XCD: 16 uneven
+    // groups' 8192 rows, dw of 4096 x 7168 each 663 us, so 597; 16384 rows, 7168 x 2048 677 and 503.  XCDs that
+    // begin with different groups: 604, but 32 groups' 32768 rows 2210 instead of 2090.)
     const int mt = (g.out_m + BM - 1) / BM, tiles = mt * nt, per = (tiles + 7) / 8;
     const int x = blockIdx.x & 7, q = blockIdx.x >> 3, all = q / per;
     split = all / g.G;
