@@ -14,14 +14,15 @@ namespace mvq {
 namespace {
 
 constexpr int PACK_THREADS = 256;
+constexpr size_t STREAM_BYTES = (size_t)256 << 20;
 
-// Eight columns per thread, four threads to a block.  The columns behind the row's last are zeros.
+// Eight columns per thread, four threads to a block; rows from `first` on.  The columns behind the row's last are zeros.
 template <int DTYPE>
-__global__ __launch_bounds__(PACK_THREADS) void rows8_pack_kernel(Rows8Args a, uint32_t units) {
-  const uint32_t id = blockIdx.x * PACK_THREADS + threadIdx.x, row = id / units;
-  const int c = (int)(id - row * units) * 8;
-  bool there = row < (uint32_t)a.M;
-  if (a.start) there = there && (int)row >= a.start[0] && (int)row < a.start[a.G];
+__global__ __launch_bounds__(PACK_THREADS) void rows8_pack_kernel(Rows8Args a, uint32_t units, int first) {
+  const uint32_t id = blockIdx.x * PACK_THREADS + threadIdx.x, at_row = id / units;
+  const int row = first + (int)at_row, c = (int)(id - at_row * units) * 8;
+  bool there = row < a.M;
+  if (a.start) there = there && row >= a.start[0] && row < a.start[a.G];
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = 0.f;
@@ -34,27 +35,44 @@ __global__ __launch_bounds__(PACK_THREADS) void rows8_pack_kernel(Rows8Args a, u
   if ((threadIdx.x & 3) == 0) a.e[row * (pitch / 32) + (c >> 5)] = (uint8_t)scale;
 }
 
-// Sixteen columns per thread, to each of the token's k rows (GATHER) or to its own.
-template <int DTYPE, bool GATHER>
-__global__ __launch_bounds__(PACK_THREADS) void rows8_unpack_kernel(Rows8Args a, uint32_t units) {
-  const uint32_t id = blockIdx.x * PACK_THREADS + threadIdx.x, row = id / units;
-  const int c = (int)(id - row * units) * 16, left = (int)a.pitch - c;
-  if (row >= (uint32_t)a.M) return;
-  if (a.start && ((int)row < a.start[0] || (int)row >= a.start[a.G])) return;
+// 16 bytes of each output row per thread, to each of the token's k rows (GATHER) or to its own; rows from `first` on.
+// Neighbouring threads' stores join: with 32 bytes to a thread, in two stores, streamed ones take 256 us
+// instead of 92 for 4096 tokens of 7168 bf16 columns to 8 rows each (not streamed 108 either way).
+template <int DTYPE, bool GATHER, bool STREAM>
+__global__ __launch_bounds__(PACK_THREADS) void rows8_unpack_kernel(Rows8Args a, uint32_t units, int first) {
+  constexpr int N = DTYPE == MOE_VQ_BF16 ? 8 : 4;
+  const uint32_t id = blockIdx.x * PACK_THREADS + threadIdx.x, at_row = id / units;
+  const int row = first + (int)at_row, c = (int)(id - at_row * units) * N, left = (int)a.pitch - c;
+  if (row >= a.M) return;
+  if (a.start && (row < a.start[0] || row >= a.start[a.G])) return;
   const size_t pitch = rows8_pitch(a.C);
-  const u32x4_t w = *reinterpret_cast<const u32x4_t*>(a.q + row * pitch + c);
+  const uint8_t* q = a.q + row * pitch + c;
   const float scale = e8m0_to_f32(a.e[row * (pitch / 32) + (c >> 5)]);
-  float v[16];
-  const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) from_e4m3(words[i], scale, v + 4 * i);
+  float v[8];
+  if constexpr (N == 8) {
+    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(q);
+    from_e4m3(w.x, scale, v);
+    from_e4m3(w.y, scale, v + 4);
+  } else {
+    from_e4m3(*reinterpret_cast<const uint32_t*>(q), scale, v);
+  }
   const int n = GATHER ? a.k : 1;
   for (int i = 0; i < n; ++i) {
-    const int to = GATHER ? a.pair_row[(size_t)row * n + i] : (int)row;
+    const int to = GATHER ? a.pair_row[(size_t)row * n + i] : row;
     if (GATHER && (uint32_t)to >= (uint32_t)(a.M * n)) continue;
     const size_t at = (size_t)to * a.pitch + c;
-    store8(a.y, at, DTYPE, left, v);
-    if (left > 8) store8(a.y, at + 8, DTYPE, left - 8, v + 8);
+    if constexpr (N == 8) {
+      store8<STREAM>(a.y, at, DTYPE, left, v);
+    } else {
+      float* y = static_cast<float*>(a.y) + at;
+      if (left >= 4) {
+        store_vec<STREAM>(reinterpret_cast<f32x4_any*>(y), f32x4_any{v[0], v[1], v[2], v[3]});
+      } else {
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+          if (j < left) y[j] = v[j];
+      }
+    }
   }
 }
 
@@ -94,7 +112,7 @@ __device__ __forceinline__ void act_values(float lim, const float* zg, const flo
 
 constexpr int ACT_THREADS = 256;
 
-// A pair by TX threads (a wave, or the workgroup), eight columns of a thread at a time.  ALIGNED: N is a
+// A pair by TX threads (16, a wave, or the workgroup), eight columns of a thread at a time.  ALIGNED: N is a
 // multiple of 8, and so are the up values' places.
 template <int DTYPE, int DY_DTYPE, int ACT, int TX, bool ALIGNED>
 __global__ __launch_bounds__(ACT_THREADS) void act_back_kernel(ActBackArgs a) {
@@ -131,7 +149,7 @@ __global__ __launch_bounds__(ACT_THREADS) void act_back_kernel(ActBackArgs a) {
     }
   }
   if (!a.dw) return;
-  sum = wave_sum(sum);
+  sum = group_sum<TX < 64 ? TX : 64>(sum);
   if (TX > 64) {
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
     __syncthreads();
@@ -144,28 +162,43 @@ __global__ __launch_bounds__(ACT_THREADS) void act_back_kernel(ActBackArgs a) {
 
 }  // namespace
 
-static unsigned rows8_grid(int M, uint32_t units) { return (unsigned)(((size_t)M * units + PACK_THREADS - 1) / PACK_THREADS); }
+// f(workgroups, first row): threads count their units, `units` to a row, in 32 bits, so many rows take several launches.
+template <typename F>
+static void rows8_go(int M, uint32_t units, F&& f) {
+  const int most = (int)((1u << 30) / units);  // (units: 1 to 8192)
+  for (int first = 0, n; first < M; first += n) {
+    n = M - first < most ? M - first : most;
+    f((unsigned)(((size_t)n * units + PACK_THREADS - 1) / PACK_THREADS), first);
+  }
+}
 
 hipError_t launch_rows8_pack(const Rows8Args& a, int dtype, hipStream_t st) {
   const uint32_t units = (uint32_t)(rows8_pitch(a.C) / 8);
-  const unsigned grid = rows8_grid(a.M, units);
-  if (dtype == MOE_VQ_BF16) rows8_pack_kernel<MOE_VQ_BF16><<<grid, PACK_THREADS, 0, st>>>(a, units);
-  else rows8_pack_kernel<MOE_VQ_F32><<<grid, PACK_THREADS, 0, st>>>(a, units);
+  rows8_go(a.M, units, [&](unsigned grid, int first) {
+    if (dtype == MOE_VQ_BF16) rows8_pack_kernel<MOE_VQ_BF16><<<grid, PACK_THREADS, 0, st>>>(a, units, first);
+    else rows8_pack_kernel<MOE_VQ_F32><<<grid, PACK_THREADS, 0, st>>>(a, units, first);
+  });
   return hipGetLastError();
 }
 
 hipError_t launch_rows8_unpack(const Rows8Args& a, int dtype, hipStream_t st) {
-  const uint32_t units = (uint32_t)((a.pitch + 15) / 16);
-  const unsigned grid = rows8_grid(a.M, units);
-  auto go = [&](auto t, auto gather) {
-    rows8_unpack_kernel<decltype(t)::value, decltype(gather)::value><<<grid, PACK_THREADS, 0, st>>>(a, units);
-  };
-  auto typed = [&](auto t) {
-    if (a.pair_row) go(t, std::true_type{});
-    else go(t, std::false_type{});
-  };
-  if (dtype == MOE_VQ_BF16) typed(std::integral_constant<int, MOE_VQ_BF16>{});
-  else typed(std::integral_constant<int, MOE_VQ_F32>{});
+  const int size = dtype == MOE_VQ_BF16 ? 2 : 4, per = 16 / size;
+  const uint32_t units = (uint32_t)((a.pitch + per - 1) / per);
+  const bool stream = (size_t)a.M * (a.pair_row ? a.k : 1) * a.pitch * size > STREAM_BYTES;
+  rows8_go(a.M, units, [&](unsigned grid, int first) {
+    auto go = [&](auto t, auto gather) {
+      constexpr int T = decltype(t)::value;
+      constexpr bool G = decltype(gather)::value;
+      if (stream) rows8_unpack_kernel<T, G, true><<<grid, PACK_THREADS, 0, st>>>(a, units, first);
+      else rows8_unpack_kernel<T, G, false><<<grid, PACK_THREADS, 0, st>>>(a, units, first);
+    };
+    auto typed = [&](auto t) {
+      if (a.pair_row) go(t, std::true_type{});
+      else go(t, std::false_type{});
+    };
+    if (dtype == MOE_VQ_BF16) typed(std::integral_constant<int, MOE_VQ_BF16>{});
+    else typed(std::integral_constant<int, MOE_VQ_F32>{});
+  });
   return hipGetLastError();
 }
 
@@ -176,7 +209,9 @@ static void act_back_go(const ActBackArgs& a, hipStream_t st) {
     act_back_kernel<DTYPE, DY_DTYPE, ACT, TX, decltype(aligned)::value><<<(a.P + rows - 1) / rows, ACT_THREADS, 0, st>>>(a);
   };
   auto wide = [&](auto aligned) {
-    if (a.N <= 1024) go(std::integral_constant<int, 64>{}, aligned);
+    // (129312 rows of 128 fp32 columns, swiglu: 115 us by a wave to a row, 68 by 16 lanes)
+    if (a.N <= 256) go(std::integral_constant<int, 16>{}, aligned);
+    else if (a.N <= 1024) go(std::integral_constant<int, 64>{}, aligned);
     else go(std::integral_constant<int, ACT_THREADS>{}, aligned);
   };
   if (a.N % 8 == 0) wide(std::true_type{});
