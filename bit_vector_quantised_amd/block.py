@@ -147,15 +147,11 @@ class Router(_OnDevice):
         self.dlogits = self._new((max_tokens, E), torch.float32) if backward else None
         self.n_tokens = None  # of the last forward
 
-    def _here(self) -> None:
-        """The buffers are in use by the current stream, through this object's parts."""
-        self._call(lambda stream: None)
-
     def forward(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         """x [T, H] -> ids [T, k] (int32) and w [T, k] (fp32), valid until the next forward."""
         T = x.shape[0]
         self.n_tokens = None
-        self._here()
+        self._here()  # (the parts' calls use this object's buffers)
         if T > self.linear.max_rows:
             raise ValueError(f"{T} tokens, made for {self.linear.max_rows}")
         self.linear.forward(x, out=self.logits[:T])
@@ -214,9 +210,9 @@ class MoeBlock(_OnDevice):
         self._kept = None
         if T > self.experts.rows.max_tokens:
             raise ValueError(f"{T} tokens, made for {self.experts.rows.max_tokens}")
-        if keep and self.dn is None:
+        if keep and (self.dn is None or self.router.dlogits is None or self.norm.ws is None):
             raise ValueError("made without backward")
-        self._call(lambda stream: None)
+        self._here()  # (the parts' calls use this object's buffers)
         kept8 = keep and self.experts.kept8
         self.norm.forward(x, residual, s, self.n[:T], self.experts.x8 if kept8 else None)
         ids, w = self.router.forward(self.n[:T])
@@ -232,7 +228,7 @@ class MoeBlock(_OnDevice):
         if self._kept is None:
             raise ValueError("the last forward kept nothing")
         T, self._kept = self._kept, None
-        self._call(lambda stream: None)
+        self._here()  # (the parts' calls use this object's buffers)
         self.experts.backward(dy, self.dn[:T], self.dw[:T], dw1, dw2)
         self.router.backward(self.experts.x8 if self.experts.kept8 else self.n[:T], self.dw[:T], self.dn2[:T], drouter)
         self.norm.backward(s, self.dn[:T], self.dn2[:T], ds, dx, dgain)

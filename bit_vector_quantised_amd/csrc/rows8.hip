@@ -14,7 +14,7 @@ namespace mvq {
 namespace {
 
 constexpr int PACK_THREADS = 256;
-constexpr size_t STREAM_BYTES = (size_t)256 << 20;
+constexpr size_t STREAM_BYTES = (size_t)256 << 20;  // outputs that the memory-side cache does not hold are streamed
 
 // Eight columns per thread, four threads to a block; rows from `first` on.  The columns behind the row's last are zeros.
 template <int DTYPE>
@@ -114,7 +114,7 @@ constexpr int ACT_THREADS = 256;
 
 // A pair by TX threads (16, a wave, or the workgroup), eight columns of a thread at a time.  ALIGNED: N is a
 // multiple of 8, and so are the up values' places.
-template <int DTYPE, int DY_DTYPE, int ACT, int TX, bool ALIGNED>
+template <int DTYPE, int DY_DTYPE, int ACT, int TX, bool ALIGNED, bool STREAM>
 __global__ __launch_bounds__(ACT_THREADS) void act_back_kernel(ActBackArgs a) {
   __shared__ float red[ACT_THREADS / 64];
   constexpr bool two = ACT == MOE_VQ_ACT_SWIGLU;
@@ -141,10 +141,10 @@ __global__ __launch_bounds__(ACT_THREADS) void act_back_kernel(ActBackArgs a) {
         dg[j] *= d;
         if (two) du[j] *= d;
       }
-      if (a.y) store8(a.y, row * a.N + n, DTYPE, left, y);
+      if (a.y) store8<STREAM>(a.y, row * a.N + n, DTYPE, left, y);
       if (a.dz) {
-        store8(a.dz, row * a.R + n, DTYPE, left, dg);
-        if (two) store8(a.dz, row * a.R + a.N + n, DTYPE, left, du);
+        store8<STREAM>(a.dz, row * a.R + n, DTYPE, left, dg);
+        if (two) store8<STREAM>(a.dz, row * a.R + a.N + n, DTYPE, left, du);
       }
     }
   }
@@ -206,7 +206,15 @@ template <int DTYPE, int DY_DTYPE, int ACT>
 static void act_back_go(const ActBackArgs& a, hipStream_t st) {
   auto go = [&](auto tx, auto aligned) {
     constexpr int TX = decltype(tx)::value, rows = ACT_THREADS / TX;
-    act_back_kernel<DTYPE, DY_DTYPE, ACT, TX, decltype(aligned)::value><<<(a.P + rows - 1) / rows, ACT_THREADS, 0, st>>>(a);
+    constexpr bool A = decltype(aligned)::value;
+    // (32768 rows of 2048 columns, swiglu: 144 us, streamed 140; of fp32 rows a thread's 32 bytes are two stores, see above)
+    if constexpr (TX == ACT_THREADS && DTYPE == MOE_VQ_BF16 && A) {
+      if ((size_t)a.P * (a.R + a.N) * 2 > STREAM_BYTES) {
+        act_back_kernel<DTYPE, DY_DTYPE, ACT, TX, A, true><<<(a.P + rows - 1) / rows, ACT_THREADS, 0, st>>>(a);
+        return;
+      }
+    }
+    act_back_kernel<DTYPE, DY_DTYPE, ACT, TX, A, false><<<(a.P + rows - 1) / rows, ACT_THREADS, 0, st>>>(a);
   };
   auto wide = [&](auto aligned) {
     // (129312 rows of 128 fp32 columns, swiglu: 115 us by a wave to a row, 68 by 16 lanes)

@@ -57,7 +57,8 @@ class _OnDevice:
         self._streams.clear()  # (whatever this object's streams know, they may not know of this one)
         return t
 
-    def _call(self, fn, *args) -> None:
+    def _here(self) -> int:
+        """The current stream of the object's device, which is told to the buffers' allocator."""
         # (the bindings beneath torch.cuda.current_stream and current_device: an object for the stream costs a
         # microsecond, a sixth of a small call)
         index = self.device.index
@@ -66,10 +67,14 @@ class _OnDevice:
             for t in self._buffers:
                 t.record_stream(torch.cuda.current_stream(index))
             self._streams.add(stream)
-        if torch._C._cuda_getDevice() == index:
+        return stream
+
+    def _call(self, fn, *args) -> None:
+        stream = self._here()
+        if torch._C._cuda_getDevice() == self.device.index:
             fn(*args, stream)
         else:
-            with torch.cuda.device(index):
+            with torch.cuda.device(self.device.index):
                 fn(*args, stream)
 
 
@@ -77,7 +82,7 @@ class Rows8(_OnDevice):
     """Rows in 8 bits, for up to n_rows rows of n_cols columns: q [n_rows, pitch] holds e4m3 values (pitch: n_cols
     rounded up to 32), e [n_rows, pitch / 32] a power of two (+ 127, as an exponent) for each 32 columns.  A value is
     off by at most 1/16 of itself (by 2^-10 scales if it is below 2^-6 of them), and what the bytes stand for is
-    exact in bf16 and fp32.  Like a tensor it is the caller's: a call that reads it uses its first rows."""
+    exact in bf16 and fp32.  Calls of other objects that take it use its first rows."""
 
     def __init__(self, n_rows: int, n_cols: int, device="cuda"):
         super().__init__(_device(device))
@@ -90,10 +95,11 @@ class Rows8(_OnDevice):
         self._shapes = self.q.shape, self.e.shape
 
     def desc(self, what: str, n_rows: int, n_cols: int, device) -> _lib.Rows8Desc:
-        """The addresses, for a call that takes n_rows rows of n_cols columns."""
+        """The addresses, for a call on the current stream that takes n_rows rows of n_cols columns."""
         if n_rows > self.n_rows or n_cols != self.n_cols or device != self.device:
             raise ValueError(f"{what}: need up to {n_rows} rows of {n_cols} columns on {device}, "
                              f"got {self.n_rows} of {self.n_cols} on {self.device}")
+        self._here()
         return _lib.Rows8Desc(_need(self.q, "q", self._shapes[0], torch.uint8, self.device),
                               _need(self.e, "e", self._shapes[1], torch.uint8, self.device))
 

@@ -158,6 +158,46 @@ def test_act_backward(act, T, k, N, dtype, dy_dtype, dropped, weighted):
             assert torch.equal(one, whole), name
 
 
+def test_outputs_larger_than_the_cache():
+    """Streamed rows: gathered from 8 bits, unpacked, and those of the way back through swiglu, looked at where they begin, end
+    and in between."""
+    say("streamed rows")
+    g = gen(77)
+    T, k, E, N = 9000, 8, 16, 1032
+    rows = ExpertRows(E, k, T)
+    ids = torch.randint(-1, E, (T, k), generator=g, dtype=torch.int32)
+    rows.sort(ids.cuda())
+    pair_row, P = rows.pair_row.cpu(), T * k
+    some = torch.cat((torch.arange(4), torch.randint(0, T, (60,), generator=g), torch.arange(T - 4, T)))
+    x8 = Rows8(T, 2 * N).pack(torch.randn(T, 2 * N, device="cuda"))
+    for dtype in (BF16, F32):
+        out = torch.full((P, 2 * N), -3.0, dtype=dtype, device="cuda")
+        rows.gather(x8, out)
+        for t in some.tolist():
+            want = ref.from8(x8.q[t:t + 1], x8.e[t:t + 1], 2 * N)[0]
+            for i in range(k):
+                r = int(pair_row[t * k + i])
+                if r >= 0:
+                    assert torch.equal(out[r].double().cpu(), want)
+        n = int(rows.expert_start[-1])
+        assert (out[n:] == -3).all()
+    z8 = Rows8(P, 2 * N).pack(out)
+    assert torch.equal(z8.unpack()[:n], out[:n].to(BF16))  # (they are values of 8 bits already)
+    del out
+    dy, w = torch.randn(P, N, device="cuda").bfloat16(), torch.rand(T, k, generator=g)
+    dz, y, dw = torch.empty(P, 2 * N, dtype=BF16, device="cuda"), torch.empty(P, N, dtype=BF16, device="cuda"), torch.empty(T, k, device="cuda")
+    rows.act_backward(z8, dy, w.cuda(), "swiglu", 2.0, dz, y, dw)
+    pairs = torch.cat([torch.arange(t * k, t * k + k) for t in some.tolist()])
+    pairs = pairs[pair_row[pairs] >= 0]
+    at = pair_row[pairs].long()
+    want, _ = ref.act_backward64(ref.from8(z8.q[at.cuda()], z8.e[at.cuda()], 2 * N), dy[at.cuda()].cpu(), torch.arange(len(at)),
+                                 w.view(-1)[pairs], "swiglu", 2.0, BF16)
+    dense_ref.check(dz[at.cuda()], *want["dz"], "dz")
+    dense_ref.check(y[at.cuda()], *want["y"], "y")
+    dense_ref.check(dw.view(-1)[pairs.cuda()], *want["dw"], "dw")
+    assert not dw[ids.cuda() < 0].any()
+
+
 @pytest.mark.parametrize("x8,z8", [(True, True), (True, False), (False, True)])
 @pytest.mark.parametrize("M,K,N,act,start,dtype,dy_dtype,bias", [
     (40, 64, 48, "swiglu", None, BF16, BF16, True), (33, 100, 37, "gelu", None, F32, F32, True),

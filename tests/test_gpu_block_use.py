@@ -301,6 +301,65 @@ def test_on_another_stream():
         assert torch.equal(a, c)
 
 
+def test_buffers_outlive_the_calls_of_a_dropped_object():
+    """An object used on a side stream and dropped at once, also one that only other objects' calls have used there: its
+    buffers are not given out again while the side stream's work is under way."""
+    say("buffers of dropped objects")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    T, H, I, E, k = 64, 64, 32, 4, 2
+    x = randn(gen(2), T, H, dtype=BF16).cuda()
+    s, y = torch.empty_like(x), torch.empty_like(x)
+    gain = torch.ones(H, device="cuda")
+    norm = RmsNorm(gain, max_rows=T)
+    out = {}
+
+    def parts(o, seen, met):
+        if id(o) in met:
+            return seen
+        met.add(id(o))
+        for v in vars(o).values():
+            if isinstance(v, torch.Tensor):
+                seen[v.data_ptr()] = v.numel() * v.element_size()
+            elif type(v).__module__.startswith("bit_vector_quantised_amd") and hasattr(v, "__dict__") and not isinstance(v, type):
+                parts(v, seen, met)
+        return seen
+
+    def whole(b):
+        b.forward(x, x, s, y, keep=True)
+        b.backward(s, x, x, *out.values())
+
+    b = block(gen(3), T, H, I, E, k, BF16, True)
+    out = {"dx": torch.empty_like(x), "dgain": torch.empty(H, device="cuda"), "drouter": torch.empty_like(b.router.linear.w),
+           "dw1": torch.empty_like(b.experts.fc1.w), "dw2": torch.empty_like(b.experts.fc2.w)}
+    w = [b.norm.gain, b.router.linear.w, b.experts.fc1.w, b.experts.fc2.w]  # (what a caller owns)
+    del b
+
+    def new_block():
+        step = DenseExperts(w[2], w[3], k, T, backward=True, kept8=True)
+        return MoeBlock(RmsNorm(w[0], max_rows=T, backward=True), Router(w[1], k, T, backward=True), step)
+
+    makers = [(lambda: Rows8(T, H), lambda o: norm.forward(x, rows8=o, dense=False)),
+              (lambda: RmsNorm(gain, max_rows=T, backward=True), lambda o: o.backward(x, x, dgain=out["dgain"])),
+              (lambda: Router(w[1], k, T, backward=True), lambda o: o.forward(x)), (new_block, whole)]
+    mine = {t.data_ptr() for t in (x, s, y, gain, *w, *out.values())}
+    for make, call in makers:
+        o = make()
+        own = {p: n for p, n in parts(o, {}, set()).items() if p not in mine and n}
+        assert own
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)
+            call(o)
+        del o
+        again = [torch.empty(size, dtype=torch.uint8, device="cuda") for size in own.values() for _ in range(3)]
+        assert not side.query()  # (the wait is still under way, so the answer means something)
+        for t in again:
+            assert not any(p <= t.data_ptr() < p + size for p, size in own.items())
+        side.synchronize()
+
+
 def test_router_for_one_token_and_for_none():
     say("router: one token, none")
     g = gen(10)
@@ -392,6 +451,11 @@ def test_refusals():
                          (small, Router(torch.zeros(4, 32, dtype=BF16, device="cuda"), 1, 4)), (small, Router(torch.zeros(4, 32, dtype=BF16, device="cuda"), 2, 3))):
         with pytest.raises(ValueError):
             MoeBlock(norm, router, step)
+    forward_only = MoeBlock(RmsNorm(torch.ones(32, device="cuda"), max_rows=4), Router(torch.zeros(4, 32, dtype=BF16, device="cuda"), 2, 4, backward=True), step)
+    x32 = torch.zeros(4, 32, dtype=BF16, device="cuda")
+    with pytest.raises(ValueError, match="backward"):
+        forward_only.forward(x32, keep=True)
+    assert forward_only.forward(x32).shape == (4, 32)
 
 
 def test_far_rows():
