@@ -287,7 +287,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   // ---- which tile
   constexpr int per_n = GATED ? BN / 2 : BN;  // output columns of a tile
   const int nt = (g.out_n + per_n - 1) / per_n;
-  int grp = 0, im, in, split, r0, r1, m0;
+  constexpr bool HALVES_AT_END = MODE != GEMM_DW && BM * BN >= 256 * 256;
+  int grp = 0, im, in, split, r0, r1, m0, half = 0;
   if (MODE == GEMM_DW) {
     // Every XCD takes an eighth of each group's tiles (neighbouring ones), as groups differ in their rows, by which a
     // tile's work goes; which eighth, the longer ones first, turns with the group.  (Whole groups to an XCD: 16 uneven
@@ -318,8 +319,19 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     }
     const int inc = wave_incl_scan(cnt);
     const int tiles = __builtin_amdgcn_readlane(inc, 63) * nt;
-    if ((int)blockIdx.x >= tiles * g.splits) return;  // (the grid is an upper bound)
-    const int bid = xcd_order(blockIdx.x, tiles * g.splits);
+    int bid;
+    if constexpr (HALVES_AT_END) {
+      // xcd_order, with the tiles of an XCD's last round, if they are half a round or less, as two halves of their rows (16
+      // groups' 8192 rows, 7168 -> 4096, even 601 us forward, so 558, uneven 564 and 537, their dx 600 and 589)
+      const int x = blockIdx.x & 7, q = blockIdx.x >> 3, mine = (tiles >> 3) + (x < (tiles & 7) ? 1 : 0);
+      const int whole = mine & ~31, rest = mine - whole <= 16 ? mine - whole : 0, full = mine - rest;
+      if (q >= full + 2 * rest) return;  // (the grid is an upper bound)
+      half = q < full ? 0 : 1 + ((q - full) & 1);
+      bid = x * (tiles >> 3) + (x < (tiles & 7) ? x : (tiles & 7)) + (q < full ? q : full + ((q - full) >> 1));
+    } else {
+      if ((int)blockIdx.x >= tiles * g.splits) return;  // (the grid is an upper bound)
+      bid = xcd_order(blockIdx.x, tiles * g.splits);
+    }
     split = bid / tiles;
     const int id = bid - split * tiles, row_tile = id / nt;
     const int l = __popcll(__ballot(inc <= row_tile));  // the lane whose groups hold it
@@ -334,6 +346,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     }
     band_order<8>(id - before * nt, n, nt, im, in);
     m0 = r0 + im * BM;
+    if (half) {
+      const int end = m0 + BM < r1 ? m0 + BM : r1, mid = m0 + BM / 2;
+      if (half == 1) r1 = mid < end ? mid : end;
+      else if (mid < end) { m0 = mid; r1 = end; }
+      else return;  // (its rows fit the first half)
+    }
   }
   const int n0 = in * per_n;
 
@@ -895,7 +913,8 @@ void gemm_go(const GemmArgs& g, hipStream_t st) {
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
   const long grid = MODE == GEMM_DW ? (nt * div_up(g.out_m, BM) + 7) / 8 * 8 * g.G * g.splits : nt * mt * g.splits;
-  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
+  const long more = MODE != GEMM_DW && BM * BN >= 256 * 256 ? 8 * 17 : 0;  // (an XCD's last 16 tiles in halves)
+  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)(grid + more), 64 * WM * WN, 0, st>>>(g);
 }
 
 template <int MODE>
