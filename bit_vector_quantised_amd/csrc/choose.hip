@@ -284,7 +284,10 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
   return mine;
 }
 
-// The choice: 64 / L tokens of a wave side by side, N experts in a lane.  Values become whole numbers of
+// The choice: 64 / L tokens of a wave side by side, N experts in a lane: what goes over a token's lanes is shared by
+// four tokens (a token to a wave with its rounds over 64-bit words: 92 us for 16384 tokens among 256 experts in 8 groups
+// with biases, this way 18, of which the last 5 are waves with a token for 64 bits; 65536 tokens 42 us, some 380
+// instructions a token, where their logits alone take 14; one token 5.6).  Values become whole numbers of
 // BITS bits over their range with the expert's number below them, so that a round of the choice is a maximum of 32-bit
 // words that are all different, and ties fall to the lower expert.
 template <int L, int N>

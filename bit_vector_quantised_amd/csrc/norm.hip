@@ -6,7 +6,9 @@
 //             dg = sum over the rows of (dy + dy2) s rho
 //
 // Every value is moved once and the sums are over the row that a workgroup holds in registers, so both are bound
-// by memory.  Sums are fp32 in a fixed order, without atomics.
+// by memory: 4096 rows of 7168 columns in bf16 take 55 us forward with s, y and 8 bits (265 MB: 4.8 TB/s; a large copy
+// reaches 5.0) and 59 us back with two gradients of y and one of s (294 MB), the gain's parts 5 us more; one row 3.3 us.
+// Sums are fp32 in a fixed order, without atomics.
 #include "rows8_device.h"
 
 namespace mvq {
@@ -39,7 +41,9 @@ __device__ __forceinline__ void row_sums(float* v, float (*red)[N]) {
   }
 }
 
-// A row by LPR lanes, or (0) by a workgroup, NCH chunks of eight columns per thread.
+// A row by LPR lanes, or (0) by a workgroup of as many threads as it has eights of columns (up to 8192 columns in one
+// chunk: one load of each operand per thread, and as many waves on their way as a CU takes), NCH chunks of eight
+// columns per thread.
 template <int XT, int ST, int YT, int NCH, int LPR>
 __global__ __launch_bounds__(LPR ? 256 : 1024) void norm_kernel(NormArgs a) {
   __shared__ float red[16][1];

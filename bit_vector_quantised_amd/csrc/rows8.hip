@@ -6,7 +6,9 @@
 //   act_back  from z in 8 bits and dy, the gradient of the weighted sum's input rows, of each routed pair p with
 //             row r:  y_r = w_p act(z_r),  dz_r = w_p dy_r act'(z_r),  dw_p = <dy_r, act(z_r)>
 //
-// All of them move each byte once and are bound by memory.
+// All of them move each byte once and are bound by memory (a large copy: 5.0 TB/s).  In bf16: 32768 rows of 4096 columns
+// into 8 bits 80 us (406 MB), out of them 69; 4096 tokens of 7168 columns to 8 rows each 91 us (500 MB); the way back
+// through swiglu of 32768 rows of 2048 columns 140 us (674 MB).
 #include "rows8_device.h"
 
 namespace mvq {
