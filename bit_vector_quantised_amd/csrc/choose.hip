@@ -95,7 +95,7 @@ __device__ __forceinline__ void load_row(const float* row, int E, int j, float* 
     }
   }
 }
-// A token's logits (-inf where an expert is off: where l + b is -inf or NaN) and the biases.
+// A token's logits (-inf where an expert is off) and the biases.
 template <int L, int N>
 __device__ __forceinline__ void load_token(const ChooseArgs& a, int t, int j, float* l, float* b) {
   load_row<L, N>(a.logits + (size_t)t * a.E, a.E, j, l);
@@ -104,7 +104,7 @@ __device__ __forceinline__ void load_token(const ChooseArgs& a, int t, int j, fl
   if (a.bias) load_row<L, N>(a.bias, a.E, j, b);
 #pragma unroll
   for (int i = 0; i < N; ++i)
-    l[i] = expert_of<L>(i, j) < a.E && l[i] + b[i] > -INFINITY ? l[i] : -INFINITY;
+    l[i] = expert_of<L>(i, j) < a.E && l[i] > -INFINITY && b[i] > -INFINITY ? l[i] : -INFINITY;  // (NaN too)
 }
 // Scores, for softmax also the sum of exp(l - top).  exp and 1/x by the hardware: an error of |x| 2^-24 of
 // the exponential beside a few roundings.
@@ -218,7 +218,7 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
   for (int i = 0; i < N; ++i) {
     const int e = lane + 64 * i, at = e < a.E ? e : 0;
     const float x = a.logits[(size_t)t * a.E + at], b = a.bias ? a.bias[at] : 0.f;
-    l[i] = e < a.E && x + b > -INFINITY ? x : -INFINITY;
+    l[i] = e < a.E && x > -INFINITY && b > -INFINITY ? x : -INFINITY;
     v[i] = l[i];
   }
   if (a.bias || groups) {

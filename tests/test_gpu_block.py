@@ -437,6 +437,28 @@ def test_choose_infinities():
         assert torch.isfinite(d).all() and (d[:, [9, 11]] == 0).all()
 
 
+def test_choose_masks_of_the_lowest_value():
+    """The type's lowest value is a value, not -inf: such experts come last, in order, with weights of 0."""
+    say("choose: lowest values")
+    E, T, k = 96, 12, 16
+    low = torch.finfo(F32).min
+    g = gen(31)
+    logits = randn(g, T, E)
+    logits[:, 5:] = torch.where(torch.rand(T, E - 5, generator=g) < 0.9, low, logits[:, 5:])
+    logits[1] = low
+    bias = 0.1 * randn(g, E)
+    bias[[2, 40, 41]] = low
+    for b in (None, bias):
+        for kw in (dict(), dict(score="sigmoid"), dict(score="softmax", renorm=False), dict(score="sigmoid", groups=8, top_groups=5)):
+            choice = make(E, k, bias=None if b is None else b.cuda(), **kw)
+            ids, w = choice.forward(logits.cuda())
+            want, ww, rel = ref.choose64(logits, b, k, **{"top_groups": kw.get("groups", 1), **kw})
+            assert torch.equal(ids.cpu().long(), want) and (ids >= 0).all()
+            dense_ref.check(w, ww, rel * ww.abs(), "w")
+            d = choice.backward(logits.cuda(), ids, torch.ones(T, k, device="cuda"))
+            assert torch.isfinite(d).all()
+
+
 def test_choose_backward_of_other_ids():
     """The same expert twice gets both parts; ids that are none get nothing."""
     say("choose backward: other ids")
