@@ -286,11 +286,12 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
 
 // The choice: 64 / L tokens of a wave side by side, N experts in a lane: what goes over a token's lanes is shared by
 // four tokens (a token to a wave with its rounds over 64-bit words: 92 us for 16384 tokens among 256 experts in 8 groups
-// with biases, this way 18, of which the last 5 are waves with a token for 64 bits; 65536 tokens 42 us, some 380
-// instructions a token, where their logits alone take 14; one token 5.6).  Values become whole numbers of
+// with biases, this way 17, of which the last 5 are waves with a token for 64 bits; 65536 tokens 38 us, some 350
+// instructions a token, where their logits alone take 14; one token 5.1).  Values become whole numbers of
 // BITS bits over their range with the expert's number below them, so that a round of the choice is a maximum of 32-bit
 // words that are all different, and ties fall to the lower expert.
-template <int L, int N>
+// KEEP of a lane's words in order are enough for k + 1 rounds.
+template <int L, int N, int KEEP>
 __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   constexpr int TOK = 64 / L, ID_BITS = L == 16 ? 8 : 10, BITS = 32 - ID_BITS;
   constexpr uint32_t ID_MASK = (1u << ID_BITS) - 1;
@@ -317,7 +318,8 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   const bool groups = a.top_groups < a.groups;
   bool sure = top < INFINITY;
   float near = 0.f, most = 0.f;  // how close two values may be for fp32 to order them; the largest score
-  if (a.bias || groups || !(a.renorm || a.sigmoid)) {
+  const bool scored = a.bias || groups || !(a.renorm || a.sigmoid);
+  if (scored) {
     scores<L, N>(a, l, top, v, total);
     most = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-top)) : (total > 0.f ? __builtin_amdgcn_rcpf(total) : 0.f);
     // In units of 2^-23: exp(-l) is off by 0.75 |l| + 1 of itself (the exponent's rounding, v_exp_f32), 1 + exp(-l) by
@@ -327,8 +329,14 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
     // All of it twice, for two values.
     near = ldexpf(most * (a.sigmoid ? 9.f + fmaxf(-top, 0.f) * 1.5f : 16.f) + b_most, -23);
     if (!(top > -INFINITY)) near = 0.f;
+    if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = l[i] == -INFINITY ? -INFINITY : v[i] + b[i];
+      for (int i = 0; i < N; ++i) v[i] += b[i];
+    }
+    if (groups) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = l[i] == -INFINITY ? -INFINITY : v[i];
+    }
   }
   uint64_t taken = ~0ull;
   const int size = a.E / a.groups;
@@ -384,32 +392,29 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
       }
     }
     lds_turn();
-    // Every lane of a token ranks some of its groups.
+    // Lane j of a token ranks group j, then j + L ..
     taken = 0;
     float in = INFINITY, out = -INFINITY;
 #pragma unroll 1
-    for (int g = j; g < a.groups; g += L) {
-      const float mine = part[g];
+    for (int g0 = 0; g0 < a.groups; g0 += L) {
+      const int g = g0 + j;
+      const float mine = part[g < a.groups ? g : 0];
       int rank = 0;
 #pragma unroll 8
       for (int h = 0; h < a.groups; ++h) {
         const float o = part[h];
         rank += o > mine || (o == mine && h < g) ? 1 : 0;
       }
-      if (rank < a.top_groups) {
-        taken |= 1ull << g;
-        in = fminf(in, mine);
-      } else {
-        out = fmaxf(out, mine);
-      }
+      const bool real = g < a.groups, stays = real && rank < a.top_groups;
+      if (stays) in = fminf(in, mine);
+      else if (real) out = fmaxf(out, mine);
+      const uint64_t all = __ballot(stays) >> (lane - j);
+      taken |= (L == 64 ? all : all & 0xFFFFull) << g0;
     }
     in = -max_of<L>(-in);
     out = max_of<L>(out);
     // (both values are sums of two; nothing hangs on groups without experts)
     if (out > -INFINITY && !(in - out > 2.f * near)) sure = false;
-    // every lane's bits together
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) taken |= __shfl_xor((unsigned long long)taken, d);
   }
   // ---- whole numbers, 1 and more
   uint32_t key[N], tol = 0;
@@ -424,11 +429,13 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
     } else {
       low = top - 16.f;  // (what lies below is told apart in 64 bits)
       unit = UNITS / 16.f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = l[i];
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = expert_of<L>(i, j);
-      const float x = fmaf((a.bias ? v[i] : l[i]) - low, unit, 1.f);
+      const float x = fmaf(v[i] - low, unit, 1.f);
       const uint32_t n = (uint32_t)__builtin_amdgcn_fmed3f(x, 1.f, UNITS - 1.f);
       key[i] = l[i] > -INFINITY ? (n << ID_BITS) | (ID_MASK - e) : 0u;
     }
@@ -449,18 +456,20 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
   }
   // ---- the rounds, one more than k for the border: every lane's words in order, the largest first one is taken
   order_all<N>(key);
-  uint32_t mine = 0, last = 0;
+  uint32_t mine = 0, last = 0, gap = ~0u;  // gap: the smallest between two words in order
 #pragma unroll 1
   for (int r = 0; r <= a.k; ++r) {
-    const uint32_t best = max_of<L>(key[0]);
-    if (r > 0 && best && (last >> ID_BITS) - (best >> ID_BITS) <= tol) sure = false;
+    const uint32_t best = max_of<L>(key[0]), less = last - best;  // (the first round's wraps: it is no gap)
+    gap = best && r > 0 && less < gap ? less : gap;
     last = best;
-    if (j == r) mine = best;
+    mine = j == r ? best : mine;
     const uint32_t out = key[0] == best ? ~0u : 0u;  // (by masks: a choice between two places becomes a search for the index)
 #pragma unroll
-    for (int i = 0; i + 1 < N; ++i) key[i] = (out & key[i + 1]) | (~out & key[i]);
-    key[N - 1] &= ~out;
+    for (int i = 0; i + 1 < KEEP; ++i) key[i] = (out & key[i + 1]) | (~out & key[i]);
+    key[KEEP - 1] &= ~out;
   }
+  // (words of values tol apart differ by less than this)
+  if (gap < (tol + 1) << ID_BITS) sure = false;
   int id = mine ? (int)(ID_MASK - (mine & ID_MASK)) : -1;
   for (uint64_t again = __ballot(there && !sure && j == 0); __builtin_expect(again != 0, 0); again &= again - 1) {
     const int first = __builtin_ctzll(again);  // of the token's lanes
@@ -557,16 +566,17 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_back_kernel(ChooseArgs 
   }
 }
 
-// f(lanes of a token, experts of a lane)
+// f(lanes of a token, experts of a lane, words that a lane keeps)
 template <typename F>
 void by_width(const ChooseArgs& a, F&& f) {
   using std::integral_constant;
-  auto wave = [&](auto n) { f(integral_constant<int, 64>{}, n); };
-  auto rows = [&](auto n) { f(integral_constant<int, 16>{}, n); };
+  auto wave = [&](auto n) { f(integral_constant<int, 64>{}, n, n); };
+  auto rows = [&](auto n) { f(integral_constant<int, 16>{}, n, n); };
   if (a.E <= 256 && a.k <= 16) {
     if (a.E <= 64) rows(integral_constant<int, 4>{});
     else if (a.E <= 128) rows(integral_constant<int, 8>{});
-    else rows(integral_constant<int, 16>{});
+    else if (a.k > 8) rows(integral_constant<int, 16>{});
+    else f(integral_constant<int, 16>{}, integral_constant<int, 16>{}, integral_constant<int, 9>{});
   } else if (a.E <= 256) {
     wave(integral_constant<int, 4>{});
   } else if (a.E <= 512) {
@@ -583,14 +593,14 @@ unsigned choose_grid(const ChooseArgs& a, int lanes) {
 }  // namespace
 
 hipError_t launch_choose(const ChooseArgs& a, hipStream_t st) {
-  by_width(a, [&](auto l, auto n) {
-    choose_kernel<decltype(l)::value, decltype(n)::value><<<choose_grid(a, decltype(l)::value), CHOOSE_THREADS, 0, st>>>(a);
+  by_width(a, [&](auto l, auto n, auto keep) {
+    choose_kernel<decltype(l)::value, decltype(n)::value, decltype(keep)::value><<<choose_grid(a, decltype(l)::value), CHOOSE_THREADS, 0, st>>>(a);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_choose_back(const ChooseArgs& a, hipStream_t st) {
-  by_width(a, [&](auto l, auto n) {
+  by_width(a, [&](auto l, auto n, auto) {
     choose_back_kernel<decltype(l)::value, decltype(n)::value><<<choose_grid(a, decltype(l)::value), CHOOSE_THREADS, 0, st>>>(a);
   });
   return hipGetLastError();
