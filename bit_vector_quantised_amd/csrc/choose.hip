@@ -329,6 +329,7 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
     // All of it twice, for two values.
     near = ldexpf(most * (a.sigmoid ? 9.f + fmaxf(-top, 0.f) * 1.5f : 16.f) + b_most, -23);
     if (!(top > -INFINITY)) near = 0.f;
+    else if (a.sigmoid && top < -60.f) sure = false;  // (scores near and below fp32's smallest have no such errors)
     if (a.bias) {
 #pragma unroll
       for (int i = 0; i < N; ++i) v[i] += b[i];

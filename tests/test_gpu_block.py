@@ -416,6 +416,25 @@ def test_choose_tells_close_values_apart():
     assert torch.equal(ids.cpu().long(), want)
 
 
+def test_choose_scores_below_fp32():
+    """Scores and biases that are subnormal in fp32, or less, are ordered by their values all the same."""
+    say("choose: scores below fp32")
+    E, T = 64, 48
+    g = gen(17)
+    logits = torch.cat([0.5 * randn(g, T // 3, E) - 89.5, 8 * randn(g, T // 3, E) - 110, 2 * randn(g, T // 3, E) - 62])
+    # one score that fp32 may hold against a group whose scores it may not, of which two are more
+    for row, (one, many) in enumerate([(-87.2, -87.5), (-88.6, -88.75), (-88.0, -88.5)]):
+        logits[row] = -97.0 - torch.arange(E) / 16
+        logits[row, 0], logits[row, 8], logits[row, 9] = one, many, many + 0.01
+    for bias in (None, 1e-40 * randn(g, E), torch.zeros(E)):
+        for kw in (dict(), dict(groups=8, top_groups=1), dict(groups=8, top_groups=3)):
+            choice = make(E, 8, "sigmoid", bias=None if bias is None else bias.cuda(), **kw)
+            ids, w = choice.forward(logits.cuda())
+            want, ww, rel = ref.choose64(logits, bias, 8, "sigmoid", **{"top_groups": kw.get("groups", 1), **kw})
+            assert torch.equal(ids.cpu().long(), want)
+            dense_ref.check(w, ww, rel * ww.abs(), "w")
+
+
 def test_choose_infinities():
     say("choose: infinities")
     E = 70
