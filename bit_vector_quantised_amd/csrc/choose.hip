@@ -166,14 +166,15 @@ __device__ __forceinline__ void order_all(uint32_t* k) {
   });
 }
 
-// ---- A token by the whole wave in 64 bits: expert e = lane + 64 i in entry i.  Hardly any token comes here, but a
-// wave that does is the last of its launch (of 16384 tokens among 256 experts some 40 do).
+// ---- A token by the whole wave in 64 bits: experts N lane .. N lane + N - 1 in a lane.  Hardly any token comes here, but
+// a wave that does is the last of its launch (of 16384 tokens among 256 experts some 40 do; 5 us with an entry's exponential
+// after another's and groups by a scan of LDS, this way 4).
 
 template <int CTRL>
-__device__ __forceinline__ double max_with(double v) {
+__device__ __forceinline__ double dpp_f64(double v) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
   const uint32_t lo = (uint32_t)dpp_i32<CTRL>((int)(uint32_t)u), hi = (uint32_t)dpp_i32<CTRL>((int)(u >> 32));
-  return fmax(v, __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 __device__ __forceinline__ double lane_f64(double v, int lane) {
   const uint64_t u = __builtin_bit_cast(uint64_t, v);
@@ -181,84 +182,93 @@ __device__ __forceinline__ double lane_f64(double v, int lane) {
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 __device__ __forceinline__ double wave_max64(double v) {
-  v = max_with<dpp::QUAD_XOR1>(v);
-  v = max_with<dpp::QUAD_XOR2>(v);
-  v = max_with<dpp::ROW_HALF_MIRROR>(v);
-  v = max_with<dpp::ROW_MIRROR>(v);
+  v = fmax(v, dpp_f64<dpp::QUAD_XOR1>(v));
+  v = fmax(v, dpp_f64<dpp::QUAD_XOR2>(v));
+  v = fmax(v, dpp_f64<dpp::ROW_HALF_MIRROR>(v));
+  v = fmax(v, dpp_f64<dpp::ROW_MIRROR>(v));
   return fmax(fmax(lane_f64(v, 0), lane_f64(v, 16)), fmax(lane_f64(v, 32), lane_f64(v, 48)));
 }
+// The larger two of both pairs (m1 >= m2).
+__device__ __forceinline__ void two_of(double& m1, double& m2, double o1, double o2) {
+  m2 = fmax(fmin(m1, o1), fmax(m2, o2));
+  m1 = fmax(m1, o1);
+}
+template <int CTRL>
+__device__ __forceinline__ void two_best(double& m1, double& m2) { two_of(m1, m2, dpp_f64<CTRL>(m1), dpp_f64<CTRL>(m2)); }
 
 // The entry with the largest of v over the wave (of equal ones the lowest expert), which is set to -inf; -1 if all are.
 template <int N>
-__device__ __forceinline__ int take_best(double* v, int lane, double& best) {
-  best = v[0];
+__device__ __forceinline__ int take_best(double* v, int lane) {
+  double most = v[0];
+  int at = 0;
 #pragma unroll
-  for (int i = 1; i < N; ++i) best = fmax(best, v[i]);
-  best = wave_max64(best);
-  int id = -1;
-#pragma unroll
-  for (int i = N - 1; i >= 0; --i) {
-    const uint64_t m = __ballot(v[i] == best);
-    id = m ? 64 * i + __builtin_ctzll(m) : id;
+  for (int i = 1; i < N; ++i) {
+    at = v[i] > most ? i : at;
+    most = fmax(most, v[i]);
   }
+  const double best = wave_max64(most);
   if (!(best > -INFINITY)) return -1;
+  const int first = __builtin_ctzll(__ballot(most == best));
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = id == lane + 64 * i ? -INFINITY : v[i];
-  return id;
+  for (int i = 0; i < N; ++i) v[i] = lane == first && at == i ? -INFINITY : v[i];
+  return first * N + __builtin_amdgcn_readlane(at, first);
 }
 
 // Place j's expert in lane j (-1: none).  room: the wave's LDS, 64 N values.
 template <int N>
 __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, float top, double* room) {
   const double NONE = -INFINITY;
-  float l[N];
+  float l[N], b[N];
   double v[N], sum = 0;
   const bool groups = a.top_groups < a.groups;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int e = lane + 64 * i, at = e < a.E ? e : 0;
-    const float x = a.logits[(size_t)t * a.E + at], b = a.bias ? a.bias[at] : 0.f;
-    l[i] = e < a.E && x > -INFINITY && b > -INFINITY ? x : -INFINITY;
+    const int e = lane * N + i, at = e < a.E ? e : 0;
+    const float x = a.logits[(size_t)t * a.E + at];
+    b[i] = a.bias ? a.bias[at] : 0.f;
+    l[i] = e < a.E && x > -INFINITY && b[i] > -INFINITY ? x : -INFINITY;
     v[i] = l[i];
   }
   if (a.bias || groups) {
+    // (both scores by the same exponentials, so that the entries' chains of steps run side by side)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (a.sigmoid) v[i] = 1.0 / (1.0 + exp(-(double)l[i]));
-      else v[i] = l[i] == top ? 1.0 : exp((double)l[i] - top);
-      if (l[i] == -INFINITY) v[i] = 0.0;
-      sum += v[i];
-    }
-    if (!a.sigmoid) {
+    for (int i = 0; i < N; ++i) v[i] = exp(a.sigmoid ? -(double)l[i] : (l[i] == top ? 0.0 : (double)l[i] - top));
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = 1.0 / (1.0 + v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) sum += l[i] == -INFINITY ? 0.0 : v[i];
 #pragma unroll
       for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] /= sum;
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 64 * i;
-      if (!a.sigmoid) v[i] /= sum;
-      if (a.bias) v[i] += (double)a.bias[e < a.E ? e : 0];
-      if (l[i] == -INFINITY) v[i] = NONE;
-    }
+    for (int i = 0; i < N; ++i) v[i] = l[i] == -INFINITY ? NONE : v[i] + (double)b[i];
   }
-  double best;
   if (groups) {
-    const int size = a.E / a.groups;
-    // lane g: the value of group g by a scan (its two best by exchanges, one group after the other: 8 us of a launch
-    // instead of 1), and its rank among the groups
-#pragma unroll
-    for (int i = 0; i < N; ++i) room[lane + 64 * i] = v[i];
-    lds_turn();
+    const int size = a.E / a.groups, w = size / N;  // w: lanes of a group
     double m1 = NONE, m2 = NONE;
-    if (lane < a.groups) {
-      const double* from = room + lane * size;
-#pragma unroll 8
-      for (int c = 0; c < size; ++c) {
-        const int at = c + lane < size ? c + lane : c + lane - size;  // (lanes start apart, so that their reads meet other banks)
-        const double x = from[lane < size ? at : c];
-        m2 = fmax(m2, fmin(m1, x));
-        m1 = fmax(m1, x);
+    // lane g: the two best of group g
+    if (size % N == 0 && w <= 16 && (w & (w - 1)) == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) two_of(m1, m2, v[i], NONE);
+      if (w >= 2) two_best<dpp::QUAD_XOR1>(m1, m2);
+      if (w >= 4) two_best<dpp::QUAD_XOR2>(m1, m2);
+      if (w >= 8) two_best<dpp::ROW_HALF_MIRROR>(m1, m2);
+      if (w >= 16) two_best<dpp::ROW_MIRROR>(m1, m2);
+      m1 = __shfl(m1, lane * w & 63);
+      m2 = __shfl(m2, lane * w & 63);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) room[lane * N + i] = v[i];
+      lds_turn();
+      if (lane < a.groups) {
+#pragma unroll 4
+        for (int c = 0; c < size; ++c) two_of(m1, m2, room[lane * size + c], NONE);
       }
+      lds_turn();
     }
     const double of = a.best > 1 && m2 > NONE ? m1 + m2 : m1;
     int rank = 0;
@@ -268,17 +278,16 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
       rank += o > of || (o == of && g < lane) ? 1 : 0;
     }
     const uint64_t taken = __ballot(lane < a.groups && rank < a.top_groups);
-    lds_turn();
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const bool on = l[i] > -INFINITY && ((taken >> ((lane + 64 * i) / size)) & 1);
+      const bool on = l[i] > -INFINITY && ((taken >> ((lane * N + i) / size)) & 1);
       v[i] = !on ? NONE : (a.bias ? v[i] : (double)l[i]);
     }
   }
   int mine = -1;
 #pragma unroll 1
   for (int r = 0; r < a.k; ++r) {
-    const int id = take_best<N>(v, lane, best);
+    const int id = take_best<N>(v, lane);
     mine = lane == r ? id : mine;
   }
   return mine;
@@ -286,7 +295,7 @@ __device__ __forceinline__ int choose64(const ChooseArgs& a, int t, int lane, fl
 
 // The choice: 64 / L tokens of a wave side by side, N experts in a lane: what goes over a token's lanes is shared by
 // four tokens (a token to a wave with its rounds over 64-bit words: 92 us for 16384 tokens among 256 experts in 8 groups
-// with biases, this way 17, of which the last 5 are waves with a token for 64 bits; 65536 tokens 38 us, some 350
+// with biases, this way 16, of which the last 4 are waves with a token for 64 bits; 65536 tokens 36 us, some 350
 // instructions a token, where their logits alone take 14; one token 5.1).  Values become whole numbers of
 // BITS bits over their range with the expert's number below them, so that a round of the choice is a maximum of 32-bit
 // words that are all different, and ties fall to the lower expert.
