@@ -54,7 +54,7 @@ struct LinearPlan {
   } fwd, dx, dw;
   bool few;                  // forward by the few-rows kernel, unless rows are in a table
   int split_bias;            // parts of a group's rows in the sums of dbias
-  size_t xp, wp, dz, bias_part, part, total;
+  size_t xp, wp, dz, bias_part, part, dw_part, total;
 };
 // kept8: with room for x from 8 bits
 LinearPlan linear_plan(const moe_vq_linear* L, int n_rows, bool backward, bool kept8 = false);

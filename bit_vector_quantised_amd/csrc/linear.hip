@@ -7,7 +7,7 @@
 //   dx        dx = dz W                                contraction over the weight rows R
 //   dw        dW_g = dz_g^T x_g                        contraction over the group's rows
 //
-// One kernel does the three products.  It is bound by the matrix cores once a tile's
+// One kernel does the three products, and another dx and dw side by side if they are small.  It is bound by the matrix cores once a tile's
 // operands come from LDS often enough: a BM x BN tile moves (BM + BN) * 128 bytes through
 // LDS for BM * BN * 128 / size products.  What differs is how an operand lies in memory:
 //   "along"   the contraction runs along its rows (x and W forward, dz for dx)
@@ -269,8 +269,11 @@ struct Operand {
   }
 };
 
+// Workgroup `block` of a product; lds_mem: tile_bytes of LDS.
+constexpr int tile_bytes(int BM, int BN, int NS) { return NS * (BM + BN) * STEP_BYTES; }
+
 template <typename E, int BM, int BN, int WM, int WN, int NS, int MODE>
-__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs& g, int block, char* lds_mem) {
   constexpr int NW = WM * WN;
   constexpr int FM = BM / WM / 16, FN = BN / WN / 16;
   using OpA = Operand<E, BM, MODE != GEMM_DW, NW>;
@@ -279,7 +282,6 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   using OpB = Operand<E, BN, FORWARD, NW>;
   constexpr int KT = OpA::KT;
   constexpr int STAGE = (BM + BN) * STEP_BYTES;
-  __shared__ __align__(1024) char lds_mem[NS * STAGE];
   lds_char* lds = (lds_char*)lds_mem;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -295,7 +297,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     // groups' 8192 rows, dw of 4096 x 7168 each 663 us, so 597; 16384 rows, 7168 x 2048 677 and 503.  XCDs that
     // begin with different groups: 604, but 32 groups' 32768 rows 2210 instead of 2090.)
     const int mt = (g.out_m + BM - 1) / BM, tiles = mt * nt, per = (tiles + 7) / 8;
-    const int x = blockIdx.x & 7, q = blockIdx.x >> 3, all = q / per;
+    const int x = block & 7, q = block >> 3, all = q / per;
     split = all / g.G;
     grp = all - split * g.G;
     const int eighth = (x + grp) & 7, id = eighth * per + q - all * per;
@@ -323,14 +325,14 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     if constexpr (HALVES_AT_END) {
       // xcd_order, with the tiles of an XCD's last round, if they are half a round or less, as two halves of their rows (16
       // groups' 8192 rows, 7168 -> 4096, even 601 us forward, so 558, uneven 564 and 537, their dx 600 and 589)
-      const int x = blockIdx.x & 7, q = blockIdx.x >> 3, mine = (tiles >> 3) + (x < (tiles & 7) ? 1 : 0);
+      const int x = block & 7, q = block >> 3, mine = (tiles >> 3) + (x < (tiles & 7) ? 1 : 0);
       const int whole = mine & ~31, rest = mine - whole <= 16 ? mine - whole : 0, full = mine - rest;
       if (q >= full + 2 * rest) return;  // (the grid is an upper bound)
       half = q < full ? 0 : 1 + ((q - full) & 1);
       bid = x * (tiles >> 3) + (x < (tiles & 7) ? x : (tiles & 7)) + (q < full ? q : full + ((q - full) >> 1));
     } else {
-      if ((int)blockIdx.x >= tiles * g.splits) return;  // (the grid is an upper bound)
-      bid = xcd_order(blockIdx.x, tiles * g.splits);
+      if (block >= tiles * g.splits) return;  // (the grid is an upper bound)
+      bid = xcd_order(block, tiles * g.splits);
     }
     split = bid / tiles;
     const int id = bid - split * tiles, row_tile = id / nt;
@@ -481,7 +483,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
   // rows leave in long runs.  Two parts take turns, so one can fill while the other is read.
   constexpr int PITCH = FN * 16 + 4;
   constexpr int COLS = GATED ? FN * 8 : FN * 16;  // output columns of the wave
-  static_assert(NW * 2 * 16 * PITCH * 4 <= (int)sizeof(lds_mem), "output staging");
+  static_assert(NW * 2 * 16 * PITCH * 4 <= tile_bytes(BM, BN, NS), "output staging");
   // The largest tiles' outputs exceed the L2s many times over: streamed, dw of 16 experts' 512 rows each
   // takes 779 us instead of 924, and at 8192^3 dx gains 9 % and dw 9 %.
   constexpr bool STREAM = BM * BN >= 256 * 256;
@@ -534,6 +536,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
     for (int t = 0; t < 16 * COLS / 8; t += 64)
       if (16 * COLS / 8 >= 64 || lane < 16 * COLS / 8) put(part, i, t + lane);
   });
+}
+
+template <typename E, int BM, int BN, int WM, int WN, int NS, int MODE>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmArgs g) {
+  __shared__ __align__(1024) char lds[tile_bytes(BM, BN, NS)];
+  gemm_tile<E, BM, BN, WM, WN, NS, MODE>(g, blockIdx.x, lds);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -642,9 +650,9 @@ __device__ __forceinline__ int group_of(const GemmArgs& g, int m) {
 // The sum of the splits' parts in order, then the epilogue: eight columns per thread.  ROWS: of forward or dx,
 // whose rows in no group have no sums and are left as they were.
 template <bool GATED, bool ROWS>
-__global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
+__device__ __forceinline__ void split_sum(const GemmArgs& g, int rows, unsigned block) {
   const int units = (g.ldo + 7) / 8;
-  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const size_t at = (size_t)block * 256 + threadIdx.x;
   if (at >= (size_t)rows * units) return;
   const size_t m = at / units;
   const int n = (int)(at - m * units) * 8, left = g.ldo - n;
@@ -668,6 +676,15 @@ __global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
     }
   }
   epilogue8<GATED>(g, grp, m, n, v, u);
+}
+template <bool GATED, bool ROWS>
+__global__ __launch_bounds__(256) void split_sum_kernel(GemmArgs g, int rows) {
+  split_sum<GATED, ROWS>(g, rows, blockIdx.x);
+}
+// The sums of both gradients: n_dx workgroups, and the rest.
+__global__ __launch_bounds__(256) void gradients_sum_kernel(GemmArgs dx, GemmArgs dw, unsigned n_dx) {
+  if (blockIdx.x < n_dx) split_sum<false, true>(dx, dx.M, blockIdx.x);
+  else split_sum<false, false>(dw, dw.G * dw.out_m, blockIdx.x - n_dx);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -838,10 +855,9 @@ __global__ __launch_bounds__(DZ_TX* DZ_TY) void dz_kernel(DzArgs a) {
 }
 
 // The splits' column sums added up: 32 columns by 8 shares of the splits per workgroup, the shares in order.
-__global__ __launch_bounds__(256) void bias_sum_kernel(const float* part, float* out, int n, int splits) {
-  __shared__ float red[8][32];
+__device__ __forceinline__ void bias_sum(const float* part, float* out, int n, int splits, int block, float (*red)[32]) {
   const int c = threadIdx.x & 31, share = threadIdx.x >> 5;
-  const int i = blockIdx.x * 32 + c;
+  const int i = block * 32 + c;
   const int per = (splits + 7) / 8, q0 = share * per, q1 = q0 + per < splits ? q0 + per : splits;
   float s = 0.f;
   if (i < n) {
@@ -857,9 +873,38 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(const float* part, float*
     out[i] = t;
   }
 }
+struct BiasSum {
+  const float* part;
+  float* out;
+  int n, splits;
+};
+__global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum b) {
+  __shared__ float red[8][32];
+  bias_sum(b.part, b.out, b.n, b.splits, blockIdx.x, red);
+}
+
+// Small gradients, whose products leave CUs idle: dx, dw and the sum of the bias parts side by side in one launch, of
+// n_dx (a multiple of 8, for the order of the XCDs) and n_dw workgroups and the rest.  With dz, one after the other and
+// side by side: 515 rows of 1000 -> 333 in fp32 33 us, so 25; bf16 64 rows of 512 -> 512 18 and 13, 512 of 2048 -> 2048
+// 43 and 29, 2048 of 2048 -> 2048 82 and 53.  Nothing of some 30 sizes takes longer.
+constexpr int stages_of(int side) { return side == 64 ? 4 : 2; }
+
+template <typename E, int DX, int DW>
+__global__ __launch_bounds__(256) void gradients_kernel(GemmArgs dx, GemmArgs dw, BiasSum b, int n_dx, int n_dw) {
+  constexpr int BYTES = tile_bytes(DX, DX, stages_of(DX));
+  static_assert(tile_bytes(DW, DW, stages_of(DW)) == BYTES, "either tile takes as much LDS");
+  __shared__ __align__(1024) char lds[BYTES];
+  const int block = blockIdx.x;
+  if (block < n_dx) gemm_tile<E, DX, DX, 2, 2, stages_of(DX), GEMM_DX>(dx, block, lds);
+  else if (block < n_dx + n_dw) gemm_tile<E, DW, DW, 2, 2, stages_of(DW), GEMM_DW>(dw, block - n_dx, lds);
+  else bias_sum(b.part, b.out, b.n, b.splits, block - n_dx - n_dw, reinterpret_cast<float(*)[32]>(lds));
+}
 
 using Cut = LinearPlan::Cut;
 constexpr int CUS = 256;
+// Products of more workgroups in all are made one after the other: the ends of the two count ever less (fp32 at 4096^3,
+// 2048 workgroups, 1965 us, side by side 1971; 4096 x 2048 x 2048 555 and 549).
+constexpr long GRADIENTS_TOGETHER = 16 * CUS;
 
 // A kind of tile: its side, how many workgroups of it a CU holds, and what a workgroup takes (microseconds,
 // measured): per contraction step with its CU full, per step if it has the CU to itself, and before
@@ -905,16 +950,29 @@ Cut pick_cut(int dtype, long rows, long groups, long cols, int steps, bool forwa
 
 int div_up(long a, long b) { return (int)((a + b - 1) / b); }
 
-template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS>
-void gemm_go(const GemmArgs& g, hipStream_t st) {
+template <int MODE>
+long gemm_grid(const GemmArgs& g, int BM, int BN) {
   const int per_n = MODE == GEMM_GATED ? BN / 2 : BN;
   const long nt = div_up(g.out_n, per_n);
   // (each group of rows adds at most one partial row tile)
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
   const long grid = MODE == GEMM_DW ? (nt * div_up(g.out_m, BM) + 7) / 8 * 8 * g.G * g.splits : nt * mt * g.splits;
-  const long more = MODE != GEMM_DW && BM * BN >= 256 * 256 ? 8 * 17 : 0;  // (an XCD's last 16 tiles in halves)
-  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)(grid + more), 64 * WM * WN, 0, st>>>(g);
+  const long more = grid > 0 && MODE != GEMM_DW && BM * BN >= 256 * 256 ? 8 * 17 : 0;  // (an XCD's last 16 tiles in halves)
+  return grid + more;
+}
+
+template <typename E, int MODE, int BM, int BN, int WM, int WN, int NS>
+void gemm_go(const GemmArgs& g, hipStream_t st) {
+  const long grid = gemm_grid<MODE>(g, BM, BN);
+  if (grid > 0) gemm_kernel<E, BM, BN, WM, WN, NS, MODE><<<(unsigned)grid, 64 * WM * WN, 0, st>>>(g);
+}
+
+// Workgroups of the sum of a product's parts (0: it was not split).
+template <int MODE>
+unsigned split_sum_grid(const GemmArgs& g) {
+  const int rows = MODE == GEMM_DW ? g.G * g.out_m : g.M;
+  return g.splits > 1 ? (unsigned)(((size_t)rows * ((g.ldo + 7) / 8) + 255) / 256) : 0;
 }
 
 template <int MODE>
@@ -927,11 +985,30 @@ hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t s
     if (tile == 128) gemm_go<F32, MODE, 128, 128, 2, 2, 2>(g, st);
     else gemm_go<F32, MODE, 64, 64, 2, 2, 4>(g, st);
   }
-  if (g.splits > 1) {
-    const int rows = MODE == GEMM_DW ? g.G * g.out_m : g.M;
-    const size_t n = (size_t)rows * ((g.ldo + 7) / 8);
-    split_sum_kernel<MODE == GEMM_GATED, MODE != GEMM_DW><<<(unsigned)((n + 255) / 256), 256, 0, st>>>(g, rows);
-  }
+  const unsigned sums = split_sum_grid<MODE>(g);
+  if (sums) split_sum_kernel<MODE == GEMM_GATED, MODE != GEMM_DW><<<sums, 256, 0, st>>>(g, MODE == GEMM_DW ? g.G * g.out_m : g.M);
+  return hipGetLastError();
+}
+
+// Both products and the bias parts' sum (b.n 0: none) in one launch, what was split summed up in another.
+hipError_t launch_gradients(const LinearPlan& p, const GemmArgs& dx, const GemmArgs& dw, const BiasSum& b, hipStream_t st) {
+  const int n_dx = (int)((gemm_grid<GEMM_DX>(dx, p.dx.tile, p.dx.tile) + 7) / 8 * 8), n_dw = (int)gemm_grid<GEMM_DW>(dw, p.dw.tile, p.dw.tile);
+  auto go = [&](auto e, auto side_dx, auto side_dw) {
+    gradients_kernel<decltype(e), decltype(side_dx)::value, decltype(side_dw)::value>
+        <<<(unsigned)(n_dx + n_dw + div_up(b.n, 32)), 256, 0, st>>>(dx, dw, b, n_dx, n_dw);
+  };
+  auto sides = [&](auto e) {
+    using S = std::integral_constant<int, 64>;
+    using L = std::integral_constant<int, 128>;
+    if (p.dx.tile == 64 && p.dw.tile == 64) go(e, S{}, S{});
+    else if (p.dx.tile == 64) go(e, S{}, L{});
+    else if (p.dw.tile == 64) go(e, L{}, S{});
+    else go(e, L{}, L{});
+  };
+  if (p.dtype == MOE_VQ_BF16) sides(Bf16{});
+  else sides(F32{});
+  const unsigned sum_dx = split_sum_grid<GEMM_DX>(dx), sum_dw = split_sum_grid<GEMM_DW>(dw);
+  if (sum_dx + sum_dw) gradients_sum_kernel<<<sum_dx + sum_dw, 256, 0, st>>>(dx, dw, sum_dx);
   return hipGetLastError();
 }
 
@@ -1033,15 +1110,11 @@ static LinearPlan plan_of(const moe_vq_linear* L, int n_rows, bool backward, boo
     const long strips = (long)div_up(p.N, DZ_TX * 8) * p.G, want = 2048 / strips, can = div_up(p.M, DZ_TY * p.G);
     p.split_bias = (int)(want < 1 || can < 1 ? 1 : (want < can ? want : can));
     p.bias_part = take(p.split_bias > 1 ? (size_t)p.split_bias * p.G * p.R * 4 : 0);
-    if (bound) {
-      part = most(p.M, p.K);
-      const size_t dw = most((size_t)p.G * p.R, p.K);
-      part = part > dw ? part : dw;
-    } else {
-      part = p.dx.splits > 1 ? (size_t)p.dx.splits * p.M * p.K * 4 : 0;
-      const size_t dw = p.dw.splits > 1 ? (size_t)p.dw.splits * p.G * p.R * p.K * 4 : 0;
-      part = part > dw ? part : dw;
-    }
+    // (dx and dw may be made side by side: their parts lie apart)
+    const size_t dx = bound ? most(p.M, p.K) : (p.dx.splits > 1 ? (size_t)p.dx.splits * p.M * p.K * 4 : 0);
+    const size_t dw = bound ? most((size_t)p.G * p.R, p.K) : (p.dw.splits > 1 ? (size_t)p.dw.splits * p.G * p.R * p.K * 4 : 0);
+    p.dw_part = take(dw);
+    part = dx;
   }
   p.part = take(part);
   p.total = off < 256 ? 256 : off;
@@ -1091,11 +1164,21 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
                                        : launch_gemm<GEMM_FWD>(p, g, p.fwd.tile, st);
 }
 
+// Whether one launch makes both products: of small tiles, dw not over the weights that dx reads.
+static bool gradients_together(const LinearPlan& p, const LinearCall& c, const GemmArgs& dx, const GemmArgs& dw) {
+  if (!c.dx || !c.dw || p.M == 0 || p.dx.tile > 128 || p.dw.tile > 128) return false;
+  const size_t bytes = (size_t)p.G * p.R * p.K * p.size;
+  const char *w = dx.b, *to = static_cast<const char*>(c.dw);
+  if (!p.pack_k && w < to + bytes && to < w + bytes) return false;
+  return gemm_grid<GEMM_DX>(dx, p.dx.tile, p.dx.tile) + gemm_grid<GEMM_DW>(dw, p.dw.tile, p.dw.tile) <= GRADIENTS_TOGETHER;
+}
+
 hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipStream_t st) {
   // dz: dy itself where nothing changes it
   const bool same = c.L->act == MOE_VQ_ACT_NONE && c.y_dtype == p.dtype && p.Rp == p.R;
   const bool need_dz = (c.dx || c.dw) && !same;
   const void* dz = same ? c.dy : at<void>(c.ws, p.dz);
+  BiasSum sum{};
   if (need_dz || c.dbias) {
     DzArgs d{};
     d.dy = c.dy; d.z = c.z; d.z8 = c.z8;
@@ -1106,8 +1189,7 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     d.M = p.M; d.N = p.N; d.R = p.R; d.G = p.G; d.pitch = p.Rp;
     d.lim = c.L->swiglu_limit;
     launch_dz(p, d, c.y_dtype, c.L->act, st);
-    if (c.dbias && d.splits > 1)
-      bias_sum_kernel<<<div_up((long)p.G * p.R, 32), 256, 0, st>>>(d.bias, c.dbias, p.G * p.R, d.splits);
+    if (c.dbias && d.splits > 1) sum = {d.bias, c.dbias, p.G * p.R, d.splits};
   }
   const void* x = c.x;
   const void* w = c.L->w;
@@ -1134,22 +1216,23 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
   g.part = at<float>(c.ws, p.part);
   g.out_n = g.ldo = p.K;
   g.out_dtype = p.dtype;
+  GemmArgs gx = g, gw = g;
+  gx.b = static_cast<const char*>(w);
+  gx.kc = p.R;
+  gx.out = c.dx;
+  gx.splits = p.dx.splits;
+  gw.b = static_cast<const char*>(x);
+  gw.out_m = p.R;
+  gw.out = c.dw;
+  gw.splits = p.dw.splits;
+  gw.part = at<float>(c.ws, p.dw_part);
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && c.dx && p.M > 0) {
-    g.b = static_cast<const char*>(w);
-    g.kc = p.R;
-    g.out = c.dx;
-    g.splits = p.dx.splits;
-    e = launch_gemm<GEMM_DX>(p, g, p.dx.tile, st);
-  }
-  if (e == hipSuccess && c.dw) {
-    g.b = static_cast<const char*>(x);
-    g.out_m = p.R;
-    g.out = c.dw;
-    g.splits = p.dw.splits;
-    e = launch_gemm<GEMM_DW>(p, g, p.dw.tile, st);
-  }
-  return e;
+  if (e != hipSuccess) return e;
+  if (gradients_together(p, c, gx, gw)) return launch_gradients(p, gx, gw, sum, st);
+  if (sum.n) bias_sum_kernel<<<div_up(sum.n, 32), 256, 0, st>>>(sum);
+  if (c.dx && p.M > 0) e = launch_gemm<GEMM_DX>(p, gx, p.dx.tile, st);
+  if (e == hipSuccess && c.dw) e = launch_gemm<GEMM_DW>(p, gw, p.dw.tile, st);
+  return e == hipSuccess ? hipGetLastError() : e;
 }
 
 }  // namespace mvq

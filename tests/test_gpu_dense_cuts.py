@@ -86,3 +86,38 @@ def test_fewer_rows_on_one_workspace(dtype, K, N):
         for name, got in (("dx", dx), ("dw", dw), ("dbias", db)):
             ref.check(got, *want[name], f"{name} of {m} rows")
         assert (big[lin.ws_bytes:] == 0xA5).all(), m
+
+
+@pytest.mark.parametrize("M,K,N,start,act,dtype", [  # dx, dw
+    (515, 1000, 333, None, "gelu", F32),             # 64 x 1, 64 x 2
+    (64, 512, 512, None, "silu", BF16),              # 64 x 1, 64 x 1
+    (700, 1000, 700, [0, 3, 3, 690], "silu", F32),   # 64, 64, rows behind the groups
+    (1000, 1024, 1024, None, "gelu", F32),           # both in parts
+    (2048, 2048, 2048, None, "silu", BF16),          # 128, in parts
+    (3000, 1500, 1500, [0, 1201, 1201, 2990], "silu", F32),  # 64 x 1, 128 x 1
+    (300, 2056, 600, [0, 17, 300], "gelu", BF16),    # 64 x 1, 128 x 1
+    (5000, 700, 300, [7, 9, 4990], "silu", BF16),    # 128 x 1, 64 x 8
+    (5000, 700, 300, None, "gelu", F32),             # 128 x 1, 64 x 4
+    (4000, 4000, 2000, None, "silu", F32),           # 128 x 1, 128 x 1
+    (5000, 520, 520, [7, 9, 4990], "silu", BF16),    # 128 x 1, 128 x 4
+])
+def test_gradients_together_and_alone(M, K, N, start, act, dtype):
+    """dx, dw and dbias of one call are those of a call for each, to the bit; dw over the weights too."""
+    say(f"gradients together {M} {K} {N} {start} {act}")
+    g, R, x, w, b, _ = linear_inputs(M, K, N, start, act, dtype, dtype, True, False)
+    x, w, z, dy = x.cuda(), w.cuda(), randn(g, M, R, dtype=dtype).cuda(), randn(g, M, N, dtype=dtype).cuda()
+    gs = None if start is None else torch.tensor(start, dtype=torch.int32, device="cuda")
+
+    def grads(names, weights=w):
+        out = {"dx": torch.full((M, K), -3.0, dtype=dtype, device="cuda"), "dw": torch.zeros_like(w), "dbias": torch.zeros_like(b, device="cuda")}
+        if weights is not w:
+            out["dw"] = weights
+        lin = Linear(weights, b.cuda(), act=act, max_rows=M, backward=True)
+        lin.ws.fill_(255)
+        lin.backward(x, dy, z, gs, **{n: out[n] for n in names})
+        return [out[n].clone() for n in names]
+
+    alone = grads(["dx"]) + grads(["dw"]) + grads(["dbias"])
+    for got in (grads(["dx", "dw", "dbias"]), grads(["dx", "dw"]), grads(["dx", "dw", "dbias"], w.clone())):
+        for a, c in zip(got, alone):
+            assert torch.equal(a, c)
