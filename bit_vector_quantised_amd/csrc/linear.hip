@@ -883,20 +883,20 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum b) {
   bias_sum(b.part, b.out, b.n, b.splits, blockIdx.x, red);
 }
 
-// Small gradients, whose products leave CUs idle: dx, dw and the sum of the bias parts side by side in one launch, of
-// n_dx (a multiple of 8, for the order of the XCDs) and n_dw workgroups and the rest.  With dz, one after the other and
+// Small gradients, whose products leave CUs idle: dx, dw and the sum of the bias parts side by side in one launch, n_dx
+// workgroups from x0 on, n_dw from w0 on (all multiples of 8, for the order of the XCDs) and the rest.  With dz, one after the other and
 // side by side: 515 rows of 1000 -> 333 in fp32 33 us, so 25; bf16 64 rows of 512 -> 512 18 and 13, 512 of 2048 -> 2048
 // 43 and 29, 2048 of 2048 -> 2048 82 and 53.  Nothing of some 30 sizes takes longer.
 constexpr int stages_of(int side) { return side == 64 ? 4 : 2; }
 
 template <typename E, int DX, int DW>
-__global__ __launch_bounds__(256) void gradients_kernel(GemmArgs dx, GemmArgs dw, BiasSum b, int n_dx, int n_dw) {
+__global__ __launch_bounds__(256) void gradients_kernel(GemmArgs dx, GemmArgs dw, BiasSum b, int x0, int n_dx, int w0, int n_dw) {
   constexpr int BYTES = tile_bytes(DX, DX, stages_of(DX));
   static_assert(tile_bytes(DW, DW, stages_of(DW)) == BYTES, "either tile takes as much LDS");
   __shared__ __align__(1024) char lds[BYTES];
   const int block = blockIdx.x;
-  if (block < n_dx) gemm_tile<E, DX, DX, 2, 2, stages_of(DX), GEMM_DX>(dx, block, lds);
-  else if (block < n_dx + n_dw) gemm_tile<E, DW, DW, 2, 2, stages_of(DW), GEMM_DW>(dw, block - n_dx, lds);
+  if (block >= x0 && block < x0 + n_dx) gemm_tile<E, DX, DX, 2, 2, stages_of(DX), GEMM_DX>(dx, block - x0, lds);
+  else if (block >= w0 && block < w0 + n_dw) gemm_tile<E, DW, DW, 2, 2, stages_of(DW), GEMM_DW>(dw, block - w0, lds);
   else bias_sum(b.part, b.out, b.n, b.splits, block - n_dx - n_dw, reinterpret_cast<float(*)[32]>(lds));
 }
 
@@ -993,9 +993,17 @@ hipError_t launch_gemm(const LinearPlan& p, GemmArgs& g, int tile, hipStream_t s
 // Both products and the bias parts' sum (b.n 0: none) in one launch, what was split summed up in another.
 hipError_t launch_gradients(const LinearPlan& p, const GemmArgs& dx, const GemmArgs& dw, const BiasSum& b, hipStream_t st) {
   const int n_dx = (int)((gemm_grid<GEMM_DX>(dx, p.dx.tile, p.dx.tile) + 7) / 8 * 8), n_dw = (int)gemm_grid<GEMM_DW>(dw, p.dw.tile, p.dw.tile);
+  // More than the device holds at once: the product with the longer tiles first, which leaves the shorter ones for the end
+  // (fp32 2048 rows of 7168 -> 256 149 us with dx first, so 135, bf16 3000 of 2048 -> 2048 90 and 81; within one round it
+  // costs 0.3).
+  auto tile_time = [&](const Cut& c, int rows) {
+    return (float)c.tile * c.tile * div_up(div_up(rows, STEP_BYTES / p.size), c.splits);
+  };
+  const bool dw_first = n_dx + n_dw > 2 * CUS && tile_time(p.dw, div_up(p.M, p.G)) > tile_time(p.dx, p.R);
+  const int x0 = dw_first ? n_dw : 0, w0 = dw_first ? 0 : n_dx;
   auto go = [&](auto e, auto side_dx, auto side_dw) {
     gradients_kernel<decltype(e), decltype(side_dx)::value, decltype(side_dw)::value>
-        <<<(unsigned)(n_dx + n_dw + div_up(b.n, 32)), 256, 0, st>>>(dx, dw, b, n_dx, n_dw);
+        <<<(unsigned)(n_dx + n_dw + div_up(b.n, 32)), 256, 0, st>>>(dx, dw, b, x0, n_dx, w0, n_dw);
   };
   auto sides = [&](auto e) {
     using S = std::integral_constant<int, 64>;
