@@ -1207,7 +1207,8 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
     r.y = at<void>(c.ws, p.xp);
     r.start = c.group_start; r.G = p.G;
     r.M = p.M; r.C = p.K; r.pitch = p.Kp;
-    if (p.M > 0) launch_rows8_unpack(r, p.dtype, st);
+    // (its status takes what the launches before it left)
+    if (const hipError_t e = p.M > 0 ? launch_rows8_unpack(r, p.dtype, st) : hipSuccess; e != hipSuccess) return e;
     x = r.y;
   }
   if (p.pack_k) {
