@@ -514,8 +514,9 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_back_kernel(ChooseArgs 
   const size_t at = (size_t)t * a.k + j;
   int id = j < a.k ? a.ids[at] : -1;
   float dw = j < a.k ? a.w[at] * a.scale : 0.f;
-  float l = (uint32_t)id < (uint32_t)a.E ? a.logits[(size_t)t * a.E + id] : -INFINITY;
-  const bool chosen = l > -INFINITY;
+  const bool named = (uint32_t)id < (uint32_t)a.E;
+  float l = named ? a.logits[(size_t)t * a.E + id] : -INFINITY;
+  const bool chosen = l > -INFINITY && !(a.bias && !(a.bias[named ? id : 0] > -INFINITY));  // (an expert that is off has no part)
   if (!chosen) { id = -1; dw = 0.f; }
   float s[N], top = -INFINITY, total = 1.f;
   if (spread) {
