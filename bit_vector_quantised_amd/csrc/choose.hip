@@ -423,8 +423,9 @@ __global__ __launch_bounds__(CHOOSE_THREADS) void choose_kernel(ChooseArgs a) {
     }
     in = -max_of<L>(-in);
     out = max_of<L>(out);
-    // (both values are sums of two; nothing hangs on groups without experts)
-    if (out > -INFINITY && !(in - out > 2.f * near)) sure = false;
+    // (both values are sums of two, each rounded once more, by 2^-24 of at most twice the largest; nothing hangs on groups
+    // without experts)
+    if (out > -INFINITY && !(in - out > 2.f * near + ldexpf(most + b_most, -22))) sure = false;
   }
   // ---- whole numbers, 1 and more
   uint32_t key[N], tol = 0;

@@ -10,7 +10,7 @@ import dense_ref
 from bit_vector_quantised_amd.block import ExpertChoice
 
 from gpu_util import say
-from test_gpu_dense import gen, randn
+from test_gpu_dense import F32, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +38,30 @@ def test_gradient_at_experts_that_the_bias_turns_off(score, renorm, E, k):
     assert torch.equal(got, choice.backward(logits.cuda(), named.cuda(), dw.cuda()))
     assert not got[:, off.cuda()].any()
     dense_ref.check(got, *ref.choose_backward64(logits, bias, named, dw, score, renorm, 1.7), "dlogits")
+
+
+@pytest.mark.parametrize("E,groups", [(4, 2), (60, 5), (320, 5)])
+@pytest.mark.parametrize("steps", [(12740, 12740, 624, 624), (15990, 4635, 976, 13613), (522, 522, 12214, 12214)])
+def test_groups_whose_roundings_add_up(E, groups, steps):
+    """Two groups whose sums of two values differ by less than the roundings of fp32 move them: 64 bits order them.  With
+    biases of some 512 values are rounded to h = 2^-14 and sums to 2 h.  The scores lie half way between two steps
+    of h, up to a few steps of fp32 logits; where rounding moves one group's two up and the other's two down, their sums
+    become 3 h and 1 h (mod 4 h), which rounding to even moves to 4 h and 0: fp32 sees 4 h where hardly
+    anything is, and its scores' own errors decide which group that favours."""
+    say(f"groups whose roundings add up E={E} {steps}")
+    g = gen(E + steps[0])
+    T, h, size = 65536, 2.0 ** -14, E // groups
+    steps = torch.tensor(steps, dtype=torch.float64)
+    score = (steps + 0.5) * h
+    l = torch.log(score / (1 - score)).float().repeat(T, 1)
+    l = (l.view(torch.int32) + torch.randint(-5, 6, l.shape, generator=g, dtype=torch.int32)).view(F32)  # up to 5 steps away
+    b = (512 + (16384 + torch.tensor([0, 4001, 0, 4001]) - steps) * h).float()  # the values: 513 + (0 or 4001, and a half) h
+    at = torch.tensor([0, 1, size, size + 1])  # two experts in each of the first two groups
+    logits, bias = torch.full((T, E), -8.0), torch.zeros(E)
+    logits[:, at], bias[at] = l, b
+    value = torch.sigmoid(l.double()) + b.double()
+    one, two = value[:, 0] + value[:, 1], value[:, 2] + value[:, 3]
+    ids, _ = ExpertChoice(E, 2, "sigmoid", bias.cuda(), groups=groups, top_groups=1).forward(logits.cuda())
+    want = torch.where((two > one)[:, None], at[[3, 2]], at[[1, 0]])  # (the one of 4001 steps more comes first)
+    told = (one - two).abs() > 1e-11  # 64 bits: values of 513 are off by 2^-44 each, sums by 2^-43
+    assert told.sum() > 0.99 * T and torch.equal(ids.cpu().long()[told], want[told])
