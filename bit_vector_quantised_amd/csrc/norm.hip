@@ -154,7 +154,7 @@ __global__ __launch_bounds__(LPR ? 256 : 1024) void norm_back_kernel(NormBackArg
     }
     row_sums<LPR, 2>(sum, part);
     const float rho = 1.0f / sqrtf(sum[0] / (float)a.C + a.eps);
-    const float pull = rho * rho * (sum[1] / (float)a.C);
+    const float pull = rho * (rho * (sum[1] / (float)a.C));  // (rho^2 alone is infinite for eps below 2^-128 and zeros)
     if (!there) return;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {

@@ -7,7 +7,7 @@ import torch
 
 import block_ref as ref
 import dense_ref
-from bit_vector_quantised_amd.block import ExpertChoice
+from bit_vector_quantised_amd.block import ExpertChoice, RmsNorm
 
 from gpu_util import say
 from test_gpu_dense import F32, gen, randn
@@ -65,3 +65,22 @@ def test_groups_whose_roundings_add_up(E, groups, steps):
     want = torch.where((two > one)[:, None], at[[3, 2]], at[[1, 0]])  # (the one of 4001 steps more comes first)
     told = (one - two).abs() > 1e-11  # 64 bits: values of 513 are off by 2^-44 each, sums by 2^-43
     assert told.sum() > 0.99 * T and torch.equal(ids.cpu().long()[told], want[told])
+
+
+@pytest.mark.parametrize("C", [64, 500, 1024, 9000])
+@pytest.mark.parametrize("eps", [1e-6, 2.0 ** -126, 2.0 ** -129, 2.0 ** -140])
+def test_norm_of_rows_of_zeros_by_any_eps(C, eps):
+    """Rows of zeros (padding) have s^3 mean(t s) = 0, whatever eps: dx = t / sqrt(eps), dgain nothing."""
+    say(f"norm of zeros C={C} eps={eps}")
+    g = gen(C)
+    M = 5
+    s, gain, dy = torch.zeros(M, C), 1 + 0.3 * randn(g, C), randn(g, M, C) * 2.0 ** -20
+    s[1], s[3] = randn(g, C), 2.0 ** -64 * randn(g, C)
+    norm = RmsNorm(gain.cuda(), eps=eps, max_rows=M, backward=True)
+    assert not norm.forward(s.cuda())[[0, 2, 4]].any()
+    dx, dg = torch.empty(M, C, device="cuda"), torch.empty(C, device="cuda")
+    norm.backward(s.cuda(), dy.cuda(), dx=dx, dgain=dg)
+    want = ref.norm_backward64(s, gain, eps, dy, None, None, F32)
+    for row in (0, 1, 2, 4):
+        dense_ref.check(dx[row], want[0][row], want[1][row], f"dx of row {row}")
+    assert torch.isfinite(dx).all() and torch.isfinite(dg).all()
