@@ -24,9 +24,10 @@ __device__ __forceinline__ uint32_t top_bits8(const float* v) {
   }
   return top;
 }
-// Eight values in units of the scale, rounded to nearest even (v_cvt_pk_fp8_f32; none is above 448).
+// Eight values in units of the scale, rounded to nearest even (v_cvt_pk_fp8_f32; none is above 448).  Zeros stay zeros in a
+// block of NaN too: those behind the row's last column are zeros always.
 __device__ __forceinline__ u32x2_t to_e4m3(const float* v, uint32_t scale) {
-  const float inv = __builtin_bit_cast(float, (254u - scale) << 23);
+  const float inv = __builtin_bit_cast(float, (scale < 254u ? 254u - scale : 0u) << 23);
   int w[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {

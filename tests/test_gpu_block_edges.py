@@ -8,9 +8,10 @@ import torch
 import block_ref as ref
 import dense_ref
 from bit_vector_quantised_amd.block import ExpertChoice, RmsNorm
+from bit_vector_quantised_amd.dense import Rows8
 
 from gpu_util import say
-from test_gpu_dense import F32, gen, randn
+from test_gpu_dense import BF16, F32, gen, randn
 
 pytestmark = pytest.mark.gpu
 
@@ -84,3 +85,24 @@ def test_norm_of_rows_of_zeros_by_any_eps(C, eps):
     for row in (0, 1, 2, 4):
         dense_ref.check(dx[row], want[0][row], want[1][row], f"dx of row {row}")
     assert torch.isfinite(dx).all() and torch.isfinite(dg).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_columns_behind_the_last_are_zeros(dtype):
+    """Also where the row's last block holds an infinity or NaN, which makes its values NaN by the exponent alone; as pack
+    and norm write it."""
+    say(f"8 bits: columns behind the last, {dtype}")
+    g = gen(11)
+    for C in (1, 35, 100, 127):
+        x = randn(g, 5, C, dtype=dtype)
+        x[1, -1], x[2, -1], x[3, -1] = math.inf, -math.inf, math.nan
+        r, by_norm = Rows8(5, C), Rows8(5, C)
+        r.q.fill_(77)
+        by_norm.q.fill_(77)
+        r.pack(x.cuda())
+        RmsNorm(torch.ones(C, device="cuda"), max_rows=5).forward(x.cuda(), rows8=by_norm, dense=False)
+        for rows in (r, by_norm):
+            assert (rows.e[1:4, -1] == 255).all() and (rows.q[:, C:] == 0).all()
+            got = rows.unpack(out=torch.empty(5, C, dtype=dtype, device="cuda"))
+            last = (C - 1) // 32 * 32
+            assert got[1:4, last:].isnan().all() and torch.isfinite(got[[0, 4]]).all()
