@@ -51,8 +51,8 @@ int backward(const moe_vq_linear* L, const void* x, const moe_vq_rows8* x8, int 
   if (!dtype_ok(dy_dtype)) return MOE_VQ_EINVAL;
   if (!dx && !dw && !dbias) return MOE_VQ_OK;
   if (off16(x) || off16(z) || off16(dy) || off16(dx) || off16(dw) || off4(dbias)) return MOE_VQ_EINVAL;
-  if (x8 && (!x8->q || !x8->e || off16(x8->q))) return MOE_VQ_EINVAL;
-  if (z8 && (!z8->q || !z8->e || off16(z8->q))) return MOE_VQ_EINVAL;
+  for (const moe_vq_rows8* r : {x8, z8})  // (the buffers of no rows may be null)
+    if (r && ((n_rows > 0 && (!r->q || !r->e)) || off16(r->q))) return MOE_VQ_EINVAL;
   if (n_rows > 0 && (!dy || (dw && !x && !x8) || (L->act != MOE_VQ_ACT_NONE && !z && !z8))) return MOE_VQ_EINVAL;
   const LinearPlan p = linear_plan(L, n_rows, true, kept8);
   if ((st = check_linear_ws(p, ws, ws_bytes))) return st;

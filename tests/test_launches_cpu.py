@@ -54,3 +54,19 @@ def test_a_launch_that_fails_is_reported(tmp_path, calls):
         for n in range(len(kernels)):
             assert results[i + 1 + n][0] == _lib.EHIP, (n, [k[0] for k in kernels])
         i += 1 + len(kernels)
+
+
+def test_no_rows_in_8_bits(tmp_path):
+    """Gradients of no rows, whose buffers in 8 bits are empty (null): zeros, as those of plain tensors without rows."""
+    from bit_vector_quantised_amd import _lib
+    results = launches.run(tmp_path, r"""
+A, D, E, F, G = (i << 38 for i in range(1, 6))
+lin = ctypes.byref(_lib.LinearDesc(64, 48, 1, _lib.ACT_SWIGLU, _lib.BF16, 0.0, A, D))
+none = ctypes.byref(_lib.Rows8Desc(None, None))
+call(raw.moe_vq_linear_backward, lin, None, 0, None, None, None, _lib.BF16, None, E, F, G, 1 << 34, None)
+call(raw.moe_vq_linear_backward8, lin, None, none, 0, None, None, none, None, _lib.BF16, None, E, F, G, 1 << 34, None)
+call(raw.moe_vq_linear_backward8, lin, None, none, 1, None, None, none, A, _lib.BF16, None, E, F, G, 1 << 34, None)
+""")
+    (plain, kernels), (status, same), (refused, nothing) = results
+    assert plain == status == _lib.OK and kernels and same == kernels
+    assert refused == _lib.EINVAL and not nothing
