@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "dense.h"
+#include "dw_order.h"
 #include "rows8_device.h"
 
 namespace mvq {
@@ -52,6 +53,7 @@ struct GemmArgs {
   int kc;     // contraction length (FWD n_in, DX R; DW: the group's rows)
   int out_m, out_n;  // DW: rows and columns of dW; FWD, DX: out_n columns of the tile space
   int splits;
+  int parts_shift;  // DW: how the tiles lie over the XCDs
   float* part;  // splits > 1: fp32 partial sums [splits][rows][columns]
   // epilogue
   const float* bias;
@@ -292,17 +294,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs& g, int block, char* ld
   constexpr bool HALVES_AT_END = MODE != GEMM_DW && BM * BN >= 256 * 256;
   int grp = 0, im, in, split, r0, r1, m0, half = 0;
   if (MODE == GEMM_DW) {
-    // Every XCD takes an eighth of each group's tiles (neighbouring ones), as groups differ in their rows, by which a
-    // tile's work goes; which eighth, the longer ones first, turns with the group.  (Whole groups to an XCD: 16 uneven
-    // groups' 8192 rows, dw of 4096 x 7168 each 663 us, so 597; 16384 rows, 7168 x 2048 677 and 503.  XCDs that
-    // begin with different groups: 604, but 32 groups' 32768 rows 2210 instead of 2090.)
-    const int mt = (g.out_m + BM - 1) / BM, tiles = mt * nt, per = (tiles + 7) / 8;
-    const int x = block & 7, q = block >> 3, all = q / per;
-    split = all / g.G;
-    grp = all - split * g.G;
-    const int eighth = (x + grp) & 7, id = eighth * per + q - all * per;
-    if (id >= tiles) return;  // (the last eighths may be short)
-    band_order<4>(id, mt, nt, im, in);
+    const int mt = (g.out_m + BM - 1) / BM, tiles = mt * nt;
+    const DwPlace at = dw_place(block, tiles, g.G, g.parts_shift);
+    split = at.split;
+    grp = at.group;
+    if (split >= g.splits || at.tile >= tiles) return;
+    band_order<4>(at.tile, mt, nt, im, in);
     group_rows(g, grp, r0, r1);
     m0 = im * BM;
   } else {
@@ -957,7 +954,7 @@ long gemm_grid(const GemmArgs& g, int BM, int BN) {
   // (each group of rows adds at most one partial row tile)
   const long mt = MODE == GEMM_DW ? (long)div_up(g.out_m, BM) * g.G
                                   : (g.group_start ? (long)g.M / BM + (g.G < g.M ? g.G : g.M) : div_up(g.M, BM));
-  const long grid = MODE == GEMM_DW ? (nt * div_up(g.out_m, BM) + 7) / 8 * 8 * g.G * g.splits : nt * mt * g.splits;
+  const long grid = MODE == GEMM_DW ? dw_workgroups((int)nt * div_up(g.out_m, BM), (long)g.G * g.splits, g.parts_shift) : nt * mt * g.splits;
   const long more = grid > 0 && MODE != GEMM_DW && BM * BN >= 256 * 256 ? 8 * 17 : 0;  // (an XCD's last 16 tiles in halves)
   return grid + more;
 }
@@ -1234,6 +1231,7 @@ hipError_t launch_linear_backward(const LinearPlan& p, const LinearCall& c, hipS
   gw.out_m = p.R;
   gw.out = c.dw;
   gw.splits = p.dw.splits;
+  gw.parts_shift = dw_parts_shift(div_up(p.R, p.dw.tile) * div_up(p.K, p.dw.tile), (long)p.G * p.dw.splits, p.dw.tile);
   gw.part = at<float>(c.ws, p.dw_part);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
