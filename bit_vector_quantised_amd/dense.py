@@ -417,7 +417,7 @@ class DenseExperts:
         self.fc2.forward(self.h[:P], start, out=self.o[:P])
         out = self.rows.combine(self.o[:P], w, y if add else None, y)
         if keep:
-            self._kept = (x, self.w_kept[:x.shape[0]].copy_(w))  # (of x only the number of tokens is used)
+            self._kept = (x.shape[0], self.w_kept[:x.shape[0]].copy_(w))
         return out
 
     def backward(self, dy: torch.Tensor, dx: torch.Tensor, dw: torch.Tensor, dw1: torch.Tensor,
@@ -425,9 +425,9 @@ class DenseExperts:
         """Gradients of the last forward(keep=True): dx [T, H], dw [T, k], dw1 and dw2 (as w1 and w2)."""
         if self._kept is None:
             raise ValueError("the last forward kept nothing")
-        x, w = self._kept
+        _, w = self._kept
         self._kept = None
-        P = x.shape[0] * self.rows.top_k
+        P = w.shape[0] * self.rows.top_k
         start = self.rows.expert_start
         if self.kept8:
             self.rows.gather(dy, self.do[:P])

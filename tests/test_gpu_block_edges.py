@@ -1,6 +1,8 @@
 """Calls of the operators around the experts at their edges, each against a 64-bit plain form or against a call that it must
 equal to the bit."""
+import gc
 import math
+import weakref
 
 import pytest
 import torch
@@ -8,7 +10,7 @@ import torch
 import block_ref as ref
 import dense_ref
 from bit_vector_quantised_amd.block import ExpertChoice, RmsNorm
-from bit_vector_quantised_amd.dense import Rows8
+from bit_vector_quantised_amd.dense import DenseExperts, Rows8
 
 from gpu_util import say
 from test_gpu_dense import BF16, F32, gen, randn
@@ -106,3 +108,27 @@ def test_columns_behind_the_last_are_zeros(dtype):
             got = rows.unpack(out=torch.empty(5, C, dtype=dtype, device="cuda"))
             last = (C - 1) // 32 * 32
             assert got[1:4, last:].isnan().all() and torch.isfinite(got[[0, 4]]).all()
+
+
+def small_experts(g, T, k, H=64, I=48, E=4, kept8=True, **more):
+    w1, w2 = randn(g, E, 2 * I, H, dtype=BF16, scale=H ** -0.5).cuda(), randn(g, E, H, I, dtype=BF16, scale=I ** -0.5).cuda()
+    return DenseExperts(w1, w2, k, T, backward=True, kept8=kept8, **more)
+
+
+@pytest.mark.parametrize("kept8", [False, True])
+def test_a_kept_pass_holds_no_tensor_of_its_caller(kept8):
+    """What backward needs is kept in the step's own buffers: the caller's x, ids and w may be freed before it."""
+    say(f"kept pass, the caller's tensors kept8={kept8}")
+    g = gen(21)
+    T, k, H, E = 30, 2, 64, 4
+    step = small_experts(g, T, k, kept8=kept8)
+    inputs = [randn(g, T, H, dtype=BF16).cuda(), torch.randint(0, E, (T, k), generator=g).int().cuda(), torch.rand(T, k, generator=g).cuda()]
+    refs = [weakref.ref(t) for t in inputs]
+    step.forward(*inputs, keep=True)
+    del inputs
+    gc.collect()
+    assert [r() for r in refs] == [None] * 3
+    dy = randn(g, T, H, dtype=BF16).cuda()
+    dx, dw = torch.empty(T, H, dtype=BF16, device="cuda"), torch.empty(T, k, device="cuda")
+    step.backward(dy, dx, dw, torch.empty_like(step.fc1.w), torch.empty_like(step.fc2.w))
+    assert dx.any() and dw.any()
