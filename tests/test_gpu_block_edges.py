@@ -132,3 +132,22 @@ def test_a_kept_pass_holds_no_tensor_of_its_caller(kept8):
     dx, dw = torch.empty(T, H, dtype=BF16, device="cuda"), torch.empty(T, k, device="cuda")
     step.backward(dy, dx, dw, torch.empty_like(step.fc1.w), torch.empty_like(step.fc2.w))
     assert dx.any() and dw.any()
+
+
+def test_a_kept_pass_records_no_graph():
+    """Weights that require a gradient leave none in the step's buffers, pass after pass."""
+    say("kept pass, weights that require a gradient")
+    g = gen(22)
+    T, k, H, E = 9, 2, 64, 4
+    step = small_experts(g, T, k)
+    x, ids = randn(g, T, H, dtype=BF16).cuda(), torch.randint(0, E, (T, k), generator=g).int().cuda()
+    results = []
+    for leaf in (False, True, True):
+        w = torch.full((T, k), 0.5, device="cuda", requires_grad=leaf)
+        y = step.forward(x, ids, w, keep=True)
+        assert not step.w_kept.requires_grad and step.w_kept.grad_fn is None and not y.requires_grad
+        dx, dw = torch.empty_like(x), torch.empty(T, k, device="cuda")
+        step.backward(x, dx, dw, torch.empty_like(step.fc1.w), torch.empty_like(step.fc2.w))
+        results.append((y, dx, dw))
+    for got in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got, results[0]))
