@@ -436,6 +436,7 @@ class DenseExperts:
             self.rows.act_backward(self.z8, self.dh[:P], w, "swiglu", self.swiglu_limit, self.z[:P], self.h[:P], dw)
             self.fc2.backward(self.h[:P], self.do[:P], group_start=start, dw=dw2)
             self.rows.gather(self.x8, self.xs[:P])
+            self.fc1_back.w = self.fc1.w  # (it may have been replaced since)
             self.fc1_back.backward(self.xs[:P], self.z[:P], group_start=start, dx=self.do[:P], dw=dw1)
             self.rows.gather_backward(self.do[:P], dx)
             return

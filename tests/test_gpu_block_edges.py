@@ -151,3 +151,24 @@ def test_a_kept_pass_records_no_graph():
         results.append((y, dx, dw))
     for got in results[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got, results[0]))
+
+
+@pytest.mark.parametrize("kept8", [False, True])
+def test_weights_replaced_between_passes(kept8):
+    """A step whose weight tensors are replaced computes with the new ones, forward and back, as one made from them."""
+    say(f"weights replaced kept8={kept8}")
+    g = gen(23)
+    T, k, H, E = 20, 2, 64, 4
+    step, other = small_experts(g, T, k, kept8=kept8), small_experts(g, T, k, kept8=kept8)
+    x, ids, w = randn(g, T, H, dtype=BF16).cuda(), torch.randint(0, E, (T, k), generator=g).int().cuda(), torch.rand(T, k, generator=g).cuda()
+    dy = randn(g, T, H, dtype=BF16).cuda()
+    results = []
+    step.forward(x, ids, w, keep=True)
+    step.fc1.w, step.fc2.w = other.fc1.w.clone(), other.fc2.w.clone()
+    for one in (step, other):
+        y = one.forward(x, ids, w, keep=True)
+        grads = [torch.empty_like(t) for t in (x, w, one.fc1.w, one.fc2.w)]
+        one.backward(dy, *grads)
+        results.append([y, *grads])
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
