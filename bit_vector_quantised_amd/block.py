@@ -146,17 +146,18 @@ class Router(_OnDevice):
         self.w = self._new((max_tokens, top_k), torch.float32)
         self.dlogits = self._new((max_tokens, E), torch.float32) if backward else None
         self.n_tokens = None  # of the last forward
+        self._pass = None     # its mark, for a block that goes back through it
 
     def forward(self, x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
         """x [T, H] -> ids [T, k] (int32) and w [T, k] (fp32), valid until the next forward."""
         T = x.shape[0]
-        self.n_tokens = None
+        self.n_tokens = self._pass = None
         self._here()  # (the parts' calls use this object's buffers)
         if T > self.linear.max_rows:
             raise ValueError(f"{T} tokens, made for {self.linear.max_rows}")
         self.linear.forward(x, out=self.logits[:T])
         ids, w = self.choice.forward(self.logits[:T], self.ids[:T], self.w[:T])
-        self.n_tokens = T
+        self.n_tokens, self._pass = T, object()
         return ids, w
 
     def backward(self, x: Union[torch.Tensor, Rows8, None], dw: torch.Tensor, dx: Optional[torch.Tensor] = None,
@@ -176,7 +177,8 @@ class Router(_OnDevice):
 class MoeBlock(_OnDevice):
     """A layer's mixture of experts with the norm before it: s = x + residual, n = norm(s), ids and w = router(n), y =
     sum_i w_i E_i(n).  The next block adds y to s.  After a forward with keep=True, backward gives the gradients; what it
-    needs beside s is kept here, by experts made with kept8 in 8 bits, which the norm then writes.  work: another block of
+    needs beside s is kept here and in its router and experts (made with kept8 in 8 bits, which the norm then writes), so
+    that backward refuses if either has made another pass since, alone or in another block.  work: another block of
     the same sizes whose buffers this one uses (see DenseExperts; both of experts with kept8)."""
 
     def __init__(self, norm: RmsNorm, router: Router, experts: DenseExperts, work: Optional["MoeBlock"] = None):
@@ -218,7 +220,7 @@ class MoeBlock(_OnDevice):
         ids, w = self.router.forward(self.n[:T])
         y = self.experts.forward(self.n[:T], ids, w, y, keep=keep, x8_there=kept8)
         if keep:
-            self._kept = T
+            self._kept = T, self.router._pass, self.experts._kept[0]
         return y
 
     def backward(self, s: torch.Tensor, dy: torch.Tensor, ds: Optional[torch.Tensor], dx: torch.Tensor, dgain: torch.Tensor,
@@ -227,7 +229,9 @@ class MoeBlock(_OnDevice):
         is used): dx [T, H] (of x and of residual alike; it may be ds), dgain, drouter, dw1 and dw2."""
         if self._kept is None:
             raise ValueError("the last forward kept nothing")
-        T, self._kept = self._kept, None
+        (T, routed, kept), self._kept = self._kept, None
+        if self.router._pass is not routed or self.experts._kept is None or self.experts._kept[0] is not kept:
+            raise ValueError("the router or the experts have made another pass since")
         self._here()  # (the parts' calls use this object's buffers)
         self.experts.backward(dy, self.dn[:T], self.dw[:T], dw1, dw2)
         self.router.backward(self.experts.x8 if self.experts.kept8 else self.n[:T], self.dw[:T], self.dn2[:T], drouter)

@@ -417,7 +417,7 @@ class DenseExperts:
         self.fc2.forward(self.h[:P], start, out=self.o[:P])
         out = self.rows.combine(self.o[:P], w, y if add else None, y)
         if keep:
-            self._kept = (x.shape[0], self.w_kept[:x.shape[0]].copy_(w.detach()))
+            self._kept = (object(), self.w_kept[:x.shape[0]].copy_(w.detach()))  # (a mark of the pass, its weights)
         return out
 
     def backward(self, dy: torch.Tensor, dx: torch.Tensor, dw: torch.Tensor, dw1: torch.Tensor,

@@ -9,7 +9,7 @@ import torch
 
 import block_ref as ref
 import dense_ref
-from bit_vector_quantised_amd.block import ExpertChoice, RmsNorm
+from bit_vector_quantised_amd.block import ExpertChoice, MoeBlock, RmsNorm, Router
 from bit_vector_quantised_amd.dense import DenseExperts, Rows8
 
 from gpu_util import say
@@ -172,3 +172,43 @@ def test_weights_replaced_between_passes(kept8):
         results.append([y, *grads])
     for a, b in zip(*results):
         assert torch.equal(a, b)
+
+
+def small_block(g, T, k, H=64, E=4, kept8=True, router=None, step=None):
+    step = small_experts(g, T, k, H=H, E=E, kept8=kept8) if step is None else step
+    router = Router(randn(g, E, H, dtype=BF16).cuda(), k, T, backward=True) if router is None else router
+    return MoeBlock(RmsNorm((1 + 0.2 * randn(g, H)).cuda(), max_rows=T, backward=True), router, step)
+
+
+def block_gradients(b, s, dy):
+    out = [torch.empty_like(s), torch.empty_like(b.norm.gain), torch.empty_like(b.router.linear.w), torch.empty_like(b.experts.fc1.w),
+           torch.empty_like(b.experts.fc2.w)]
+    b.backward(s, dy, None, *out)
+    return out
+
+
+@pytest.mark.parametrize("kept8", [False, True])
+def test_a_block_whose_parts_went_on_refuses(kept8):
+    """A kept block goes back through its own pass only: not after its router or its experts have made another one, alone or
+    as parts of another block, of as many tokens."""
+    say(f"block whose parts went on kept8={kept8}")
+    g = gen(24)
+    T, k, H, E = 20, 2, 64, 4
+    b = small_block(g, T, k, kept8=kept8)
+    x, other, dy = (randn(g, T, H, dtype=BF16).cuda() for _ in range(3))
+    ids, w = torch.randint(0, E, (T, k), generator=g).int().cuda(), torch.rand(T, k, generator=g).cuda()
+    b.forward(x, keep=True)
+    want = block_gradients(b, x, dy)
+    same_router = small_block(g, T, k, kept8=kept8, router=b.router)
+    same_experts = small_block(g, T, k, kept8=kept8, step=b.experts)
+    for went_on in (lambda: b.router.forward(other), lambda: b.experts.forward(other, ids, w), lambda: b.experts.forward(other, ids, w, keep=True),
+                    lambda: same_router.forward(other, keep=True), lambda: same_experts.forward(other, keep=True),
+                    lambda: same_router.forward(other), lambda: same_experts.forward(other)):
+        b.forward(x, keep=True)
+        went_on()
+        for _ in range(2):  # (nor later)
+            with pytest.raises(ValueError, match="another pass|kept nothing"):
+                block_gradients(b, x, dy)
+    b.forward(x, keep=True)
+    for a, c in zip(block_gradients(b, x, dy), want):
+        assert torch.equal(a, c)
