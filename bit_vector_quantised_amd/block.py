@@ -216,6 +216,8 @@ class MoeBlock(_OnDevice):
             raise ValueError("made without backward")
         self._here()  # (the parts' calls use this object's buffers)
         kept8 = keep and self.experts.kept8
+        if kept8:
+            self.experts._kept = None  # (the norm writes x8, even if a call after it is refused)
         self.norm.forward(x, residual, s, self.n[:T], self.experts.x8 if kept8 else None)
         ids, w = self.router.forward(self.n[:T])
         y = self.experts.forward(self.n[:T], ids, w, y, keep=keep, x8_there=kept8)

@@ -212,3 +212,21 @@ def test_a_block_whose_parts_went_on_refuses(kept8):
     b.forward(x, keep=True)
     for a, c in zip(block_gradients(b, x, dy), want):
         assert torch.equal(a, c)
+
+
+def test_a_refused_block_leaves_no_mixed_pass():
+    """The norm writes the experts' rows in 8 bits first: if the router then refuses, a pass that the experts kept before is
+    gone."""
+    say("refused block")
+    g = gen(25)
+    T, k, H, E = 20, 2, 64, 4
+    b = small_block(g, T, k)
+    x, other, dy = (randn(g, T, H, dtype=BF16).cuda() for _ in range(3))
+    ids, w = torch.randint(0, E, (T, k), generator=g).int().cuda(), torch.rand(T, k, generator=g).cuda()
+    b.experts.forward(x, ids, w, keep=True)
+    weights, b.router.linear.w = b.router.linear.w, b.router.linear.w.float()  # (of another type: refused)
+    with pytest.raises(ValueError):
+        b.forward(other, keep=True)
+    b.router.linear.w = weights
+    with pytest.raises(ValueError, match="kept nothing"):
+        b.experts.backward(dy, torch.empty_like(x), torch.empty_like(w), torch.empty_like(b.experts.fc1.w), torch.empty_like(b.experts.fc2.w))
