@@ -61,8 +61,10 @@ int backward(const moe_vq_linear* L, const void* x, const moe_vq_rows8* x8, int 
   const Span dx_s{dx, (size_t)p.M * p.K * p.size}, dw_s{dw, in.w.n}, db_s{dbias, in.bias.n}, ws_s{ws, p.total};
   const Span dy_s{dy, (size_t)p.M * p.N * size_of(dy_dtype)}, z_s{act ? z : nullptr, (size_t)p.M * p.R * p.size};
   const Span x_s{dw ? x : nullptr, dx_s.n}, w_s{dx ? L->w : nullptr, in.w.n};  // (each read for one product only)
-  // In order: dz and its column sums from dy and z, then dx from w, then dw from x.  So dx and dw may lie over
-  // z, and over dy where dz is another tensor, and dw over w; without an activation both products read dy.
+  // In order: dz and its column sums' parts from dy and z; then dx from dz and w, dw from dz and x and the sum of the bias
+  // parts, which may run side by side in one launch.  So dx and dw may lie over z, and over dy where dz is another
+  // tensor (without an activation both products read dy), but neither over what the other reads or writes.  dw may
+  // lie over w all the same: launch_linear_backward then makes dx in a launch of its own before dw.
   if (clash({dx_s, dw_s, db_s, ws_s}, {x_s, in.table}) || clash({db_s, ws_s}, {dy_s, z_s, w_s}) || overlap(dx_s, w_s) ||
       (!act && (overlap(dx_s, dy_s) || overlap(dw_s, dy_s))))
     return MOE_VQ_EINVAL;

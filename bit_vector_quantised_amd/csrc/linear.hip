@@ -1169,7 +1169,8 @@ hipError_t launch_linear_forward(const LinearPlan& p, const LinearCall& c, hipSt
                                        : launch_gemm<GEMM_FWD>(p, g, p.fwd.tile, st);
 }
 
-// Whether one launch makes both products: of small tiles, dw not over the weights that dx reads.
+// Whether one launch makes both products: of small tiles, dw not over the weights that dx reads (the calls allow that;
+// every other overlap of the two is refused before).
 static bool gradients_together(const LinearPlan& p, const LinearCall& c, const GemmArgs& dx, const GemmArgs& dw) {
   if (!c.dx || !c.dw || p.M == 0 || p.dx.tile > 128 || p.dw.tile > 128) return false;
   const size_t bytes = (size_t)p.G * p.R * p.K * p.size;

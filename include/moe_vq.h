@@ -486,7 +486,7 @@ int moe_vq_linear_backward(const moe_vq_linear *lin, const void *x, int n_rows, 
 /* Rows in 8 bits.  q [n_rows][pitch]: e4m3 values, pitch = moe_vq_rows8_pitch(n_cols), n_cols rounded up to
  * a multiple of 32 (the columns behind the last are zeros); e [n_rows][pitch/32]: E8M0 exponents
  * of the scales, one for each block of 32 columns.  A value is q * 2^(e-127), NaN where e is 255, and
- * exact in bf16 and fp32 where e is 17..247.  q 16-byte aligned. */
+ * exact in bf16 and fp32 where e is 17..247 and its magnitude below 2^128.  q 16-byte aligned. */
 typedef struct moe_vq_rows8 {
   uint8_t *q;
   uint8_t *e;
@@ -497,7 +497,8 @@ size_t moe_vq_rows8_pitch(int n_cols);
 
 /* x [n_rows][n_cols] in dtype to rows in 8 bits: a block's scale is the smallest power of two, 2^-110 or
  * more, that brings its largest magnitude to 448 or less, and each value is rounded to the nearest
- * e4m3 value (ties to even); a block that holds an infinity or NaN gets e = 255.  group_start
+ * e4m3 value (ties to even), magnitudes of 248 * 2^120 (3.3e38) and more so to 2^128, which is an infinity in
+ * fp32 and bf16; a block that holds an infinity or NaN gets e = 255.  group_start
  * [n_groups + 1] (device) or NULL: rows outside group_start[0] .. group_start[n_groups]-1 are neither read nor
  * written.  x 16-byte aligned; n_rows * pitch <= 2^34. */
 int moe_vq_rows8_pack(const void *x, int dtype, int n_rows, int n_cols, const int32_t *group_start, int n_groups,
