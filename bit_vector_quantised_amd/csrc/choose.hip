@@ -151,7 +151,7 @@ __device__ __forceinline__ void order_two(uint32_t* k) {  // the larger first
   k[I] = x > y ? x : y;
   k[J] = x > y ? y : x;
 }
-// N words, the largest first (a merge exchange network over powers of two).
+// N words, the largest first (Batcher's merge exchange network over powers of two).
 template <int N>
 __device__ __forceinline__ void order_all(uint32_t* k) {
   static_for<0, log2_of(N)>([&](auto pp) {
@@ -168,7 +168,8 @@ __device__ __forceinline__ void order_all(uint32_t* k) {
 
 // ---- A token by the whole wave in 64 bits: experts N lane .. N lane + N - 1 in a lane.  Hardly any token comes here, but
 // a wave that does is the last of its launch (of 16384 tokens among 256 experts some 40 do; 5 us with an entry's exponential
-// after another's and groups by a scan of LDS, this way 4).
+// after another's and groups by a scan of LDS, this way 4).  Ties all come: 16384 tokens by softmax 10 us, from bf16 logits 21,
+// with all logits equal 26; sigmoid with biases and groups 15, with one bias of -1e9 41.
 
 template <int CTRL>
 __device__ __forceinline__ double dpp_f64(double v) {

@@ -9,8 +9,8 @@ namespace mvq {
 //     XCD end far apart (16 uneven groups' 8192 rows, dw of 4096 x 7168 each, 1340 us, so 550; 16384 rows, 2560 x 2560 616,
 //     248; in quarters 292);
 //   otherwise parts of about a quarter of what an XCD holds at once, as long as every XCD has one (even groups, 32 of
-//     512 x 512: 16.5 us whole, 21.3 in eighths, 16.6 so; 16 of 1024 x 1024 38, 43 and 40; 64 of 1024 x 512 44, 53 and 45;
-//     one group in 4 to 16 splits, 1024 x 512 to 1024 x 1024, 3 to 7 % under eighths).
+//     512 x 512: 16.5 us whole, 21.3 in eighths, 16.6 so; 16 of 1024 x 1024 41, 43 and 40; 64 of 1024 x 512 44, 53 and 45;
+//     one group, 8192 rows of 1024 -> 512 28.6, 29.4, 27.4).
 // Parts follow each other over the XCDs, one XCD further with every eight, so that those of a few sets use all of them.
 constexpr int dw_parts_shift(int tiles, long sets, int side) {
   const int quarter = side >= 256 ? 8 : 16;

@@ -882,8 +882,8 @@ __global__ __launch_bounds__(256) void bias_sum_kernel(BiasSum b) {
 
 // Small gradients, whose products leave CUs idle: dx, dw and the sum of the bias parts side by side in one launch, n_dx
 // workgroups from x0 on, n_dw from w0 on (all multiples of 8, for the order of the XCDs) and the rest.  With dz, one after the other and
-// side by side: 515 rows of 1000 -> 333 in fp32 33 us, so 25; bf16 64 rows of 512 -> 512 18 and 13, 512 of 2048 -> 2048
-// 43 and 29, 2048 of 2048 -> 2048 82 and 53.  Nothing of some 30 sizes takes longer.
+// side by side: 515 rows of 1000 -> 333 in fp32 32 us, so 24; bf16 64 rows of 512 -> 512 17 and 12, 512 of 2048 -> 2048
+// 43 and 29, 2048 of 2048 -> 2048 85 and 50.  Nothing of some 30 sizes takes longer.
 constexpr int stages_of(int side) { return side == 64 ? 4 : 2; }
 
 template <typename E, int DX, int DW>
@@ -900,7 +900,7 @@ __global__ __launch_bounds__(256) void gradients_kernel(GemmArgs dx, GemmArgs dw
 using Cut = LinearPlan::Cut;
 constexpr int CUS = 256;
 // Products of more workgroups in all are made one after the other: the ends of the two count ever less (fp32 at 4096^3,
-// 2048 workgroups, 1965 us, side by side 1971; 4096 x 2048 x 2048 555 and 549).
+// 2048 workgroups, 1967 us, side by side 1958; 4096 x 2048 x 2048 558 and 547).
 constexpr long GRADIENTS_TOGETHER = 16 * CUS;
 
 // A kind of tile: its side, how many workgroups of it a CU holds, and what a workgroup takes (microseconds,
